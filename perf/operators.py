@@ -107,7 +107,8 @@ def _gen(seed):
 
 def _e4m3(W):
     """(codes, scale) of one expert matrix: scale = amax / 448, nearest even."""
-    s = W.float().abs().amax() / 448.0
+    amax = W.float().abs().amax()
+    s = amax / torch.full_like(amax, 448.0)      # by a Python number it is not the rounded quotient
     return (W.float() / s).clamp_(-448.0, 448.0).to(torch.float8_e4m3fn), s
 
 
