@@ -313,6 +313,49 @@ MOE_API moe_status moe_forward(const moe_forward_args* args, void* ws, size_t ws
                        moe_stream_t stream);
 
 /*
+ * The whole layer for a few tokens (T <= 16, T * k <= 128) in one kernel, plus
+ * an optional residual:
+ *   out[t] = residual[t] + sum_j w(t, j) * y(t, j)
+ * For decode steps: moe_forward's chain of kernels has a fixed cost that
+ * outweighs the stream of a few small experts' weights.  Same routing (ids and
+ * w bit for bit), same packed weights and scales.  It differs in precision
+ * only: h enters the down product with 16 bits of mantissa instead of bf16's
+ * 8, and for MOE_FP8_E4M3 the activations stay bf16 (moe_forward quantises
+ * them); every sum is fp32 in a fixed order, out is rounded once.
+ *   x, out    device bf16 [T,H]; logits device f32 [T,E]
+ *   residual  device bf16 [T,H] or NULL; may be out itself
+ *   ids, w    optional device outputs [T,k]
+ *   status    optional device status word (NULL: the first int32 of ws)
+ *   ws        moe_decode_workspace_size bytes, made ready once by
+ *             moe_decode_workspace_init before its first call; every call
+ *             leaves it ready for the next, of any T, k or layer whose size
+ *             fits.  Calls that may run at the same time need workspaces of
+ *             their own.  A workspace that was not initialised is reported as
+ *             MOE_ERR_DEVICE in the status word (out is not written).
+ * The kernel is launched cooperatively: its blocks (one per SM) exchange
+ * partial sums, with bounded waits (MOE_ERR_TIMEOUT in the status word).
+ * Errors: as for moe_forward; T > 16 or T * k > 128 -> MOE_ERR_UNSUPPORTED.
+ */
+typedef struct {
+    moe_dtype dtype;
+    int T, k, E, H, I;
+    const void* x;
+    const float* logits;
+    const void* packed;
+    const float* scales;
+    const void* residual;
+    void* out;
+    int32_t* ids;
+    float* w;
+    int32_t* status;
+} moe_decode_args;
+
+MOE_API size_t moe_decode_workspace_size(moe_dtype dtype, int T, int k, int E, int H, int I);
+MOE_API moe_status moe_decode_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream);
+MOE_API moe_status moe_decode_forward(const moe_decode_args* args, void* ws, size_t ws_bytes,
+                                      moe_stream_t stream);
+
+/*
  * Reads a device status word: synchronises the stream, then returns
  * MOE_OK or the code the device recorded (MOE_ERR_TIMEOUT, MOE_ERR_DEVICE).
  * Errors: MOE_ERR_INVALID_ARG for NULL, MOE_ERR_CUDA if the copy fails.

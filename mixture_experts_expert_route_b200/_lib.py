@@ -7,6 +7,7 @@ raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -55,6 +56,12 @@ class ForwardArgs(ctypes.Structure):
                 ("lora", ctypes.POINTER(LoraArgs))]
 
 
+class DecodeArgs(ctypes.Structure):
+    _fields_ = [("dtype", I32), ("T", I32), ("k", I32), ("E", I32), ("H", I32), ("I", I32),
+                ("x", P), ("logits", P), ("packed", P), ("scales", P), ("residual", P),
+                ("out", P), ("ids", P), ("w", P), ("status", P)]
+
+
 class SplitCosts(ctypes.Structure):
     _fields_ = [("cpu_us", ctypes.c_double), ("cpu_us_per_token", ctypes.c_double),
                 ("xfer_us", ctypes.c_double), ("gpu_us", ctypes.c_double),
@@ -91,6 +98,9 @@ _SIGS = {
     "moe_combine": ([P, P, I32, I32, I32, P, P], I32),
     "moe_forward_workspace_size": ([I32, I32, I32, I32, I32, I32, I32], SZ),
     "moe_forward": ([ctypes.POINTER(ForwardArgs), P, SZ, P], I32),
+    "moe_decode_workspace_size": ([I32, I32, I32, I32, I32, I32], SZ),
+    "moe_decode_workspace_init": ([P, SZ, P], I32),
+    "moe_decode_forward": ([ctypes.POINTER(DecodeArgs), P, SZ, P], I32),
     "moe_check_status": ([P, P], I32),
     "moe_selftest_wait_timeout": ([P, I32, P], I32),
     # CPU/GPU split (include/moe_split.h)
@@ -318,6 +328,88 @@ def forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int, out=N
     return out
 
 
+DECODE_MAX_T, DECODE_MAX_ASSIGN = 16, 128     # tokens, T * k
+
+
+def _on_device(dev: torch.device, stream=None):
+    """Makes the tensors' device the current one, and the given stream (if any) torch's
+    current stream, so that buffers made inside belong to it."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("the stream belongs to another device than the tensors")
+        return torch.cuda.stream(stream)
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
+def _take(t, name, shape, dtype, dev):
+    """Checks an argument tensor of the decode and linear entry points."""
+    if t is None:
+        return None
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t
+
+
+def decode_workspace(dtype: int, T: int, k: int, E: int, H: int, I: int, device,
+                     stream=None) -> torch.Tensor:
+    """A workspace of decode_forward, initialised on the stream."""
+    n = lib().moe_decode_workspace_size(dtype, T, k, E, H, I)
+    if n == 0:
+        raise MoEError(2, "moe_decode_workspace_size")
+    with _on_device(torch.device(device), stream):
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        _check(lib().moe_decode_workspace_init(ws.data_ptr(), n, _stream(stream)),
+               "moe_decode_workspace_init")
+    return ws
+
+
+def decode_forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int,
+                   residual=None, out=None, ids=None, w=None, status=None, ws=None,
+                   stream=None):
+    """The whole layer for T <= 16 tokens (T * k <= 128) in one kernel:
+    out = residual + sum_j w_j * FFN_{id_j}(x).  ``ws`` comes from decode_workspace
+    and is reused from call to call (None: a new one for this call)."""
+    if x.dim() != 2:
+        raise ValueError("x: expected [T, H]")
+    T, H = x.shape
+    dev = x.device
+    if not x.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    bf16, f32 = torch.bfloat16, torch.float32
+    _take(x, "x", (T, H), bf16, dev)
+    _take(logits, "logits", (T, E), f32, dev)
+    _take(residual, "residual", (T, H), bf16, dev)
+    _take(out, "out", (T, H), bf16, dev)
+    _take(ids, "ids", (T, k), torch.int32, dev)
+    _take(w, "w", (T, k), f32, dev)
+    _take(scales, "scales", (E, 3), f32, dev)
+    if packed.device != dev or (status is not None and status.device != dev):
+        raise ValueError(f"packed and status: expected on {dev}")
+    if packed.numel() < lib().moe_packed_weights_size(dtype, E, H, I):
+        raise ValueError("packed: smaller than these sizes need")
+    with _on_device(dev, stream):
+        out = torch.empty((T, H), dtype=bf16, device=dev) if out is None else out
+        if ws is None and T > 0:
+            ws = decode_workspace(dtype, T, k, E, H, I, dev)
+        elif ws is not None and ws.device != dev:
+            raise ValueError(f"ws: on {ws.device}, expected {dev}")
+        a = DecodeArgs(dtype, T, k, E, H, I, x.data_ptr(), logits.data_ptr(),
+                       packed.data_ptr(), _ptr(scales), _ptr(residual), out.data_ptr(),
+                       _ptr(ids), _ptr(w), _ptr(status))
+        _check(lib().moe_decode_forward(ctypes.byref(a), _ptr(ws),
+                                        0 if ws is None else ws.numel(), _stream(stream)),
+               "moe_decode_forward")
+    return out
+
+
 def check_status(status: torch.Tensor, stream=None) -> int:
     return lib().moe_check_status(_ptr(status), _stream(stream))
 
@@ -343,6 +435,7 @@ class MoELayer:
         self.device = Wg.device
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._ws = {}
+        self._decode_ws = {}
 
     def workspace(self, T: int) -> torch.Tensor:
         if T not in self._ws:
@@ -357,6 +450,32 @@ class MoELayer:
                        self.k, out=out, status=self.status, ws=self.workspace(T),
                        block_m=self.block_m, max_ctas=self.max_ctas, events=events,
                        combine=self.combine, stream=stream)
+
+    def decode_workspace(self, T: int, stream=None) -> torch.Tensor:
+        """The workspace of decode calls on a stream (one per stream: calls on
+        different streams may overlap).  A call captured into a graph gets one of
+        its own, whose initialisation is captured with it: the graph may be
+        replayed on any stream, and outlive the cache."""
+        if torch.cuda.is_current_stream_capturing():
+            return decode_workspace(self.dtype, T, self.k, self.E, self.H, self.I,
+                                    self.device, stream)
+        key = _stream(stream)
+        n = lib().moe_decode_workspace_size(self.dtype, T, self.k, self.E, self.H, self.I)
+        ws = self._decode_ws.get(key)
+        if ws is None or ws.numel() < n:
+            ws = decode_workspace(self.dtype, T, self.k, self.E, self.H, self.I, self.device,
+                                  stream)
+            self._decode_ws[key] = ws
+        return ws
+
+    def decode(self, x, logits, residual=None, out=None, ids=None, w=None, stream=None):
+        """The layer for a few tokens in one kernel (see decode_forward)."""
+        T = x.shape[0]
+        with _on_device(self.device, stream):
+            ws = self.decode_workspace(T, stream) if T > 0 else None
+            return decode_forward(self.dtype, x, logits, self.packed, self.scales, self.E,
+                                  self.I, self.k, residual=residual, out=out, ids=ids, w=w,
+                                  status=self.status, ws=ws, stream=stream)
 
     def check(self) -> int:
         return check_status(self.status)

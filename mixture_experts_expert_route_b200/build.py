@@ -18,11 +18,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["route_permute.cu", "elementwise.cu", "grouped_gemm.cu", "moe_api.cu", "noalloc.cu",
-           "split.cu"]
+           "split.cu", "decode.cu"]
 # host code of the CPU/GPU split (g++: the AVX512_BF16 kernel selects its
 # instruction set per function and checks the CPU at run time)
 HOST_SOURCES = ["host_ffn.cpp"]
-HEADERS = ["common.cuh", "kernels.h"]
+HEADERS = ["common.cuh", "kernels.h", "topk.cuh"]
 LIB = os.path.join(HERE, "libmoe_b200.so")
 LIB_DEBUG = os.path.join(HERE, "libmoe_b200_debug.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

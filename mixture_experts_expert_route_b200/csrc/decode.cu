@@ -1,0 +1,749 @@
+// decode.cu -- the whole MoE layer for a few tokens (T <= 16) in one kernel:
+// routing, the experts' gate/up and down products, the weighted combine and
+// the residual.
+//
+//   ids, w  = top-k of the token's logits, softmax over the selected ones
+//   h       = SiLU(x W_g[e]) * (x W_u[e])
+//   out[t]  = residual[t] + sum_j w(t, j) * (h W_d[e])
+//
+// What bounds it is the stream of the active experts' packed weights, each
+// read once; everything around the stream is latency.  One cooperative grid,
+// one CTA per SM, runs the layer in three steps with two grid barriers:
+//
+//   1 every CTA routes the T tokens itself (the logits are a few KB), then the
+//     gate/up tiles of all active experts, in (expert, row tile, k-block)
+//     order, are cut into equal contiguous ranges, one per CTA.  A range ends
+//     inside a row tile, so each CTA writes fp32 partial sums.
+//   2 the down tiles in (expert, k-block, row tile) order are cut the same way.
+//     A CTA then needs only the few k-blocks of h that its range covers: it
+//     sums their partials, applies SiLU * up once, and keeps h in shared
+//     memory.  (With the row tile outermost every CTA would need all of h.)
+//     It writes fp32 partial sums of the output rows.
+//   3 the partial sums of every output are added in a fixed order, with the
+//     routing weights, over all CTAs, the residual added and rounded once.
+//
+// The weights arrive as 16 KB tiles (the packed layout of the grouped GEMMs)
+// through a ring of bulk copies that one thread keeps full across the
+// barriers: while the CTAs exchange partial sums the first down tiles land.
+// The products are m16n8k16 warp MMAs, weight rows in the M slot, tokens in N:
+// at 1 to 16 tokens the tensor work is a few percent of the stream's time, and
+// the register path lets e4m3 weights be widened to bf16 exactly (the
+// activations stay bf16; nothing is quantised) and h enter as the sum of two
+// bf16 values (16 bits of mantissa), so the only coarse rounding is out's.
+//
+// All sums are in a fixed order: results do not depend on timing.
+#include <cstdint>
+#include <mutex>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "topk.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kConsumerWarps = 8;                 // 16 weight rows of a tile each
+constexpr int kConsumers = kConsumerWarps * 32;
+constexpr int kThreads = kConsumers + 32;         // and one producer warp
+constexpr int kMaxSlots = 12;
+constexpr int kSmemBytes = 227 * 1024;
+constexpr uint32_t kMagic = 0x4d6f4465u;
+
+// h columns held at a time: 512 (8 k-blocks of bf16 tiles, 4 of e4m3 tiles)
+template <bool FP8> __host__ __device__ constexpr int tile_k() { return FP8 ? 128 : 64; }
+template <bool FP8> __host__ __device__ constexpr int chunk_kb() { return FP8 ? 4 : 8; }
+// bytes of one token's row of an x slice, and of a k-block of h (hi | lo), each
+// plus 16 so that two rows start an odd number of 16-byte banks apart
+template <bool FP8> __host__ __device__ constexpr int x_row_bytes() { return tile_k<FP8>() * 2 + 16; }
+template <bool FP8> __host__ __device__ constexpr int h_row_bytes() { return tile_k<FP8>() * 4 + 16; }
+template <bool FP8, int NB> __host__ __device__ constexpr int slot_bytes() {
+    return kTileBytes + NB * 8 * x_row_bytes<FP8>();
+}
+template <bool FP8, int NB> __host__ __device__ constexpr int h_bytes() {
+    return chunk_kb<FP8>() * NB * 8 * h_row_bytes<FP8>();
+}
+
+// Workspace header, zeroed but for the magic by moe_decode_workspace_init.
+// The arrival counters only grow, by one per CTA and launch, so each launch
+// finds them at a multiple of the grid and no launch has to reset them.
+struct Header {
+    int32_t status;
+    uint32_t magic;
+    uint64_t pad0[7];
+    uint64_t arrive[2][8];      // one 64-byte line per barrier
+};
+
+struct Args {
+    int T, k, E, H, I;
+    int mt_gu, kb_gu, mt_dn, kb_dn;
+    const uint8_t* w_gu;
+    const uint8_t* w_dn;
+    const float* scales;         // [E][3], e4m3
+    const __nv_bfloat16* x;
+    const float* logits;
+    const __nv_bfloat16* residual;
+    __nv_bfloat16* out;
+    int32_t* ids;
+    float* w;
+    int32_t* status;
+    Header* hdr;
+    float* p1;                   // gate/up partial columns of 128 rows
+    float* p2;                   // down partial columns of 128 rows
+    int slots;
+};
+
+struct Shared {
+    uint64_t full[kMaxSlots];
+    uint64_t empty[kMaxSlots];
+    int abort;
+    int n_active;
+    int ids[kDecodeMaxAssign];          // [T][k]
+    float w[kDecodeMaxAssign];
+    uint32_t mask[kMaxExperts];         // tokens that chose an expert
+    int rank[kMaxExperts];              // index among the active experts
+    int scan[kConsumerWarps];
+    int expert[kDecodeMaxAssign];       // active experts, ascending
+    int base[kDecodeMaxAssign + 1];     // first column of an active expert
+    int tok[kDecodeMaxAssign];          // column -> token
+    int start1[kMaxCtas + 1];           // first gate/up tile of each CTA
+    int start2[kMaxCtas + 1];           // first down tile of each CTA
+    float red[kConsumers];
+};
+
+__device__ __forceinline__ void consumer_sync() {
+    asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(const uint8_t* p) {
+    return *reinterpret_cast<const uint4*>(p);
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two e4m3 codes (the low 16 bits) as two bf16 values: exact, NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t v) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// The CTA whose range of tiles holds tile X.
+__device__ __forceinline__ int owner(const int* start, int G, int X, float tiles_per_cta_inv) {
+    int c = static_cast<int>(static_cast<float>(X) * tiles_per_cta_inv);
+    c = c < 0 ? 0 : (c > G - 1 ? G - 1 : c);
+    while (start[c] > X) --c;
+    while (start[c + 1] <= X) ++c;
+    return c;
+}
+
+__device__ __forceinline__ void fault(Shared& s, int32_t* status) {
+    report(status, MOE_ERR_TIMEOUT);
+    *reinterpret_cast<volatile int*>(&s.abort) = 1;
+}
+
+// Arrive of this CTA at a grid barrier, and the bounded wait for the others.
+// Called by one thread, between two CTA barriers of the consumers.
+__device__ __forceinline__ bool grid_barrier(uint64_t* counter, int G) {
+    __threadfence();
+    const unsigned long long old =
+        atomicAdd(reinterpret_cast<unsigned long long*>(counter), 1ull);
+    const unsigned long long target = (old / G + 1) * G;
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        unsigned long long v;
+        asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(counter) : "memory");
+        if (v >= target) break;
+        if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+    }
+    __threadfence();
+    return true;
+}
+
+// One tile's products: acc += W[16 rows of this warp] x B[NB * 8 tokens].
+// The K order inside a 128-byte row is permuted the same way for both
+// operands: lane (g, t) takes 16-byte pieces 2t and 2t+1 of its rows, whose
+// swizzled places are conflict-free for a quarter warp.  `b` points at this
+// lane's column g; block n of 8 columns is at +8 rows.
+template <bool FP8, int NB>
+__device__ __forceinline__ void load_a(uint4 (&a)[4], const uint8_t* tile, int warp, int g, int t) {
+    const uint8_t* r = tile + (16 * warp + g) * kTileRowBytes;
+    const int p0 = ((2 * t) ^ g) * 16, p1 = ((2 * t + 1) ^ g) * 16;
+    a[0] = lds16(r + p0);
+    a[1] = lds16(r + p1);
+    a[2] = lds16(r + 8 * kTileRowBytes + p0);
+    a[3] = lds16(r + 8 * kTileRowBytes + p1);
+}
+
+template <bool FP8, int NB>
+__device__ __forceinline__ void tile_mma(float (&acc)[NB][4], const uint4 (&a)[4],
+                                         const uint8_t* b, int row_bytes, int t, bool half_row,
+                                         int nb) {
+    if constexpr (!FP8) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            if (n < nb) {
+                const uint4 b0 = lds16(b + n * 8 * row_bytes + 32 * t);
+                const uint4 b1 = lds16(b + n * 8 * row_bytes + 32 * t + 16);
+                mma_bf16(acc[n], a[0].x, a[2].x, a[0].y, a[2].y, b0.x, b0.y);
+                mma_bf16(acc[n], a[0].z, a[2].z, a[0].w, a[2].w, b0.z, b0.w);
+                mma_bf16(acc[n], a[1].x, a[3].x, a[1].y, a[3].y, b1.x, b1.y);
+                mma_bf16(acc[n], a[1].z, a[3].z, a[1].w, a[3].w, b1.z, b1.w);
+            }
+        }
+    } else {
+        // 16 codes per piece: word q of a piece meets 8 bytes of b
+        const uint32_t lo[8] = {a[0].x, a[0].y, a[0].z, a[0].w, a[1].x, a[1].y, a[1].z, a[1].w};
+        const uint32_t hi[8] = {a[2].x, a[2].y, a[2].z, a[2].w, a[3].x, a[3].y, a[3].z, a[3].w};
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            uint32_t f[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                f[4 * q + 0] = e4m3x2_to_bf16x2(lo[2 * p + q] & 0xffffu);
+                f[4 * q + 1] = e4m3x2_to_bf16x2(hi[2 * p + q] & 0xffffu);
+                f[4 * q + 2] = e4m3x2_to_bf16x2(lo[2 * p + q] >> 16);
+                f[4 * q + 3] = e4m3x2_to_bf16x2(hi[2 * p + q] >> 16);
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                if (n < nb) {
+                    uint4 bv = lds16(b + n * 8 * row_bytes + 64 * t + 16 * p);
+                    // the last k-block may hold 64 of its 128 columns: the
+                    // weights are zero there, the activations not written
+                    if (half_row && t >= 2) bv = make_uint4(0, 0, 0, 0);
+                    mma_bf16(acc[n], f[0], f[1], f[2], f[3], bv.x, bv.y);
+                    mma_bf16(acc[n], f[4], f[5], f[6], f[7], bv.z, bv.w);
+                }
+            }
+        }
+    }
+}
+
+template <int EPL>
+__device__ __forceinline__ void route_tokens(const Args& g, Shared& s, int warp) {
+    for (int t = warp; t < g.T; t += kThreads / 32)
+        warp_topk<EPL>(g.logits + static_cast<long>(t) * g.E, g.E, g.k, s.ids + t * g.k,
+                       s.w + t * g.k);
+}
+
+// Ring position shared by the producer's and the consumers' loops.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    int slots;
+    __device__ __forceinline__ explicit Ring(int n) : slots(n) {}
+    __device__ __forceinline__ void next() {
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// One expert's part of a CTA's range of down tiles: [a, b) in kb * MT + m.
+// The tiles are taken by chunks of k-blocks, within a chunk row tile by row
+// tile, so a row tile's sum over the chunk stays in registers.
+__device__ __forceinline__ int kb_lo(int kbA, int m, int MT, int a) {
+    return kbA + (kbA * MT + m < a ? 1 : 0);
+}
+__device__ __forceinline__ int kb_hi(int kbB, int m, int MT, int b) {
+    return kbB - ((kbB - 1) * MT + m >= b ? 1 : 0);
+}
+
+template <bool FP8, int NB>
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
+    extern __shared__ uint8_t dsmem_raw[];
+    __shared__ Shared s;
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(dsmem_raw) + 127) & ~static_cast<uintptr_t>(127));
+    constexpr int SLOT = slot_bytes<FP8, NB>();
+    constexpr int BK = tile_k<FP8>();
+    constexpr int CK = chunk_kb<FP8>();
+    uint8_t* hbuf = smem + g.slots * SLOT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = gridDim.x, cta = blockIdx.x;
+
+    // a workspace that was never initialised would hang the barriers: every
+    // CTA sees the same word and leaves
+    if (__ldcg(&g.hdr->magic) != kMagic) {
+        if (threadIdx.x == 0) report(g.status, MOE_ERR_DEVICE);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < g.slots; ++i) {
+            mbar_init(&s.full[i], 1);
+            mbar_init(&s.empty[i], kConsumerWarps);
+        }
+        fence_mbar_init();
+        s.abort = 0;
+    }
+    for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) s.mask[e] = 0;
+
+    // ---- routing (every CTA, all tokens)
+    if (g.E <= 32) route_tokens<1>(g, s, warp);
+    else if (g.E <= 64) route_tokens<2>(g, s, warp);
+    else if (g.E <= 128) route_tokens<4>(g, s, warp);
+    else route_tokens<8>(g, s, warp);
+    __syncthreads();
+    const int A = g.T * g.k;
+    for (int f = threadIdx.x; f < A; f += kThreads)
+        atomicOr(&s.mask[s.ids[f]], 1u << (f / g.k));
+    if (cta == 0) {
+        for (int f = threadIdx.x; f < A; f += kThreads) {
+            if (g.ids) g.ids[f] = s.ids[f];
+            if (g.w) g.w[f] = s.w[f];
+        }
+    }
+    __syncthreads();
+    // active experts in ascending order, and the first column of each
+    {
+        const int e = threadIdx.x;
+        const uint32_t mk = e < kMaxExperts ? s.mask[e] : 0u;
+        const unsigned bal = __ballot_sync(kFullWarp, mk != 0);
+        if (lane == 0 && warp < kConsumerWarps) s.scan[warp] = __popc(bal);
+        __syncthreads();
+        int before = __popc(bal & ((1u << lane) - 1u));
+        for (int i = 0; i < kConsumerWarps; ++i)
+            if (i < warp) before += s.scan[i];
+        if (mk != 0) {
+            s.rank[e] = before;
+            s.expert[before] = e;
+        }
+        if (e == kMaxExperts - 1) s.n_active = before + (mk != 0);
+    }
+    __syncthreads();
+    const int n_active = s.n_active;
+    if (warp == 0) {
+        // exclusive scan of the active experts' token counts
+        int run = 0;
+        for (int i0 = 0; i0 < n_active; i0 += 32) {
+            const int i = i0 + lane;
+            const int c = i < n_active ? __popc(s.mask[s.expert[i]]) : 0;
+            int inc = c;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int o = __shfl_up_sync(kFullWarp, inc, off);
+                if (lane >= off) inc += o;
+            }
+            if (i < n_active) s.base[i] = run + inc - c;
+            run += __shfl_sync(kFullWarp, inc, 31);
+        }
+        if (lane == 0) s.base[n_active] = run;
+    }
+    const int L1 = n_active * g.mt_gu * g.kb_gu, L2 = n_active * g.mt_dn * g.kb_dn;
+    const int G1 = L1 < G ? L1 : G, G2 = L2 < G ? L2 : G;
+    for (int c = threadIdx.x; c <= G; c += kThreads) {
+        s.start1[c] = c < G1 ? static_cast<int>(static_cast<long long>(L1) * c / G1) : L1;
+        s.start2[c] = c < G2 ? static_cast<int>(static_cast<long long>(L2) * c / G2) : L2;
+    }
+    __syncthreads();
+    for (int f = threadIdx.x; f < A; f += kThreads) {
+        const int e = s.ids[f], t = f / g.k;
+        s.tok[s.base[s.rank[e]] + __popc(s.mask[e] & ((1u << t) - 1u))] = t;
+    }
+    __syncthreads();
+    const int a1 = s.start1[cta], b1 = s.start1[cta + 1];
+    const int a2 = s.start2[cta], b2 = s.start2[cta + 1];
+    const int S1 = g.mt_gu * g.kb_gu, S2 = g.mt_dn * g.kb_dn;   // tiles per expert
+
+    if (warp == kConsumerWarps) {
+        // ---- producer: one thread keeps the ring full through both products
+        if (lane == 0) {
+            Ring ring(g.slots);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int X = a1; X < b1 && ok; ++X) {
+                const int i = X / S1;
+                const int r = X - i * S1;
+                const int kb = r % g.kb_gu;
+                const int e = s.expert[i], c0 = s.base[i], cnt = s.base[i + 1] - c0;
+                if (it >= static_cast<uint32_t>(g.slots) &&
+                    !mbar_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* dst = smem + ring.slot * SLOT;
+                const int left = (g.H - kb * BK) * 2;
+                const uint32_t xb = left < BK * 2 ? left : BK * 2;
+                mbar_arrive_expect_tx(&s.full[ring.slot], kTileBytes + cnt * xb);
+                bulk_load(dst, g.w_gu + (static_cast<size_t>(e) * S1 + r) * kTileBytes, kTileBytes,
+                          &s.full[ring.slot], kEvictFirst);
+                for (int c = 0; c < cnt; ++c)
+                    bulk_load(dst + kTileBytes + c * x_row_bytes<FP8>(),
+                              g.x + static_cast<size_t>(s.tok[c0 + c]) * g.H + kb * BK, xb,
+                              &s.full[ring.slot], kEvictLast);
+                ring.next();
+                ++it;
+            }
+            for (int X = a2; X < b2 && ok;) {
+                const int i = X / S2, e = s.expert[i];
+                const int a = X - i * S2;
+                const int b = b2 - i * S2 < S2 ? b2 - i * S2 : S2;
+                const uint8_t* w = g.w_dn + static_cast<size_t>(e) * S2 * kTileBytes;
+                const int kb_end = (b - 1) / g.mt_dn + 1;
+                for (int kbA = a / g.mt_dn; kbA < kb_end && ok; kbA += CK) {
+                    const int kbB = kbA + CK < kb_end ? kbA + CK : kb_end;
+                    for (int m = 0; m < g.mt_dn && ok; ++m) {
+                        const int hi = kb_hi(kbB, m, g.mt_dn, b);
+                        for (int kb = kb_lo(kbA, m, g.mt_dn, a); kb < hi; ++kb) {
+                            if (it >= static_cast<uint32_t>(g.slots) &&
+                                !mbar_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
+                                ok = false;
+                                break;
+                            }
+                            mbar_arrive_expect_tx(&s.full[ring.slot], kTileBytes);
+                            bulk_load(smem + ring.slot * SLOT,
+                                      w + (static_cast<size_t>(m) * g.kb_dn + kb) * kTileBytes,
+                                      kTileBytes, &s.full[ring.slot], kEvictFirst);
+                            ring.next();
+                            ++it;
+                        }
+                    }
+                }
+                X = i * S2 + b;
+            }
+            if (!ok) {
+                fault(s, g.status);
+                // this CTA's copies in flight land before its memory goes:
+                // the last `slots` of them, or fewer
+                Ring back(g.slots);
+                const uint32_t first = it > static_cast<uint32_t>(g.slots) ? it - g.slots : 0;
+                for (uint32_t j = 0; j < it; ++j) {
+                    if (j >= first) mbar_wait(&s.full[back.slot], back.phase, nullptr, 10000000ull);
+                    back.next();
+                }
+            }
+        }
+    } else {
+        // ---- consumers.  After a fault every wait returns at once, and the
+        // loops run on to their ends, so all warps meet at the same barriers.
+        const int gq = lane >> 2, t = lane & 3;
+        Ring ring(g.slots);
+        // step 1: gate/up partial sums
+        for (int X = a1; X < b1;) {
+            const int r = X / g.kb_gu;                 // row tile over all active experts
+            const int i = r / g.mt_gu, m = r - i * g.mt_gu;
+            const int end = (r + 1) * g.kb_gu < b1 ? (r + 1) * g.kb_gu : b1;
+            const int cnt = s.base[i + 1] - s.base[i];
+            const int nb = NB == 1 ? 1 : (cnt + 7) >> 3;
+            float acc[NB][4];
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[n][q] = 0.0f;
+            for (; X < end; ++X) {
+                if (!mbar_wait(&s.full[ring.slot], ring.phase, &s.abort)) fault(s, g.status);
+                const uint8_t* tile = smem + ring.slot * SLOT;
+                uint4 a[4];
+                load_a<FP8, NB>(a, tile, warp, gq, t);
+                const bool half_row = FP8 && (X - r * g.kb_gu + 1) * BK > g.H;
+                tile_mma<FP8, NB>(acc, a, tile + kTileBytes + gq * x_row_bytes<FP8>(),
+                                  x_row_bytes<FP8>(), t, half_row, nb);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
+                ring.next();
+            }
+            // columns of 128 rows; segment (row tile r, CTA c) starts at column
+            // sum of the counts before r + c * T: segments follow one another
+            // with r or c or both growing, so no two overlap
+            float* p = g.p1 + (static_cast<size_t>(s.base[i]) * g.mt_gu + m * cnt +
+                               static_cast<size_t>(cta) * g.T) * kTileRows;
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int col = n * 8 + 2 * t + (q & 1);
+                    if (col < cnt)
+                        __stcg(p + col * kTileRows + 16 * warp + gq + 8 * (q >> 1), acc[n][q]);
+                }
+        }
+        consumer_sync();
+        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[0][0], G)) fault(s, g.status);
+        consumer_sync();
+
+        // step 2: h of this CTA's k-blocks, and the down partial sums
+        const float per1 = static_cast<float>(G1) / static_cast<float>(L1);
+        for (int X = a2; X < b2;) {
+            const int i = X / S2, e = s.expert[i];
+            const int a = X - i * S2;
+            const int b = b2 - i * S2 < S2 ? b2 - i * S2 : S2;
+            const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
+            const int nb = NB == 1 ? 1 : (cnt + 7) >> 3;
+            const int kb_first = a / g.mt_dn, kb_end = (b - 1) / g.mt_dn + 1;
+            float sg = 1.0f, su = 1.0f;
+            if constexpr (FP8) {
+                sg = __ldg(g.scales + e * 3);
+                su = __ldg(g.scales + e * 3 + 1);
+            }
+            float* p = g.p2 + (static_cast<size_t>(c0) + static_cast<size_t>(cta) * g.T) *
+                                  g.mt_dn * kTileRows;
+            for (int kbA = kb_first; kbA < kb_end; kbA += CK) {
+                const int kbB = kbA + CK < kb_end ? kbA + CK : kb_end;
+                const int cols = (kbB - kbA) * BK;
+                for (int idx = threadIdx.x; idx < cols * cnt; idx += kConsumers) {
+                    const int c = idx / cols, j = idx - c * cols;
+                    const int hc = kbA * BK + j;
+                    float h = 0.0f;
+                    if (hc < g.I) {
+                        const int m = hc >> 6, l = hc & 63;
+                        const int row = 32 * (l >> 4) + (l & 15);
+                        const int X0 = (i * g.mt_gu + m) * g.kb_gu;
+                        const int cf = owner(s.start1, G1, X0, per1);
+                        const int cl = owner(s.start1, G1, X0 + g.kb_gu - 1, per1);
+                        const float* q = g.p1 + (static_cast<size_t>(c0) * g.mt_gu + m * cnt + c +
+                                                 static_cast<size_t>(cf) * g.T) * kTileRows + row;
+                        float gt = 0.0f, up = 0.0f;
+                        for (int cc = cf; cc <= cl; ++cc) {
+                            gt += __ldcg(q);
+                            up += __ldcg(q + 16);
+                            q += static_cast<size_t>(g.T) * kTileRows;
+                        }
+                        gt *= sg;
+                        up *= su;
+                        h = gt / (1.0f + expf(-gt)) * up;
+                    }
+                    // hi + lo: 16 bits of h's mantissa; an infinite or NaN h is
+                    // all in hi
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(h);
+                    const float rest = h - __bfloat162float(hi);
+                    const __nv_bfloat16 lo =
+                        __float2bfloat16_rn(fabsf(h) < 3.0e38f ? rest : 0.0f);
+                    const int kl = j / BK, jj = j - kl * BK;
+                    __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(
+                        hbuf + (kl * NB * 8 + c) * h_row_bytes<FP8>());
+                    d[jj] = hi;
+                    d[BK + jj] = lo;
+                }
+                consumer_sync();
+                for (int m = 0; m < g.mt_dn; ++m) {
+                    const int lo = kb_lo(kbA, m, g.mt_dn, a), hi = kb_hi(kbB, m, g.mt_dn, b);
+                    if (lo >= hi) continue;
+                    float acc[NB][4];
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) acc[n][q] = 0.0f;
+                    for (int kb = lo; kb < hi; ++kb) {
+                        if (!mbar_wait(&s.full[ring.slot], ring.phase, &s.abort))
+                            fault(s, g.status);
+                        uint4 w[4];
+                        load_a<FP8, NB>(w, smem + ring.slot * SLOT, warp, gq, t);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
+                        ring.next();
+                        const uint8_t* hb =
+                            hbuf + ((kb - kbA) * NB * 8 + gq) * h_row_bytes<FP8>();
+                        tile_mma<FP8, NB>(acc, w, hb, h_row_bytes<FP8>(), t, false, nb);
+                        tile_mma<FP8, NB>(acc, w, hb + BK * 2, h_row_bytes<FP8>(), t, false, nb);
+                    }
+                    // later chunks of the same expert add to the columns that
+                    // the same thread wrote: of several chunks the first has at
+                    // least four k-blocks, so every row tile is in it
+                    const bool first = kbA == kb_first;
+                    float* d = p + static_cast<size_t>(m) * cnt * kTileRows;
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int col = n * 8 + 2 * t + (q & 1);
+                            if (col < cnt) {
+                                float* dd = d + col * kTileRows + 16 * warp + gq + 8 * (q >> 1);
+                                __stcg(dd, first ? acc[n][q] : __ldcg(dd) + acc[n][q]);
+                            }
+                        }
+                }
+                consumer_sync();   // hbuf is free
+            }
+            X = i * S2 + b;
+        }
+        consumer_sync();
+        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[1][0], G)) fault(s, g.status);
+        consumer_sync();
+
+        // step 3: out[t] = residual[t] + sum over the token's assignments and
+        // their CTAs, in ascending order of both.  SPL warps of a CTA share an
+        // output's terms (each every SPL-th) when there are few outputs.
+        const int rows32 = g.T * ((g.H + 31) / 32);
+        int spl = 1;
+        while (spl < kConsumerWarps && rows32 * spl * 2 <= G * kConsumerWarps) spl *= 2;
+        const int groups = kConsumerWarps / spl;
+        const int sub = warp % spl, grp = warp / spl;
+        const float per2 = static_cast<float>(G2) / static_cast<float>(L2);
+        const int hrows = (g.H + 31) / 32;
+        for (int item0 = cta * groups; item0 < rows32; item0 += G * groups) {
+            const int item = item0 + grp;
+            const int tk = item / hrows, col = (item - tk * hrows) * 32 + lane;
+            float sum = 0.0f;
+            if (item < rows32) {
+                const int m = col / kTileRows, row = col - m * kTileRows;
+                int cum = 0;
+                for (int j = 0; j < g.k; ++j) {
+                    const int e = s.ids[tk * g.k + j], i = s.rank[e];
+                    const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
+                    const int c = __popc(s.mask[e] & ((1u << tk) - 1u));
+                    const int cf = owner(s.start2, G2, i * S2, per2);
+                    const int n = owner(s.start2, G2, (i + 1) * S2 - 1, per2) - cf + 1;
+                    const float* q = g.p2 + ((static_cast<size_t>(c0) +
+                                              static_cast<size_t>(cf) * g.T) * g.mt_dn +
+                                             static_cast<size_t>(m) * cnt + c) * kTileRows + row;
+                    const size_t step = static_cast<size_t>(g.T) * g.mt_dn * kTileRows;
+                    float part = 0.0f;
+#pragma unroll 4
+                    for (int cc = (sub - cum) & (spl - 1); cc < n; cc += spl) {
+                        // does CTA cf + cc hold a tile of row tile m?
+                        int a = s.start2[cf + cc] - i * S2, b = s.start2[cf + cc + 1] - i * S2;
+                        a = a < 0 ? 0 : a;
+                        b = b > S2 ? S2 : b;
+                        bool has = b - a >= g.mt_dn;
+                        if (!has) {
+                            int d = m - a % g.mt_dn;
+                            if (d < 0) d += g.mt_dn;
+                            has = d < b - a;
+                        }
+                        if (has) part += __ldcg(q + cc * step);
+                    }
+                    cum += n;
+                    float wt = s.w[tk * g.k + j];
+                    if constexpr (FP8) wt *= __ldg(g.scales + e * 3 + 2);
+                    sum += wt * part;
+                }
+            }
+            if (spl > 1) {
+                s.red[threadIdx.x] = sum;
+                consumer_sync();
+                if (sub == 0) {
+                    for (int q = 1; q < spl; ++q) sum += s.red[threadIdx.x + 32 * q];
+                }
+                consumer_sync();
+            }
+            if (sub == 0 && item < rows32 && col < g.H) {
+                const size_t o = static_cast<size_t>(tk) * g.H + col;
+                if (g.residual) sum += __bfloat162float(g.residual[o]);
+                g.out[o] = __float2bfloat16_rn(sum);
+            }
+        }
+    }
+}
+
+__global__ void decode_ws_init_kernel(Header* h) {
+    if (threadIdx.x == 0) {
+        h->status = 0;
+        h->arrive[0][0] = 0;
+        h->arrive[1][0] = 0;
+        h->magic = kMagic;
+    }
+}
+
+// The opt-in to more than 48 KB of dynamic shared memory, once per device and
+// instantiation.
+constexpr int kMaxDevices = 64;
+constexpr int kDynSmemMax = kSmemBytes - static_cast<int>(sizeof(Shared)) - 1024;
+
+template <bool FP8, int NB>
+cudaError_t opt_in_smem() {
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t err[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [dev] {
+        err[dev] = cudaFuncSetAttribute(decode_kernel<FP8, NB>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmemMax);
+    });
+    return err[dev];
+}
+
+template <bool FP8, int NB>
+cudaError_t launch(const Args& a, int grid, cudaStream_t s) {
+    auto kern = decode_kernel<FP8, NB>;
+    const cudaError_t e = opt_in_smem<FP8, NB>();
+    if (e != cudaSuccess) return e;
+    constexpr int dyn = kDynSmemMax;
+    Args g = a;
+    int slots = (dyn - 128 - h_bytes<FP8, NB>()) / slot_bytes<FP8, NB>();
+    g.slots = slots > kMaxSlots ? kMaxSlots : slots;
+    if (g.slots < 2) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = 128 + g.slots * slot_bytes<FP8, NB>() + h_bytes<FP8, NB>();
+    cfg.stream = s;
+    // cooperative: the blocks wait on one another, so all must be resident
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, g);
+}
+
+struct Sizes {
+    size_t p1, p2, total;
+};
+
+Sizes sizes(bool fp8, int T, int k, int E, int H, int I, int grid) {
+    const PackedGeom geo = packed_geom(fp8, E, H, I);
+    const size_t A = static_cast<size_t>(T) * k, col = kTileRows * sizeof(float);
+    Sizes z;
+    z.p1 = (A * geo.mt_gu + static_cast<size_t>(grid) * T) * col;
+    z.p2 = (A + static_cast<size_t>(grid) * T) * geo.mt_dn * col;
+    z.total = sizeof(Header) + z.p1 + z.p2;
+    return z;
+}
+
+}  // namespace
+
+size_t decode_ws_bytes(int fp8, int T, int k, int E, int H, int I) {
+    return sizes(fp8 != 0, T, k, E, H, I, device_sm_count()).total;
+}
+
+cudaError_t launch_decode_ws_init(void* ws, cudaStream_t s) {
+    static_assert(sizeof(Header) % 16 == 0, "partial sums stay 16-byte aligned");
+    decode_ws_init_kernel<<<1, 32, 0, s>>>(static_cast<Header*>(ws));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decode(const DecodeProblem& p, cudaStream_t s) {
+    const bool fp8 = p.fp8 != 0;
+    const PackedGeom geo = packed_geom(fp8, p.E, p.H, p.I);
+    const int grid = device_sm_count();
+    const Sizes z = sizes(fp8, p.T, p.k, p.E, p.H, p.I, grid);
+    Args g{};
+    g.T = p.T;
+    g.k = p.k;
+    g.E = p.E;
+    g.H = p.H;
+    g.I = p.I;
+    g.mt_gu = geo.mt_gu;
+    g.kb_gu = geo.kb_gu;
+    g.mt_dn = geo.mt_dn;
+    g.kb_dn = geo.kb_dn;
+    g.w_gu = static_cast<const uint8_t*>(p.packed);
+    g.w_dn = g.w_gu + geo.gu_bytes;
+    g.scales = p.scales;
+    g.x = static_cast<const __nv_bfloat16*>(p.x);
+    g.logits = p.logits;
+    g.residual = static_cast<const __nv_bfloat16*>(p.residual);
+    g.out = static_cast<__nv_bfloat16*>(p.out);
+    g.ids = p.ids;
+    g.w = p.w;
+    g.hdr = static_cast<Header*>(p.ws);
+    g.status = p.status ? p.status : &g.hdr->status;
+    g.p1 = reinterpret_cast<float*>(static_cast<char*>(p.ws) + sizeof(Header));
+    g.p2 = reinterpret_cast<float*>(static_cast<char*>(p.ws) + sizeof(Header) + z.p1);
+    // more than 8 tokens take two blocks of 8 columns
+    if (fp8) return p.T <= 8 ? launch<true, 1>(g, grid, s) : launch<true, 2>(g, grid, s);
+    return p.T <= 8 ? launch<false, 1>(g, grid, s) : launch<false, 2>(g, grid, s);
+}
+
+}  // namespace moe

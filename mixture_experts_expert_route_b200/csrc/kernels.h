@@ -192,6 +192,26 @@ cudaError_t launch_grouped_gemm(const GemmProblem& p, cudaStream_t s);
 
 int device_sm_count();
 
+// ---- the whole layer for a few tokens (decode.cu)
+constexpr int kDecodeMaxT = 16;
+constexpr int kDecodeMaxAssign = 128;   // T * k
+struct DecodeProblem {
+    int fp8, T, k, E, H, I;
+    const void* x;
+    const float* logits;
+    const void* packed;
+    const float* scales;
+    const void* residual;    // bf16 [T, H] or null
+    void* out;
+    int32_t* ids;            // optional outputs
+    float* w;
+    int32_t* status;         // null: the workspace's own
+    void* ws;                // decode_ws_bytes, initialised once
+};
+size_t decode_ws_bytes(int fp8, int T, int k, int E, int H, int I);
+cudaError_t launch_decode_ws_init(void* ws, cudaStream_t s);
+cudaError_t launch_decode(const DecodeProblem& p, cudaStream_t s);
+
 // ---- the bf16 grouped FFN (a3..a6) over E_sub consecutive segments of a
 // permutation (moe_api.cu): counts/offsets point at the first of them and
 // may start inside a larger permutation, whose other rows are left alone;

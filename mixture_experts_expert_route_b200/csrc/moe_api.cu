@@ -623,6 +623,52 @@ moe_status moe_forward(const moe_forward_args* a, void* ws, size_t ws_bytes, moe
     return MOE_OK;
 }
 
+namespace {
+moe_status check_decode(moe_dtype dt, int T, int k, int E, int H, int I) {
+    moe_status st = check_layer(dt, T, k, E, H, I, 16);
+    if (st != MOE_OK) return st;
+    if (T > kDecodeMaxT || static_cast<long long>(T) * k > kDecodeMaxAssign)
+        return MOE_ERR_UNSUPPORTED;
+    // tile indices over the active experts are 32-bit
+    const PackedGeom g = packed_geom(dt == MOE_FP8_E4M3, 1, H, I);
+    const long long act = static_cast<long long>(T) * k < E ? T * k : E;
+    if (act * g.mt_gu * g.kb_gu > 0x7fffffffLL || act * g.mt_dn * g.kb_dn > 0x7fffffffLL)
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+}  // namespace
+
+size_t moe_decode_workspace_size(moe_dtype dtype, int T, int k, int E, int H, int I) {
+    if (check_decode(dtype, T, k, E, H, I) != MOE_OK) return 0;
+    return decode_ws_bytes(dtype == MOE_FP8_E4M3, T, k, E, H, I);
+}
+
+moe_status moe_decode_workspace_init(void* ws, size_t ws_bytes, moe_stream_t stream) {
+    if (!ws || ws_bytes < kAlign || !aligned16(ws)) return MOE_ERR_WORKSPACE;
+    return from_cuda(launch_decode_ws_init(ws, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_decode_forward(const moe_decode_args* a, void* ws, size_t ws_bytes,
+                              moe_stream_t stream) {
+    if (!a) return MOE_ERR_INVALID_ARG;
+    const moe_status st = check_decode(a->dtype, a->T, a->k, a->E, a->H, a->I);
+    if (st != MOE_OK) return st;
+    if (a->T == 0) return MOE_OK;
+    if (!a->x || !a->logits || !a->packed || !a->out) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(a->x) || !aligned16(a->packed) || !aligned16(a->out) ||
+        !aligned16(a->residual))
+        return MOE_ERR_INVALID_ARG;
+    if (a->dtype == MOE_FP8_E4M3 && !a->scales) return MOE_ERR_INVALID_ARG;
+    const bool fp8 = a->dtype == MOE_FP8_E4M3;
+    if (!ws || !aligned16(ws) ||
+        ws_bytes < decode_ws_bytes(fp8, a->T, a->k, a->E, a->H, a->I))
+        return MOE_ERR_WORKSPACE;
+    const DecodeProblem p{fp8, a->T, a->k, a->E, a->H, a->I, a->x, a->logits, a->packed,
+                          a->scales, a->residual, a->out, a->ids, a->w, a->status, ws};
+    Range r("moe_decode_forward");
+    return from_cuda(launch_decode(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 moe_status moe_check_status(const int32_t* dev_status, moe_stream_t stream) {
     if (!dev_status) return MOE_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -149,3 +149,53 @@ def test_missing_library_fails_loudly(monkeypatch, tmp_path):
     # and a CUDA tensor argument is required: host tensors are refused, not copied
     with pytest.raises(ValueError):
         binding._ptr(torch.zeros(1))
+
+
+def _decode_args(L, **kw):
+    base = dict(dtype=0, T=4, k=2, E=8, H=256, I=512, x=0x1000, logits=0x1000, packed=0x1000,
+                scales=None, residual=None, out=0x1000, ids=None, w=None, status=None)
+    base.update(kw)
+    return L._lib.DecodeArgs(*[base[f] for f, _ in L._lib.DecodeArgs._fields_])
+
+
+def test_decode_argument_errors(L):
+    lib = L.lib()
+    INVALID, UNSUP, WS = 1, 2, 3
+    ws, big = ctypes.c_void_p(0x1000), 1 << 40
+
+    def call(ws=ws, n=big, **kw):
+        return lib.moe_decode_forward(ctypes.byref(_decode_args(L, **kw)), ws, n, None)
+
+    assert lib.moe_decode_forward(None, ws, big, None) == INVALID
+    assert call(T=-1) == INVALID
+    assert call(T=0, x=None, out=None, ws=None, n=0) == 0            # no-op
+    assert call(T=17) == UNSUP
+    assert call(T=16, k=9, E=16) == UNSUP                            # T * k > 128
+    assert call(k=9) == INVALID
+    assert call(E=300) == UNSUP
+    assert call(H=100) == UNSUP
+    assert call(I=32) == INVALID
+    assert call(dtype=5) == INVALID
+    assert call(dtype=1) == INVALID                                  # e4m3 without scales
+    for name in ("x", "logits", "packed", "out"):
+        assert call(**{name: None}) == INVALID
+    for name in ("x", "packed", "out", "residual"):
+        assert call(**{name: 0x1008}) == INVALID
+    need = lib.moe_decode_workspace_size(0, 4, 2, 8, 256, 512)
+    assert need > 0
+    assert call(n=need - 1) == WS
+    assert call(ws=None) == WS
+    assert call(ws=ctypes.c_void_p(0x1008)) == WS
+    assert lib.moe_decode_workspace_size(0, 17, 2, 8, 256, 512) == 0
+    assert lib.moe_decode_workspace_size(0, 4, 2, 8, 200, 512) == 0
+    assert lib.moe_decode_workspace_size(0, 16, 2, 8, 256, 512) > need
+    assert lib.moe_decode_workspace_init(None, big, None) == WS
+    assert lib.moe_decode_workspace_init(ws, 16, None) == WS
+
+
+def test_decode_binding_refuses_host_tensors(L):
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        L.decode_forward(0, x, torch.zeros((2, 8)), x, None, 8, 64, 2)
+    with pytest.raises(ValueError):
+        L.decode_forward(0, x[0], torch.zeros((2, 8)), x, None, 8, 64, 2)
