@@ -43,7 +43,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kConsumerWarps = 8;                 // 16 weight rows of a tile each
+// Two groups of eight warps, one warp per 16 weight rows of a tile; the groups
+// take tiles in turn.  Every warp waits for every tile and frees it, its own or
+// not: a warp that went by the other group's tiles unseen could come round to a
+// slot whose barrier is still a phase behind, which a parity cannot tell.
+constexpr int kGroups = 2;
+constexpr int kConsumerWarps = 8 * kGroups;
 constexpr int kConsumers = kConsumerWarps * 32;
 constexpr int kThreads = kConsumers + 32;         // and one producer warp
 constexpr int kMaxSlots = 12;
@@ -53,10 +58,12 @@ constexpr uint32_t kMagic = 0x4d6f4465u;
 // h columns held at a time: 512 (8 k-blocks of bf16 tiles, 4 of e4m3 tiles)
 template <bool FP8> __host__ __device__ constexpr int tile_k() { return FP8 ? 128 : 64; }
 template <bool FP8> __host__ __device__ constexpr int chunk_kb() { return FP8 ? 4 : 8; }
-// bytes of one token's row of an x slice, and of a k-block of h (hi | lo), each
-// plus 16 so that two rows start an odd number of 16-byte banks apart
-template <bool FP8> __host__ __device__ constexpr int x_row_bytes() { return tile_k<FP8>() * 2 + 16; }
+// bytes of one token's row of a k-block of h (hi | lo), plus 16 so that two
+// rows start an odd number of 16-byte banks apart
 template <bool FP8> __host__ __device__ constexpr int h_row_bytes() { return tile_k<FP8>() * 4 + 16; }
+// a token's x of one gate/up tile, padded likewise, and a ring slot: a weight
+// tile and the x slices of up to NB * 8 tokens
+template <bool FP8> __host__ __device__ constexpr int x_row_bytes() { return tile_k<FP8>() * 2 + 16; }
 template <bool FP8, int NB> __host__ __device__ constexpr int slot_bytes() {
     return kTileBytes + NB * 8 * x_row_bytes<FP8>();
 }
@@ -66,7 +73,8 @@ template <bool FP8, int NB> __host__ __device__ constexpr int h_bytes() {
 
 // Workspace header, zeroed but for the magic by moe_decode_workspace_init.
 // The arrival counters only grow, by one per CTA and launch, so each launch
-// finds them at a multiple of the grid and no launch has to reset them.
+// finds them at a multiple of the grid (and they stay below the next one until
+// its own CTA arrives), and no launch has to reset them.
 struct Header {
     int32_t status;
     uint32_t magic;
@@ -97,15 +105,16 @@ struct Shared {
     uint64_t full[kMaxSlots];
     uint64_t empty[kMaxSlots];
     int abort;
-    int n_active;
     int ids[kDecodeMaxAssign];          // [T][k]
     float w[kDecodeMaxAssign];
     uint32_t mask[kMaxExperts];         // tokens that chose an expert
     int rank[kMaxExperts];              // index among the active experts
-    int scan[kConsumerWarps];
+    int scan[kMaxExperts / 32];
     int expert[kDecodeMaxAssign];       // active experts, ascending
     int base[kDecodeMaxAssign + 1];     // first column of an active expert
     int tok[kDecodeMaxAssign];          // column -> token
+    int first2[kDecodeMaxAssign];       // first CTA of an expert's down tiles
+    int ncta2[kDecodeMaxAssign];        // and how many
     int start1[kMaxCtas + 1];           // first gate/up tile of each CTA
     int start2[kMaxCtas + 1];           // first down tile of each CTA
     float red[kConsumers];
@@ -150,22 +159,18 @@ __device__ __forceinline__ void fault(Shared& s, int32_t* status) {
     *reinterpret_cast<volatile int*>(&s.abort) = 1;
 }
 
-// Arrive of this CTA at a grid barrier, and the bounded wait for the others.
-// Called by one thread, between two CTA barriers of the consumers.
-__device__ __forceinline__ bool grid_barrier(uint64_t* counter, int G) {
-    __threadfence();
-    const unsigned long long old =
-        atomicAdd(reinterpret_cast<unsigned long long*>(counter), 1ull);
-    const unsigned long long target = (old / G + 1) * G;
+// Arrival of this CTA at a grid barrier and the bounded wait until the counter
+// reaches `target`.  Called by one thread, between two consumer_sync.
+__device__ __forceinline__ bool grid_barrier(uint64_t* counter, uint64_t target) {
+    asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.u64 [%0], 1;" ::"l"(counter)
+                 : "memory");
     const uint64_t t0 = globaltimer_ns();
     while (true) {
-        unsigned long long v;
+        uint64_t v;
         asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(counter) : "memory");
-        if (v >= target) break;
+        if (v >= target) return true;
         if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
     }
-    __threadfence();
-    return true;
 }
 
 // One tile's products: acc += W[16 rows of this warp] x B[NB * 8 tokens].
@@ -173,26 +178,29 @@ __device__ __forceinline__ bool grid_barrier(uint64_t* counter, int G) {
 // operands: lane (g, t) takes 16-byte pieces 2t and 2t+1 of its rows, whose
 // swizzled places are conflict-free for a quarter warp.  `b` points at this
 // lane's column g; block n of 8 columns is at +8 rows.
-template <bool FP8, int NB>
-__device__ __forceinline__ void load_a(uint4 (&a)[4], const uint8_t* tile, int warp, int g, int t) {
-    const uint8_t* r = tile + (16 * warp + g) * kTileRowBytes;
-    const int p0 = ((2 * t) ^ g) * 16, p1 = ((2 * t + 1) ^ g) * 16;
+__device__ __forceinline__ void load_a(uint4 (&a)[4], const uint8_t* tile, int row, int t) {
+    const uint8_t* r = tile + row * kTileRowBytes;
+    const int p0 = ((2 * t) ^ (row & 7)) * 16, p1 = ((2 * t + 1) ^ (row & 7)) * 16;
     a[0] = lds16(r + p0);
     a[1] = lds16(r + p1);
     a[2] = lds16(r + 8 * kTileRowBytes + p0);
     a[3] = lds16(r + 8 * kTileRowBytes + p1);
 }
 
+// One lane's activations for one tile and a block of 8 tokens: 32 (bf16 tiles)
+// or 64 (e4m3 tiles) bytes of its column's row, from 32 t or 64 t.
+template <bool FP8> struct BFrag {
+    uint4 v[FP8 ? 4 : 2];
+};
+
 template <bool FP8, int NB>
 __device__ __forceinline__ void tile_mma(float (&acc)[NB][4], const uint4 (&a)[4],
-                                         const uint8_t* b, int row_bytes, int t, bool half_row,
-                                         int nb) {
+                                         const BFrag<FP8> (&b)[NB], int nb) {
     if constexpr (!FP8) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             if (n < nb) {
-                const uint4 b0 = lds16(b + n * 8 * row_bytes + 32 * t);
-                const uint4 b1 = lds16(b + n * 8 * row_bytes + 32 * t + 16);
+                const uint4 b0 = b[n].v[0], b1 = b[n].v[1];
                 mma_bf16(acc[n], a[0].x, a[2].x, a[0].y, a[2].y, b0.x, b0.y);
                 mma_bf16(acc[n], a[0].z, a[2].z, a[0].w, a[2].w, b0.z, b0.w);
                 mma_bf16(acc[n], a[1].x, a[3].x, a[1].y, a[3].y, b1.x, b1.y);
@@ -216,23 +224,49 @@ __device__ __forceinline__ void tile_mma(float (&acc)[NB][4], const uint4 (&a)[4
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 if (n < nb) {
-                    uint4 bv = lds16(b + n * 8 * row_bytes + 64 * t + 16 * p);
-                    // the last k-block may hold 64 of its 128 columns: the
-                    // weights are zero there, the activations not written
-                    if (half_row && t >= 2) bv = make_uint4(0, 0, 0, 0);
-                    mma_bf16(acc[n], f[0], f[1], f[2], f[3], bv.x, bv.y);
-                    mma_bf16(acc[n], f[4], f[5], f[6], f[7], bv.z, bv.w);
+                    mma_bf16(acc[n], f[0], f[1], f[2], f[3], b[n].v[p].x, b[n].v[p].y);
+                    mma_bf16(acc[n], f[4], f[5], f[6], f[7], b[n].v[p].z, b[n].v[p].w);
                 }
             }
         }
     }
 }
 
+// This lane's columns of a slot's x slices.  Columns past the expert's count
+// are never read back; the last e4m3 k-block may hold 64 of its 128 columns
+// (`half`): the rest meets zero weights and must not be garbage.
+template <bool FP8, int NB>
+__device__ __forceinline__ void load_x(BFrag<FP8> (&b)[NB], const uint8_t* xs, int t, int nb,
+                                       bool half) {
+    constexpr int N = FP8 ? 4 : 2;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+        if (n < nb)
+#pragma unroll
+            for (int p = 0; p < N; ++p) {
+                b[n].v[p] = lds16(xs + n * 8 * x_row_bytes<FP8>() + t * (N * 16) + p * 16);
+                if (FP8 && half && t >= 2) b[n].v[p] = make_uint4(0, 0, 0, 0);
+            }
+}
+
+template <bool FP8, int NB>
+__device__ __forceinline__ void load_h(BFrag<FP8> (&b)[NB], const uint8_t* hb, int t, int nb) {
+    constexpr int N = FP8 ? 4 : 2;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+        if (n < nb)
+#pragma unroll
+            for (int p = 0; p < N; ++p)
+                b[n].v[p] = lds16(hb + n * 8 * h_row_bytes<FP8>() + t * (N * 16) + p * 16);
+}
+
 template <int EPL>
-__device__ __forceinline__ void route_tokens(const Args& g, Shared& s, int warp) {
-    for (int t = warp; t < g.T; t += kThreads / 32)
-        warp_topk<EPL>(g.logits + static_cast<long>(t) * g.E, g.E, g.k, s.ids + t * g.k,
-                       s.w + t * g.k);
+__device__ __forceinline__ void route_tokens(const Args& g, Shared& s, int warp, int lane) {
+    for (int t = warp; t < g.T; t += kThreads / 32) {
+        int* ids = s.ids + t * g.k;
+        warp_topk<EPL>(g.logits + static_cast<long>(t) * g.E, g.E, g.k, ids, s.w + t * g.k);
+        for (int j = lane; j < g.k; j += 32) atomicOr(&s.mask[ids[j]], 1u << t);
+    }
 }
 
 // Ring position shared by the producer's and the consumers' loops.
@@ -272,13 +306,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, cta = blockIdx.x;
 
-    // a workspace that was never initialised would hang the barriers: every
-    // CTA sees the same word and leaves
-    if (__ldcg(&g.hdr->magic) != kMagic) {
-        if (threadIdx.x == 0) report(g.status, MOE_ERR_DEVICE);
-        return;
-    }
+    // (looked at below, so that its latency hides behind the routing's loads)
+    const uint32_t magic = __ldcg(&g.hdr->magic);
+    uint64_t target[2] = {0, 0};
     if (threadIdx.x == 0) {
+        // the barriers' targets: the next multiples of the grid
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            target[i] = __ldcg(reinterpret_cast<const unsigned long long*>(&g.hdr->arrive[i][0]));
         for (int i = 0; i < g.slots; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], kConsumerWarps);
@@ -287,187 +322,204 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
         s.abort = 0;
     }
     for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) s.mask[e] = 0;
+    __syncthreads();
 
     // ---- routing (every CTA, all tokens)
-    if (g.E <= 32) route_tokens<1>(g, s, warp);
-    else if (g.E <= 64) route_tokens<2>(g, s, warp);
-    else if (g.E <= 128) route_tokens<4>(g, s, warp);
-    else route_tokens<8>(g, s, warp);
-    __syncthreads();
-    const int A = g.T * g.k;
-    for (int f = threadIdx.x; f < A; f += kThreads)
-        atomicOr(&s.mask[s.ids[f]], 1u << (f / g.k));
-    if (cta == 0) {
-        for (int f = threadIdx.x; f < A; f += kThreads) {
-            if (g.ids) g.ids[f] = s.ids[f];
-            if (g.w) g.w[f] = s.w[f];
-        }
+    if (g.E <= 32) route_tokens<1>(g, s, warp, lane);
+    else if (g.E <= 64) route_tokens<2>(g, s, warp, lane);
+    else if (g.E <= 128) route_tokens<4>(g, s, warp, lane);
+    else route_tokens<8>(g, s, warp, lane);
+    // a workspace that was never initialised would hang the barriers: every
+    // CTA sees the same word and leaves
+    if (magic != kMagic) {
+        if (threadIdx.x == 0) report(g.status, MOE_ERR_DEVICE);
+        return;
     }
-    __syncthreads();
-    // active experts in ascending order, and the first column of each
-    {
-        const int e = threadIdx.x;
-        const uint32_t mk = e < kMaxExperts ? s.mask[e] : 0u;
-        const unsigned bal = __ballot_sync(kFullWarp, mk != 0);
-        if (lane == 0 && warp < kConsumerWarps) s.scan[warp] = __popc(bal);
-        __syncthreads();
-        int before = __popc(bal & ((1u << lane) - 1u));
-        for (int i = 0; i < kConsumerWarps; ++i)
-            if (i < warp) before += s.scan[i];
-        if (mk != 0) {
-            s.rank[e] = before;
-            s.expert[before] = e;
-        }
-        if (e == kMaxExperts - 1) s.n_active = before + (mk != 0);
-    }
-    __syncthreads();
-    const int n_active = s.n_active;
-    if (warp == 0) {
-        // exclusive scan of the active experts' token counts
-        int run = 0;
-        for (int i0 = 0; i0 < n_active; i0 += 32) {
-            const int i = i0 + lane;
-            const int c = i < n_active ? __popc(s.mask[s.expert[i]]) : 0;
-            int inc = c;
+    if (threadIdx.x == 0) {
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int o = __shfl_up_sync(kFullWarp, inc, off);
-                if (lane >= off) inc += o;
-            }
-            if (i < n_active) s.base[i] = run + inc - c;
-            run += __shfl_sync(kFullWarp, inc, 31);
-        }
-        if (lane == 0) s.base[n_active] = run;
-    }
-    const int L1 = n_active * g.mt_gu * g.kb_gu, L2 = n_active * g.mt_dn * g.kb_dn;
-    const int G1 = L1 < G ? L1 : G, G2 = L2 < G ? L2 : G;
-    for (int c = threadIdx.x; c <= G; c += kThreads) {
-        s.start1[c] = c < G1 ? static_cast<int>(static_cast<long long>(L1) * c / G1) : L1;
-        s.start2[c] = c < G2 ? static_cast<int>(static_cast<long long>(L2) * c / G2) : L2;
+        for (int i = 0; i < 2; ++i) target[i] = (target[i] / G + 1) * G;
     }
     __syncthreads();
-    for (int f = threadIdx.x; f < A; f += kThreads) {
-        const int e = s.ids[f], t = f / g.k;
-        s.tok[s.base[s.rank[e]] + __popc(s.mask[e] & ((1u << t) - 1u))] = t;
+    // active experts in ascending order with their first columns: one scan of
+    // (active, count) pairs over the experts, a thread each
+    const int e_own = threadIdx.x;
+    const uint32_t mk = e_own < kMaxExperts ? s.mask[e_own] : 0u;
+    const int own = mk ? (1 << 16) | __popc(mk) : 0;
+    int inc = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(kFullWarp, inc, off);
+        if (lane >= off) inc += o;
+    }
+    if (lane == 31 && warp < kMaxExperts / 32) s.scan[warp] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i) {
+        const int v = s.scan[i];
+        if (i < warp) before += v;
+        all += v;
+    }
+    const int n_active = all >> 16;
+    if (mk) {
+        const int ex = before + inc - own;
+        const int i = ex >> 16, c0 = ex & 0xffff;
+        s.rank[e_own] = i;
+        s.expert[i] = e_own;
+        s.base[i] = c0;
+        int c = c0;
+        for (uint32_t m = mk; m; m &= m - 1) s.tok[c++] = __ffs(m) - 1;
+    }
+    if (threadIdx.x == 0) s.base[n_active] = all & 0xffff;
+    const int S1 = g.mt_gu * g.kb_gu, S2 = g.mt_dn * g.kb_dn;   // tiles per expert
+    const int L1 = n_active * S1, L2 = n_active * S2;
+    const int G1 = L1 < G ? L1 : G, G2 = L2 < G ? L2 : G;
+    {
+        // floor(L c / G) without 64-bit products
+        const int q1 = L1 / G1, r1 = L1 - q1 * G1, q2 = L2 / G2, r2 = L2 - q2 * G2;
+        for (int c = threadIdx.x; c <= G; c += kThreads) {
+            s.start1[c] = c < G1 ? q1 * c + r1 * c / G1 : L1;
+            s.start2[c] = c < G2 ? q2 * c + r2 * c / G2 : L2;
+        }
     }
     __syncthreads();
     const int a1 = s.start1[cta], b1 = s.start1[cta + 1];
     const int a2 = s.start2[cta], b2 = s.start2[cta + 1];
-    const int S1 = g.mt_gu * g.kb_gu, S2 = g.mt_dn * g.kb_dn;   // tiles per expert
 
     if (warp == kConsumerWarps) {
-        // ---- producer: one thread keeps the ring full through both products
-        if (lane == 0) {
-            Ring ring(g.slots);
-            uint32_t it = 0;
-            bool ok = true;
-            for (int X = a1; X < b1 && ok; ++X) {
-                const int i = X / S1;
-                const int r = X - i * S1;
-                const int kb = r % g.kb_gu;
-                const int e = s.expert[i], c0 = s.base[i], cnt = s.base[i + 1] - c0;
-                if (it >= static_cast<uint32_t>(g.slots) &&
-                    !mbar_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
+        // ---- producer warp: keeps the ring full through both products.  Lane
+        // 0 copies the weight tiles, lane c the x slice of token column c.
+        Ring ring(g.slots);
+        int it = 0;
+        bool ok = true;
+        for (int X = a1; X < b1 && ok;) {
+            const int i = X / S1, end = (i + 1) * S1 < b1 ? (i + 1) * S1 : b1;
+            const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
+            int r = X - i * S1, kb = r % g.kb_gu;
+            const uint8_t* w =
+                g.w_gu + (static_cast<size_t>(s.expert[i]) * S1 + r) * kTileBytes;
+            const __nv_bfloat16* x =
+                g.x + (lane < cnt ? static_cast<size_t>(s.tok[c0 + lane]) * g.H : 0);
+            for (; X < end; ++X, w += kTileBytes) {
+                if (it >= g.slots && !mbar_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
                     ok = false;
-                    break;
-                }
+                ok = __all_sync(kFullWarp, ok);
+                if (!ok) break;
                 uint8_t* dst = smem + ring.slot * SLOT;
                 const int left = (g.H - kb * BK) * 2;
                 const uint32_t xb = left < BK * 2 ? left : BK * 2;
-                mbar_arrive_expect_tx(&s.full[ring.slot], kTileBytes + cnt * xb);
-                bulk_load(dst, g.w_gu + (static_cast<size_t>(e) * S1 + r) * kTileBytes, kTileBytes,
-                          &s.full[ring.slot], kEvictFirst);
-                for (int c = 0; c < cnt; ++c)
-                    bulk_load(dst + kTileBytes + c * x_row_bytes<FP8>(),
-                              g.x + static_cast<size_t>(s.tok[c0 + c]) * g.H + kb * BK, xb,
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&s.full[ring.slot], kTileBytes + cnt * xb);
+                    bulk_load(dst, w, kTileBytes, &s.full[ring.slot], kEvictFirst);
+                }
+                __syncwarp();
+                if (lane < cnt)
+                    bulk_load(dst + kTileBytes + lane * x_row_bytes<FP8>(), x + kb * BK, xb,
                               &s.full[ring.slot], kEvictLast);
+                if (++kb == g.kb_gu) kb = 0;
                 ring.next();
                 ++it;
             }
-            for (int X = a2; X < b2 && ok;) {
-                const int i = X / S2, e = s.expert[i];
-                const int a = X - i * S2;
-                const int b = b2 - i * S2 < S2 ? b2 - i * S2 : S2;
-                const uint8_t* w = g.w_dn + static_cast<size_t>(e) * S2 * kTileBytes;
-                const int kb_end = (b - 1) / g.mt_dn + 1;
-                for (int kbA = a / g.mt_dn; kbA < kb_end && ok; kbA += CK) {
-                    const int kbB = kbA + CK < kb_end ? kbA + CK : kb_end;
-                    for (int m = 0; m < g.mt_dn && ok; ++m) {
-                        const int hi = kb_hi(kbB, m, g.mt_dn, b);
-                        for (int kb = kb_lo(kbA, m, g.mt_dn, a); kb < hi; ++kb) {
-                            if (it >= static_cast<uint32_t>(g.slots) &&
-                                !mbar_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
-                                ok = false;
-                                break;
-                            }
+        }
+        for (int X = a2; X < b2 && ok;) {
+            const int i = X / S2;
+            const int a = X - i * S2;
+            const int b = b2 - i * S2 < S2 ? b2 - i * S2 : S2;
+            const uint8_t* w = g.w_dn + static_cast<size_t>(s.expert[i]) * S2 * kTileBytes;
+            const int kb_end = (b - 1) / g.mt_dn + 1;
+            for (int kbA = a / g.mt_dn; kbA < kb_end && ok; kbA += CK) {
+                const int kbB = kbA + CK < kb_end ? kbA + CK : kb_end;
+                for (int m = 0; m < g.mt_dn && ok; ++m) {
+                    const int hi = kb_hi(kbB, m, g.mt_dn, b);
+                    for (int kb = kb_lo(kbA, m, g.mt_dn, a); kb < hi; ++kb) {
+                        if (it >= g.slots &&
+                            !mbar_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
+                            ok = false;
+                        ok = __all_sync(kFullWarp, ok);
+                        if (!ok) break;
+                        if (lane == 0) {
                             mbar_arrive_expect_tx(&s.full[ring.slot], kTileBytes);
                             bulk_load(smem + ring.slot * SLOT,
                                       w + (static_cast<size_t>(m) * g.kb_dn + kb) * kTileBytes,
                                       kTileBytes, &s.full[ring.slot], kEvictFirst);
-                            ring.next();
-                            ++it;
                         }
+                        ring.next();
+                        ++it;
                     }
                 }
-                X = i * S2 + b;
             }
-            if (!ok) {
-                fault(s, g.status);
-                // this CTA's copies in flight land before its memory goes:
-                // the last `slots` of them, or fewer
-                Ring back(g.slots);
-                const uint32_t first = it > static_cast<uint32_t>(g.slots) ? it - g.slots : 0;
-                for (uint32_t j = 0; j < it; ++j) {
-                    if (j >= first) mbar_wait(&s.full[back.slot], back.phase, nullptr, 10000000ull);
-                    back.next();
-                }
+            X = i * S2 + b;
+        }
+        if (!ok) {
+            if (lane == 0) fault(s, g.status);
+            // this CTA's copies in flight (the last `slots`, or fewer) land
+            // before its shared memory goes
+            Ring back(g.slots);
+            for (int j = 0; j < it; ++j) {
+                if (j >= it - g.slots)
+                    mbar_wait(&s.full[back.slot], back.phase, nullptr, 10000000ull);
+                back.next();
             }
         }
     } else {
         // ---- consumers.  After a fault every wait returns at once, and the
         // loops run on to their ends, so all warps meet at the same barriers.
         const int gq = lane >> 2, t = lane & 3;
+        const int grp = warp >> 3, wrow = (warp & 7) * 16 + gq;   // first weight row
         Ring ring(g.slots);
-        // step 1: gate/up partial sums
+        BFrag<FP8> bv[NB];
+        // step 1: gate/up partial sums, one set per group (tiles in turn)
         for (int X = a1; X < b1;) {
             const int r = X / g.kb_gu;                 // row tile over all active experts
             const int i = r / g.mt_gu, m = r - i * g.mt_gu;
             const int end = (r + 1) * g.kb_gu < b1 ? (r + 1) * g.kb_gu : b1;
-            const int cnt = s.base[i + 1] - s.base[i];
+            const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
             const int nb = NB == 1 ? 1 : (cnt + 7) >> 3;
             float acc[NB][4];
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) acc[n][q] = 0.0f;
-            for (; X < end; ++X) {
+            for (; X < end; ++X, ring.next()) {
                 if (!mbar_wait(&s.full[ring.slot], ring.phase, &s.abort)) fault(s, g.status);
+                if (((X - a1) & (kGroups - 1)) != grp) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
+                    continue;
+                }
                 const uint8_t* tile = smem + ring.slot * SLOT;
                 uint4 a[4];
-                load_a<FP8, NB>(a, tile, warp, gq, t);
-                const bool half_row = FP8 && (X - r * g.kb_gu + 1) * BK > g.H;
-                tile_mma<FP8, NB>(acc, a, tile + kTileBytes + gq * x_row_bytes<FP8>(),
-                                  x_row_bytes<FP8>(), t, half_row, nb);
+                load_a(a, tile, wrow, t);
+                load_x<FP8, NB>(bv, tile + kTileBytes + gq * x_row_bytes<FP8>(), t, nb,
+                                (X - r * g.kb_gu + 1) * BK > g.H);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
-                ring.next();
+                tile_mma<FP8, NB>(acc, a, bv, nb);
             }
             // columns of 128 rows; segment (row tile r, CTA c) starts at column
             // sum of the counts before r + c * T: segments follow one another
             // with r or c or both growing, so no two overlap
-            float* p = g.p1 + (static_cast<size_t>(s.base[i]) * g.mt_gu + m * cnt +
-                               static_cast<size_t>(cta) * g.T) * kTileRows;
+            float* p = g.p1 + ((static_cast<size_t>(c0) * g.mt_gu + m * cnt +
+                                static_cast<size_t>(cta) * g.T) * kGroups + grp * cnt) * kTileRows +
+                       wrow;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const int col = n * 8 + 2 * t + (q & 1);
-                    if (col < cnt)
-                        __stcg(p + col * kTileRows + 16 * warp + gq + 8 * (q >> 1), acc[n][q]);
+                    if (col < cnt) __stcg(p + col * kTileRows + 8 * (q >> 1), acc[n][q]);
                 }
         }
         consumer_sync();
-        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[0][0], G)) fault(s, g.status);
+        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[0][0], target[0]))
+            fault(s, g.status);
+        // while the others arrive: the CTAs of each expert's down tiles
+        const float per2 = static_cast<float>(G2) / static_cast<float>(L2);
+        for (int i = threadIdx.x - 32; i >= 0 && i < n_active; i += kConsumers - 32) {
+            const int cf = owner(s.start2, G2, i * S2, per2);
+            s.first2[i] = cf;
+            s.ncta2[i] = owner(s.start2, G2, (i + 1) * S2 - 1, per2) - cf + 1;
+        }
         consumer_sync();
 
         // step 2: h of this CTA's k-blocks, and the down partial sums
@@ -485,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                 su = __ldg(g.scales + e * 3 + 1);
             }
             float* p = g.p2 + (static_cast<size_t>(c0) + static_cast<size_t>(cta) * g.T) *
-                                  g.mt_dn * kTileRows;
+                                  g.mt_dn * kTileRows + wrow;
             for (int kbA = kb_first; kbA < kb_end; kbA += CK) {
                 const int kbB = kbA + CK < kb_end ? kbA + CK : kb_end;
                 const int cols = (kbB - kbA) * BK;
@@ -499,13 +551,15 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                         const int X0 = (i * g.mt_gu + m) * g.kb_gu;
                         const int cf = owner(s.start1, G1, X0, per1);
                         const int cl = owner(s.start1, G1, X0 + g.kb_gu - 1, per1);
-                        const float* q = g.p1 + (static_cast<size_t>(c0) * g.mt_gu + m * cnt + c +
-                                                 static_cast<size_t>(cf) * g.T) * kTileRows + row;
+                        const float* q = g.p1 + ((static_cast<size_t>(c0) * g.mt_gu + m * cnt +
+                                                  static_cast<size_t>(cf) * g.T) * kGroups + c) *
+                                                    kTileRows + row;
+                        const size_t step = static_cast<size_t>(g.T) * kGroups * kTileRows;
+                        const int other = cnt * kTileRows;
                         float gt = 0.0f, up = 0.0f;
-                        for (int cc = cf; cc <= cl; ++cc) {
-                            gt += __ldcg(q);
-                            up += __ldcg(q + 16);
-                            q += static_cast<size_t>(g.T) * kTileRows;
+                        for (int cc = cf; cc <= cl; ++cc, q += step) {
+                            gt += __ldcg(q) + __ldcg(q + other);
+                            up += __ldcg(q + 16) + __ldcg(q + other + 16);
                         }
                         gt *= sg;
                         up *= su;
@@ -524,9 +578,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                     d[BK + jj] = lo;
                 }
                 consumer_sync();
+                int turn = 0;
                 for (int m = 0; m < g.mt_dn; ++m) {
                     const int lo = kb_lo(kbA, m, g.mt_dn, a), hi = kb_hi(kbB, m, g.mt_dn, b);
                     if (lo >= hi) continue;
+                    // the groups take row tiles in turn
+                    if ((turn++ & (kGroups - 1)) != grp) {
+                        for (int kb = lo; kb < hi; ++kb, ring.next()) {
+                            if (!mbar_wait(&s.full[ring.slot], ring.phase, &s.abort))
+                                fault(s, g.status);
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
+                        }
+                        continue;
+                    }
                     float acc[NB][4];
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
@@ -536,17 +601,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                         if (!mbar_wait(&s.full[ring.slot], ring.phase, &s.abort))
                             fault(s, g.status);
                         uint4 w[4];
-                        load_a<FP8, NB>(w, smem + ring.slot * SLOT, warp, gq, t);
+                        load_a(w, smem + ring.slot * SLOT, wrow, t);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
                         ring.next();
                         const uint8_t* hb =
                             hbuf + ((kb - kbA) * NB * 8 + gq) * h_row_bytes<FP8>();
-                        tile_mma<FP8, NB>(acc, w, hb, h_row_bytes<FP8>(), t, false, nb);
-                        tile_mma<FP8, NB>(acc, w, hb + BK * 2, h_row_bytes<FP8>(), t, false, nb);
+                        load_h<FP8, NB>(bv, hb, t, nb);
+                        tile_mma<FP8, NB>(acc, w, bv, nb);
+                        load_h<FP8, NB>(bv, hb + BK * 2, t, nb);
+                        tile_mma<FP8, NB>(acc, w, bv, nb);
                     }
                     // later chunks of the same expert add to the columns that
-                    // the same thread wrote: of several chunks the first has at
+                    // the same CTA wrote: of several chunks the first has at
                     // least four k-blocks, so every row tile is in it
                     const bool first = kbA == kb_first;
                     float* d = p + static_cast<size_t>(m) * cnt * kTileRows;
@@ -556,31 +623,30 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                         for (int q = 0; q < 4; ++q) {
                             const int col = n * 8 + 2 * t + (q & 1);
                             if (col < cnt) {
-                                float* dd = d + col * kTileRows + 16 * warp + gq + 8 * (q >> 1);
+                                float* dd = d + col * kTileRows + 8 * (q >> 1);
                                 __stcg(dd, first ? acc[n][q] : __ldcg(dd) + acc[n][q]);
                             }
                         }
                 }
-                consumer_sync();   // hbuf is free
+                consumer_sync();   // hbuf is free, the chunk's sums are written
             }
             X = i * S2 + b;
         }
-        consumer_sync();
-        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[1][0], G)) fault(s, g.status);
+        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[1][0], target[1]))
+            fault(s, g.status);
         consumer_sync();
 
         // step 3: out[t] = residual[t] + sum over the token's assignments and
         // their CTAs, in ascending order of both.  SPL warps of a CTA share an
         // output's terms (each every SPL-th) when there are few outputs.
-        const int rows32 = g.T * ((g.H + 31) / 32);
+        const int hrows = g.H / 32, rows32 = g.T * hrows;
         int spl = 1;
         while (spl < kConsumerWarps && rows32 * spl * 2 <= G * kConsumerWarps) spl *= 2;
         const int groups = kConsumerWarps / spl;
-        const int sub = warp % spl, grp = warp / spl;
-        const float per2 = static_cast<float>(G2) / static_cast<float>(L2);
-        const int hrows = (g.H + 31) / 32;
+        const int sub = warp % spl;
+        const size_t step = static_cast<size_t>(g.T) * g.mt_dn * kTileRows;
         for (int item0 = cta * groups; item0 < rows32; item0 += G * groups) {
-            const int item = item0 + grp;
+            const int item = item0 + warp / spl;
             const int tk = item / hrows, col = (item - tk * hrows) * 32 + lane;
             float sum = 0.0f;
             if (item < rows32) {
@@ -590,12 +656,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                     const int e = s.ids[tk * g.k + j], i = s.rank[e];
                     const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
                     const int c = __popc(s.mask[e] & ((1u << tk) - 1u));
-                    const int cf = owner(s.start2, G2, i * S2, per2);
-                    const int n = owner(s.start2, G2, (i + 1) * S2 - 1, per2) - cf + 1;
+                    const int cf = s.first2[i], n = s.ncta2[i];
                     const float* q = g.p2 + ((static_cast<size_t>(c0) +
                                               static_cast<size_t>(cf) * g.T) * g.mt_dn +
                                              static_cast<size_t>(m) * cnt + c) * kTileRows + row;
-                    const size_t step = static_cast<size_t>(g.T) * g.mt_dn * kTileRows;
                     float part = 0.0f;
 #pragma unroll 4
                     for (int cc = (sub - cum) & (spl - 1); cc < n; cc += spl) {
@@ -625,10 +689,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                 }
                 consumer_sync();
             }
-            if (sub == 0 && item < rows32 && col < g.H) {
+            if (sub == 0 && item < rows32) {
                 const size_t o = static_cast<size_t>(tk) * g.H + col;
                 if (g.residual) sum += __bfloat162float(g.residual[o]);
                 g.out[o] = __float2bfloat16_rn(sum);
+            }
+        }
+        if (cta == 0) {
+            for (int f = threadIdx.x; f < g.T * g.k; f += kConsumers) {
+                if (g.ids) g.ids[f] = s.ids[f];
+                if (g.w) g.w[f] = s.w[f];
             }
         }
     }
@@ -695,7 +765,7 @@ Sizes sizes(bool fp8, int T, int k, int E, int H, int I, int grid) {
     const PackedGeom geo = packed_geom(fp8, E, H, I);
     const size_t A = static_cast<size_t>(T) * k, col = kTileRows * sizeof(float);
     Sizes z;
-    z.p1 = (A * geo.mt_gu + static_cast<size_t>(grid) * T) * col;
+    z.p1 = (A * geo.mt_gu + static_cast<size_t>(grid) * T) * kGroups * col;
     z.p2 = (A + static_cast<size_t>(grid) * T) * geo.mt_dn * col;
     z.total = sizeof(Header) + z.p1 + z.p2;
     return z;
