@@ -50,7 +50,12 @@ namespace {
 constexpr int kGroups = 2;
 constexpr int kConsumerWarps = 8 * kGroups;
 constexpr int kConsumers = kConsumerWarps * 32;
-constexpr int kThreads = kConsumers + 32;         // and one producer warp
+// ... and one producer warp; e4m3 layers have two more that widen x (see there)
+constexpr int kXWarp0 = kConsumerWarps + 1;
+constexpr int kXWarps = 2;
+template <bool FP8> __host__ __device__ constexpr int threads_for() {
+    return kConsumers + 32 + (FP8 ? kXWarps * 32 : 0);
+}
 constexpr int kMaxSlots = 12;
 constexpr int kSmemBytes = 227 * 1024;
 constexpr uint32_t kMagic = 0x4d6f4465u;
@@ -58,9 +63,11 @@ constexpr uint32_t kMagic = 0x4d6f4465u;
 // h columns held at a time: 512 (8 k-blocks of bf16 tiles, 4 of e4m3 tiles)
 template <bool FP8> __host__ __device__ constexpr int tile_k() { return FP8 ? 128 : 64; }
 template <bool FP8> __host__ __device__ constexpr int chunk_kb() { return FP8 ? 4 : 8; }
-// bytes of one token's row of a k-block of h (hi | lo), plus 16 so that two
-// rows start an odd number of 16-byte banks apart
-template <bool FP8> __host__ __device__ constexpr int h_row_bytes() { return tile_k<FP8>() * 4 + 16; }
+// bytes of one token's row of a k-block of h (bf16: hi | lo; f16 for e4m3),
+// plus 16 so that two rows start an odd number of 16-byte banks apart
+template <bool FP8> __host__ __device__ constexpr int h_row_bytes() {
+    return tile_k<FP8>() * (FP8 ? 2 : 4) + 16;
+}
 // a token's x of one gate/up tile, padded likewise, and a ring slot: a weight
 // tile and the x slices of up to NB * 8 tokens
 template <bool FP8> __host__ __device__ constexpr int x_row_bytes() { return tile_k<FP8>() * 2 + 16; }
@@ -104,6 +111,7 @@ struct Args {
 struct Shared {
     uint64_t full[kMaxSlots];
     uint64_t empty[kMaxSlots];
+    uint64_t ready[kMaxSlots];          // e4m3: the slot's x is widened to f16
     int abort;
     int ids[kDecodeMaxAssign];          // [T][k]
     float w[kDecodeMaxAssign];
@@ -117,7 +125,10 @@ struct Shared {
     int ncta2[kDecodeMaxAssign];        // and how many
     int start1[kMaxCtas + 1];           // first gate/up tile of each CTA
     int start2[kMaxCtas + 1];           // first down tile of each CTA
-    float red[kConsumers];
+    int mod2[kMaxCtas];                 // its row tile
+    float xmul[kDecodeMaxT];            // e4m3: power-of-two scale of a token's x
+    uint32_t hmax[kDecodeMaxT];         // e4m3: largest |h| of a column in the chunk
+    float4 red[kConsumers];
 };
 
 __device__ __forceinline__ void consumer_sync() {
@@ -137,12 +148,42 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 codes (the low 16 bits) as two bf16 values: exact, NaN stays NaN.
-__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t v) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Two e4m3 codes (the low 16 bits) as two f16 values: exact, NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-    return *reinterpret_cast<const uint32_t*>(&b);
+    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+}
+
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// e4m3 layers multiply in f16, whose 11 bits hold every e4m3 and bf16 mantissa;
+// its range is met by a power of two per token that brings the largest finite
+// magnitude (`bits`) to [2^14, 2^15).  What that pushes below f16's normal
+// range is off by 2^-25 there, 2^-39 of the largest: less than an fp32 ulp of
+// the sums it enters.  scale_inv is the exact reciprocal.
+__device__ __forceinline__ float f16_scale(uint32_t bits) {
+    int e = 268 - static_cast<int>(bits >> 23);     // 127 + 14 - (exponent - 127)
+    e = bits == 0 ? 127 : (e > 253 ? 253 : e);
+    return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+__device__ __forceinline__ float scale_inv(float s) {
+    return __uint_as_float((254u << 23) - __float_as_uint(s));
+}
+__device__ __forceinline__ uint32_t finite_mag(float v) {
+    const uint32_t m = __float_as_uint(v) & 0x7fffffffu;
+    return m < 0x7f800000u ? m : 0u;
 }
 
 // The CTA whose range of tiles holds tile X.
@@ -216,16 +257,16 @@ __device__ __forceinline__ void tile_mma(float (&acc)[NB][4], const uint4 (&a)[4
             uint32_t f[8];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                f[4 * q + 0] = e4m3x2_to_bf16x2(lo[2 * p + q] & 0xffffu);
-                f[4 * q + 1] = e4m3x2_to_bf16x2(hi[2 * p + q] & 0xffffu);
-                f[4 * q + 2] = e4m3x2_to_bf16x2(lo[2 * p + q] >> 16);
-                f[4 * q + 3] = e4m3x2_to_bf16x2(hi[2 * p + q] >> 16);
+                f[4 * q + 0] = e4m3x2_to_f16x2(lo[2 * p + q] & 0xffffu);
+                f[4 * q + 1] = e4m3x2_to_f16x2(hi[2 * p + q] & 0xffffu);
+                f[4 * q + 2] = e4m3x2_to_f16x2(lo[2 * p + q] >> 16);
+                f[4 * q + 3] = e4m3x2_to_f16x2(hi[2 * p + q] >> 16);
             }
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 if (n < nb) {
-                    mma_bf16(acc[n], f[0], f[1], f[2], f[3], b[n].v[p].x, b[n].v[p].y);
-                    mma_bf16(acc[n], f[4], f[5], f[6], f[7], b[n].v[p].z, b[n].v[p].w);
+                    mma_f16(acc[n], f[0], f[1], f[2], f[3], b[n].v[p].x, b[n].v[p].y);
+                    mma_f16(acc[n], f[4], f[5], f[6], f[7], b[n].v[p].z, b[n].v[p].w);
                 }
             }
         }
@@ -262,7 +303,7 @@ __device__ __forceinline__ void load_h(BFrag<FP8> (&b)[NB], const uint8_t* hb, i
 
 template <int EPL>
 __device__ __forceinline__ void route_tokens(const Args& g, Shared& s, int warp, int lane) {
-    for (int t = warp; t < g.T; t += kThreads / 32) {
+    for (int t = warp; t < g.T; t += kConsumerWarps) {
         int* ids = s.ids + t * g.k;
         warp_topk<EPL>(g.logits + static_cast<long>(t) * g.E, g.E, g.k, ids, s.w + t * g.k);
         for (int j = lane; j < g.k; j += 32) atomicOr(&s.mask[ids[j]], 1u << t);
@@ -293,8 +334,54 @@ __device__ __forceinline__ int kb_hi(int kbB, int m, int MT, int b) {
     return kbB - ((kbB - 1) * MT + m >= b ? 1 : 0);
 }
 
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// What h's first bf16 value leaves for the second: 16 bits of mantissa
+// together.  An infinite or NaN h is all in the first.
+__device__ __forceinline__ float rest(float h, float hi) {
+    return fabsf(h) < 3.0e38f ? h - hi : 0.0f;
+}
+
+// h of column c of active expert i, columns hc..hc+3: the gate/up partial sums
+// of all CTAs that hold tiles of the row tile, both groups', in ascending order.
+__device__ __forceinline__ float4 h_quad(const Args& g, const Shared& s, int i, int c0, int cnt,
+                                         int c, int hc, int G1, float per1, float sg, float su) {
+    const int m = hc >> 6, l = hc & 63;
+    const int row = 32 * (l >> 4) + (l & 15);
+    const int X0 = (i * g.mt_gu + m) * g.kb_gu;
+    const int cf = owner(s.start1, G1, X0, per1);
+    const float* q = g.p1 + ((static_cast<size_t>(c0) * g.mt_gu + m * cnt +
+                              static_cast<size_t>(cf) * g.T) * kGroups + c) * kTileRows + row;
+    const size_t step = static_cast<size_t>(g.T) * kGroups * kTileRows;
+    const int other = cnt * kTileRows;
+    float4 gt = make_float4(0.f, 0.f, 0.f, 0.f), up = gt;
+    for (int cc = cf;; ++cc, q += step) {
+        const float4 g0 = __ldcg(reinterpret_cast<const float4*>(q));
+        const float4 g1 = __ldcg(reinterpret_cast<const float4*>(q + other));
+        const float4 u0 = __ldcg(reinterpret_cast<const float4*>(q + 16));
+        const float4 u1 = __ldcg(reinterpret_cast<const float4*>(q + other + 16));
+        gt.x += g0.x + g1.x;
+        gt.y += g0.y + g1.y;
+        gt.z += g0.z + g1.z;
+        gt.w += g0.w + g1.w;
+        up.x += u0.x + u1.x;
+        up.y += u0.y + u1.y;
+        up.z += u0.z + u1.z;
+        up.w += u0.w + u1.w;
+        if (s.start1[cc + 1] >= X0 + g.kb_gu) break;
+    }
+    auto act = [&](float a, float b) {
+        a *= sg;
+        return a / (1.0f + expf(-a)) * (b * su);
+    };
+    return make_float4(act(gt.x, up.x), act(gt.y, up.y), act(gt.z, up.z), act(gt.w, up.w));
+}
+
 template <bool FP8, int NB>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
+__global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Args g) {
     extern __shared__ uint8_t dsmem_raw[];
     __shared__ Shared s;
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -303,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
     constexpr int BK = tile_k<FP8>();
     constexpr int CK = chunk_kb<FP8>();
     uint8_t* hbuf = smem + g.slots * SLOT;
+    constexpr int kThreads = threads_for<FP8>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, cta = blockIdx.x;
 
@@ -317,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
         for (int i = 0; i < g.slots; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], kConsumerWarps);
+            mbar_init(&s.ready[i], kXWarps);
         }
         fence_mbar_init();
         s.abort = 0;
@@ -325,10 +414,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
     __syncthreads();
 
     // ---- routing (every CTA, all tokens)
-    if (g.E <= 32) route_tokens<1>(g, s, warp, lane);
-    else if (g.E <= 64) route_tokens<2>(g, s, warp, lane);
-    else if (g.E <= 128) route_tokens<4>(g, s, warp, lane);
-    else route_tokens<8>(g, s, warp, lane);
+    if (warp < kConsumerWarps) {
+        if (g.E <= 32) route_tokens<1>(g, s, warp, lane);
+        else if (g.E <= 64) route_tokens<2>(g, s, warp, lane);
+        else if (g.E <= 128) route_tokens<4>(g, s, warp, lane);
+        else route_tokens<8>(g, s, warp, lane);
+    }
     // a workspace that was never initialised would hang the barriers: every
     // CTA sees the same word and leaves
     if (magic != kMagic) {
@@ -379,8 +470,11 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
         const int q1 = L1 / G1, r1 = L1 - q1 * G1, q2 = L2 / G2, r2 = L2 - q2 * G2;
         for (int c = threadIdx.x; c <= G; c += kThreads) {
             s.start1[c] = c < G1 ? q1 * c + r1 * c / G1 : L1;
-            s.start2[c] = c < G2 ? q2 * c + r2 * c / G2 : L2;
+            const int st = c < G2 ? q2 * c + r2 * c / G2 : L2;
+            s.start2[c] = st;
+            if (c < G) s.mod2[c] = st % g.mt_dn;
         }
+        if (threadIdx.x < kDecodeMaxT) s.hmax[threadIdx.x] = 0;
     }
     __syncthreads();
     const int a1 = s.start1[cta], b1 = s.start1[cta + 1];
@@ -461,6 +555,31 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                 back.next();
             }
         }
+    } else if (FP8 && warp >= kXWarp0) {
+        // ---- e4m3 layers: two warps widen the x slices of the gate/up tiles
+        // in place (bf16 -> scaled f16), every other token each, so that the
+        // sixteen product warps need not each do it
+        asm volatile("bar.sync 2, %0;" ::"n"(kConsumers + kXWarps * 32) : "memory");   // xmul
+        Ring ring(g.slots);
+        for (int X = a1; X < b1; ++X, ring.next()) {
+            const int i = X / S1;
+            if (!mbar_wait(&s.full[ring.slot], ring.phase, &s.abort)) fault(s, g.status);
+            const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
+            uint8_t* xs = smem + ring.slot * SLOT + kTileBytes;
+#pragma unroll 2
+            for (int c = warp - kXWarp0; c < cnt; c += kXWarps) {
+                // 4 values per lane; past H (the last k-block may hold 64 of
+                // its 128) whatever the slot held: not used
+                const float mul = s.xmul[s.tok[c0 + c]];
+                uint2* v = reinterpret_cast<uint2*>(xs + c * x_row_bytes<FP8>()) + lane;
+                const uint2 b = *v;
+                *v = make_uint2(f16x2(bf16_lo(b.x) * mul, bf16_hi(b.x) * mul),
+                                f16x2(bf16_lo(b.y) * mul, bf16_hi(b.y) * mul));
+            }
+            fence_proxy_async_smem();   // a later copy into the slot stays later
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.ready[ring.slot]);
+        }
     } else {
         // ---- consumers.  After a fault every wait returns at once, and the
         // loops run on to their ends, so all warps meet at the same barriers.
@@ -468,6 +587,32 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
         const int grp = warp >> 3, wrow = (warp & 7) * 16 + gq;   // first weight row
         Ring ring(g.slots);
         BFrag<FP8> bv[NB];
+        // while the first tiles are on their way: each token's f16 scale, and
+        // the CTAs of each expert's down tiles
+        if constexpr (FP8) {
+            for (int tk = warp; tk < g.T; tk += kConsumerWarps) {
+                const uint4* xr =
+                    reinterpret_cast<const uint4*>(g.x + static_cast<size_t>(tk) * g.H);
+                uint32_t m = 0;
+#pragma unroll 4
+                for (int v = lane; v < g.H / 8; v += 32) {
+                    const uint4 q = __ldg(xr + v);
+                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        m = max(m, max(finite_mag(bf16_lo(w[j])), finite_mag(bf16_hi(w[j]))));
+                }
+                m = __reduce_max_sync(kFullWarp, m);
+                if (lane == 0) s.xmul[tk] = f16_scale(m);
+            }
+            asm volatile("bar.arrive 2, %0;" ::"n"(kConsumers + kXWarps * 32) : "memory");
+        }
+        const float per2 = static_cast<float>(G2) / static_cast<float>(L2);
+        for (int i = kConsumers - 1 - threadIdx.x; i < n_active; i += kConsumers) {
+            const int cf = owner(s.start2, G2, i * S2, per2);
+            s.first2[i] = cf;
+            s.ncta2[i] = owner(s.start2, G2, (i + 1) * S2 - 1, per2) - cf + 1;
+        }
         // step 1: gate/up partial sums, one set per group (tiles in turn)
         for (int X = a1; X < b1;) {
             const int r = X / g.kb_gu;                 // row tile over all active experts
@@ -481,7 +626,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) acc[n][q] = 0.0f;
             for (; X < end; ++X, ring.next()) {
-                if (!mbar_wait(&s.full[ring.slot], ring.phase, &s.abort)) fault(s, g.status);
+                if (!mbar_wait(FP8 ? &s.ready[ring.slot] : &s.full[ring.slot], ring.phase,
+                               &s.abort))
+                    fault(s, g.status);
                 if (((X - a1) & (kGroups - 1)) != grp) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
@@ -513,13 +660,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
         consumer_sync();
         if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[0][0], target[0]))
             fault(s, g.status);
-        // while the others arrive: the CTAs of each expert's down tiles
-        const float per2 = static_cast<float>(G2) / static_cast<float>(L2);
-        for (int i = threadIdx.x - 32; i >= 0 && i < n_active; i += kConsumers - 32) {
-            const int cf = owner(s.start2, G2, i * S2, per2);
-            s.first2[i] = cf;
-            s.ncta2[i] = owner(s.start2, G2, (i + 1) * S2 - 1, per2) - cf + 1;
-        }
         consumer_sync();
 
         // step 2: h of this CTA's k-blocks, and the down partial sums
@@ -540,42 +680,52 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                                   g.mt_dn * kTileRows + wrow;
             for (int kbA = kb_first; kbA < kb_end; kbA += CK) {
                 const int kbB = kbA + CK < kb_end ? kbA + CK : kb_end;
-                const int cols = (kbB - kbA) * BK;
-                for (int idx = threadIdx.x; idx < cols * cnt; idx += kConsumers) {
-                    const int c = idx / cols, j = idx - c * cols;
-                    const int hc = kbA * BK + j;
-                    float h = 0.0f;
-                    if (hc < g.I) {
-                        const int m = hc >> 6, l = hc & 63;
-                        const int row = 32 * (l >> 4) + (l & 15);
-                        const int X0 = (i * g.mt_gu + m) * g.kb_gu;
-                        const int cf = owner(s.start1, G1, X0, per1);
-                        const int cl = owner(s.start1, G1, X0 + g.kb_gu - 1, per1);
-                        const float* q = g.p1 + ((static_cast<size_t>(c0) * g.mt_gu + m * cnt +
-                                                  static_cast<size_t>(cf) * g.T) * kGroups + c) *
-                                                    kTileRows + row;
-                        const size_t step = static_cast<size_t>(g.T) * kGroups * kTileRows;
-                        const int other = cnt * kTileRows;
-                        float gt = 0.0f, up = 0.0f;
-                        for (int cc = cf; cc <= cl; ++cc, q += step) {
-                            gt += __ldcg(q) + __ldcg(q + other);
-                            up += __ldcg(q + 16) + __ldcg(q + other + 16);
+                // four columns of h a thread and turn (cols is a multiple of 64)
+                const int quads = (kbB - kbA) * (BK / 4);
+                constexpr int TURNS = chunk_kb<FP8>() * BK / 4 * NB * 8 / kConsumers;
+                float4 hq[TURNS];
+#pragma unroll
+                for (int u = 0; u < TURNS; ++u) {
+                    const int idx = threadIdx.x + u * kConsumers;
+                    hq[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (idx < quads * cnt) {
+                        const int c = idx / quads, hc = kbA * BK + (idx - c * quads) * 4;
+                        if (hc < g.I) {
+                            float inv = 1.0f;
+                            if constexpr (FP8) inv = scale_inv(s.xmul[s.tok[c0 + c]]);
+                            hq[u] = h_quad(g, s, i, c0, cnt, c, hc, G1, per1, sg * inv, su * inv);
                         }
-                        gt *= sg;
-                        up *= su;
-                        h = gt / (1.0f + expf(-gt)) * up;
+                        if constexpr (FP8) {
+                            // the largest |h| per column: a warp's quads are of
+                            // one column (quads is a multiple of 32)
+                            const uint32_t m = __reduce_max_sync(
+                                kFullWarp, max(max(finite_mag(hq[u].x), finite_mag(hq[u].y)),
+                                               max(finite_mag(hq[u].z), finite_mag(hq[u].w))));
+                            if (lane == 0) atomicMax(&s.hmax[c], m);
+                        }
                     }
-                    // hi + lo: 16 bits of h's mantissa; an infinite or NaN h is
-                    // all in hi
-                    const __nv_bfloat16 hi = __float2bfloat16_rn(h);
-                    const float rest = h - __bfloat162float(hi);
-                    const __nv_bfloat16 lo =
-                        __float2bfloat16_rn(fabsf(h) < 3.0e38f ? rest : 0.0f);
-                    const int kl = j / BK, jj = j - kl * BK;
-                    __nv_bfloat16* d = reinterpret_cast<__nv_bfloat16*>(
-                        hbuf + (kl * NB * 8 + c) * h_row_bytes<FP8>());
-                    d[jj] = hi;
-                    d[BK + jj] = lo;
+                }
+                if constexpr (FP8) consumer_sync();
+#pragma unroll
+                for (int u = 0; u < TURNS; ++u) {
+                    const int idx = threadIdx.x + u * kConsumers;
+                    if (idx < quads * cnt) {
+                        const int c = idx / quads, j = (idx - c * quads) * 4;
+                        const int kl = j / BK, jj = j - kl * BK;
+                        uint8_t* d = hbuf + (kl * NB * 8 + c) * h_row_bytes<FP8>() + jj * 2;
+                        const float4 h = hq[u];
+                        if constexpr (FP8) {
+                            const float mul = f16_scale(s.hmax[c]);
+                            *reinterpret_cast<uint2*>(d) = make_uint2(
+                                f16x2(h.x * mul, h.y * mul), f16x2(h.z * mul, h.w * mul));
+                        } else {
+                            const uint32_t h0 = bf16x2(h.x, h.y), h1 = bf16x2(h.z, h.w);
+                            *reinterpret_cast<uint2*>(d) = make_uint2(h0, h1);
+                            *reinterpret_cast<uint2*>(d + BK * 2) =
+                                make_uint2(bf16x2(rest(h.x, bf16_lo(h0)), rest(h.y, bf16_hi(h0))),
+                                           bf16x2(rest(h.z, bf16_lo(h1)), rest(h.w, bf16_hi(h1))));
+                        }
+                    }
                 }
                 consumer_sync();
                 int turn = 0;
@@ -609,8 +759,10 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                             hbuf + ((kb - kbA) * NB * 8 + gq) * h_row_bytes<FP8>();
                         load_h<FP8, NB>(bv, hb, t, nb);
                         tile_mma<FP8, NB>(acc, w, bv, nb);
-                        load_h<FP8, NB>(bv, hb + BK * 2, t, nb);
-                        tile_mma<FP8, NB>(acc, w, bv, nb);
+                        if constexpr (!FP8) {
+                            load_h<FP8, NB>(bv, hb + BK * 2, t, nb);
+                            tile_mma<FP8, NB>(acc, w, bv, nb);
+                        }
                     }
                     // later chunks of the same expert add to the columns that
                     // the same CTA wrote: of several chunks the first has at
@@ -624,11 +776,17 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                             const int col = n * 8 + 2 * t + (q & 1);
                             if (col < cnt) {
                                 float* dd = d + col * kTileRows + 8 * (q >> 1);
-                                __stcg(dd, first ? acc[n][q] : __ldcg(dd) + acc[n][q]);
+                                float v = acc[n][q];
+                                if constexpr (FP8) v *= scale_inv(f16_scale(s.hmax[col]));
+                                __stcg(dd, first ? v : __ldcg(dd) + v);
                             }
                         }
                 }
                 consumer_sync();   // hbuf is free, the chunk's sums are written
+                if constexpr (FP8) {
+                    if (threadIdx.x < kDecodeMaxT) s.hmax[threadIdx.x] = 0;
+                    consumer_sync();
+                }
             }
             X = i * S2 + b;
         }
@@ -637,19 +795,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
         consumer_sync();
 
         // step 3: out[t] = residual[t] + sum over the token's assignments and
-        // their CTAs, in ascending order of both.  SPL warps of a CTA share an
-        // output's terms (each every SPL-th) when there are few outputs.
-        const int hrows = g.H / 32, rows32 = g.T * hrows;
+        // their CTAs, in ascending order of both; four columns a thread.  SPL
+        // warps of a CTA share an output's terms (each every SPL-th) when there
+        // are few outputs.
+        const int hquads = g.H / 4, items = g.T * hquads;
         int spl = 1;
-        while (spl < kConsumerWarps && rows32 * spl * 2 <= G * kConsumerWarps) spl *= 2;
-        const int groups = kConsumerWarps / spl;
-        const int sub = warp % spl;
+        while (spl < kConsumerWarps && items * spl * 2 <= G * kConsumers) spl *= 2;
+        const int sub = warp % spl, per_cta = kConsumers / spl;
         const size_t step = static_cast<size_t>(g.T) * g.mt_dn * kTileRows;
-        for (int item0 = cta * groups; item0 < rows32; item0 += G * groups) {
-            const int item = item0 + warp / spl;
-            const int tk = item / hrows, col = (item - tk * hrows) * 32 + lane;
-            float sum = 0.0f;
-            if (item < rows32) {
+        for (int item0 = cta * per_cta; item0 < items; item0 += G * per_cta) {
+            const int item = item0 + warp / spl * 32 + lane;
+            const int tk = item / hquads, col = (item - tk * hquads) * 4;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (item < items) {
                 const int m = col / kTileRows, row = col - m * kTileRows;
                 int cum = 0;
                 for (int j = 0; j < g.k; ++j) {
@@ -660,39 +818,60 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                     const float* q = g.p2 + ((static_cast<size_t>(c0) +
                                               static_cast<size_t>(cf) * g.T) * g.mt_dn +
                                              static_cast<size_t>(m) * cnt + c) * kTileRows + row;
-                    float part = 0.0f;
+                    float4 part = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
                     for (int cc = (sub - cum) & (spl - 1); cc < n; cc += spl) {
-                        // does CTA cf + cc hold a tile of row tile m?
-                        int a = s.start2[cf + cc] - i * S2, b = s.start2[cf + cc + 1] - i * S2;
-                        a = a < 0 ? 0 : a;
-                        b = b > S2 ? S2 : b;
-                        bool has = b - a >= g.mt_dn;
-                        if (!has) {
-                            int d = m - a % g.mt_dn;
-                            if (d < 0) d += g.mt_dn;
-                            has = d < b - a;
+                        // does CTA cf + cc hold a tile of row tile m?  Its range
+                        // within the expert starts at row tile `am` and has
+                        // `len` tiles, the row tile fastest
+                        const int st = s.start2[cf + cc] - i * S2;
+                        const int en = s.start2[cf + cc + 1] - i * S2;
+                        const int am = st < 0 ? 0 : s.mod2[cf + cc];
+                        const int len = (en > S2 ? S2 : en) - (st < 0 ? 0 : st);
+                        int d = m - am;
+                        d += d < 0 ? g.mt_dn : 0;
+                        if (d < len) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(q + cc * step));
+                            part.x += v.x;
+                            part.y += v.y;
+                            part.z += v.z;
+                            part.w += v.w;
                         }
-                        if (has) part += __ldcg(q + cc * step);
                     }
                     cum += n;
                     float wt = s.w[tk * g.k + j];
                     if constexpr (FP8) wt *= __ldg(g.scales + e * 3 + 2);
-                    sum += wt * part;
+                    sum.x += wt * part.x;
+                    sum.y += wt * part.y;
+                    sum.z += wt * part.z;
+                    sum.w += wt * part.w;
                 }
             }
             if (spl > 1) {
                 s.red[threadIdx.x] = sum;
                 consumer_sync();
                 if (sub == 0) {
-                    for (int q = 1; q < spl; ++q) sum += s.red[threadIdx.x + 32 * q];
+                    for (int q = 1; q < spl; ++q) {
+                        const float4 v = s.red[threadIdx.x + 32 * q];
+                        sum.x += v.x;
+                        sum.y += v.y;
+                        sum.z += v.z;
+                        sum.w += v.w;
+                    }
                 }
                 consumer_sync();
             }
-            if (sub == 0 && item < rows32) {
+            if (sub == 0 && item < items) {
                 const size_t o = static_cast<size_t>(tk) * g.H + col;
-                if (g.residual) sum += __bfloat162float(g.residual[o]);
-                g.out[o] = __float2bfloat16_rn(sum);
+                if (g.residual) {
+                    const uint2 r = *reinterpret_cast<const uint2*>(g.residual + o);
+                    sum.x += bf16_lo(r.x);
+                    sum.y += bf16_hi(r.x);
+                    sum.z += bf16_lo(r.y);
+                    sum.w += bf16_hi(r.y);
+                }
+                *reinterpret_cast<uint2*>(g.out + o) =
+                    make_uint2(bf16x2(sum.x, sum.y), bf16x2(sum.z, sum.w));
             }
         }
         if (cta == 0) {
@@ -745,7 +924,7 @@ cudaError_t launch(const Args& a, int grid, cudaStream_t s) {
     if (g.slots < 2) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads_for<FP8>());
     cfg.dynamicSmemBytes = 128 + g.slots * slot_bytes<FP8, NB>() + h_bytes<FP8, NB>();
     cfg.stream = s;
     // cooperative: the blocks wait on one another, so all must be resident

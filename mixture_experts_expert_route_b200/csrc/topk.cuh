@@ -30,7 +30,7 @@ __device__ __forceinline__ float key_value(uint64_t key) {
 
 // Top-k of row[0..E) by one warp (row in global or shared memory).  Each lane
 // keys its E/32 logits once; a selection round is a local max of the lane's
-// keys and a five-step warp max, after which the owning lane clears the
+// keys and two warp-wide reductions, after which the owning lane clears the
 // winner.  The j-th selection (id and logit) is kept in registers of lane
 // j % 32, slot j / 32; the weights are a softmax over the selected logits,
 // summed per lane in ascending j and then across the warp.  ids and w are
@@ -57,12 +57,14 @@ __device__ void warp_topk(const float* row, int E, int k, int32_t* ids, float* w
         uint64_t best = key[0];
 #pragma unroll
         for (int i = 1; i < EPL; ++i) best = key[i] > best ? key[i] : best;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            const uint64_t o = __shfl_xor_sync(kFullWarp, best, off);
-            best = o > best ? o : best;
-        }
-        const int bi = static_cast<int>(0xffffffffu - static_cast<uint32_t>(best));
+        // the largest logit of the warp, then the lowest index that has it
+        // (a cleared key has a zero low word, every other one's is above 0)
+        const uint32_t top = __reduce_max_sync(kFullWarp, static_cast<uint32_t>(best >> 32));
+        const uint32_t low = static_cast<uint32_t>(best);
+        const uint32_t pick = __reduce_max_sync(
+            kFullWarp, static_cast<uint32_t>(best >> 32) == top ? low : 0u);
+        best = (static_cast<uint64_t>(top) << 32) | pick;
+        const int bi = static_cast<int>(0xffffffffu - pick);
         const float bv = key_value(best);
         // selects, not indexed stores, so the arrays stay in registers
         const bool won = (bi & 31) == lane, keep = (j & 31) == lane;
