@@ -43,12 +43,13 @@ namespace moe {
 
 namespace {
 
-// Two groups of eight warps, one warp per 16 weight rows of a tile; the groups
-// take tiles in turn.  Every warp waits for every tile and frees it, its own or
-// not: a warp that went by the other group's tiles unseen could come round to a
-// slot whose barrier is still a phase behind, which a parity cannot tell.
-constexpr int kGroups = 2;
-constexpr int kConsumerWarps = 8 * kGroups;
+// Pairs of warps, one pair per 16 weight rows of a tile; the first takes the
+// even 16-byte pieces of each row's 128 bytes, the second the odd ones, and
+// their sums are added through shared memory at the end of a row tile.  (One
+// warp alone spends ~1800 cycles of latency on a tile that takes 700 to come
+// from HBM.)
+constexpr int kPairs = 8;
+constexpr int kConsumerWarps = 2 * kPairs;
 constexpr int kConsumers = kConsumerWarps * 32;
 // ... and one producer warp; e4m3 layers have two more that widen x (see there)
 constexpr int kXWarp0 = kConsumerWarps + 1;
@@ -76,6 +77,10 @@ template <bool FP8, int NB> __host__ __device__ constexpr int slot_bytes() {
 }
 template <bool FP8, int NB> __host__ __device__ constexpr int h_bytes() {
     return chunk_kb<FP8>() * NB * 8 * h_row_bytes<FP8>();
+}
+// the warp pairs' exchange: [2][pair][NB][32] float4
+template <int NB> __host__ __device__ constexpr int exchange_bytes() {
+    return 2 * kPairs * NB * 32 * 16;
 }
 
 // Workspace header, zeroed but for the magic by moe_decode_workspace_init.
@@ -128,7 +133,6 @@ struct Shared {
     int mod2[kMaxCtas];                 // its row tile
     float xmul[kDecodeMaxT];            // e4m3: power-of-two scale of a token's x
     uint32_t hmax[kDecodeMaxT];         // e4m3: largest |h| of a column in the chunk
-    float4 red[kConsumers];
 };
 
 __device__ __forceinline__ void consumer_sync() {
@@ -200,6 +204,20 @@ __device__ __forceinline__ void fault(Shared& s, int32_t* status) {
     *reinterpret_cast<volatile int*>(&s.abort) = 1;
 }
 
+// The bounded wait of this kernel's rings: the timer is read only now and then
+// (a read takes longer than a tile's products).
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 31u) != 31u) continue;
+        if (*abort) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > kWaitLimitNs) return false;
+    }
+    return true;
+}
+
 // Arrival of this CTA at a grid barrier and the bounded wait until the counter
 // reaches `target`.  Called by one thread, between two consumer_sync.
 __device__ __forceinline__ bool grid_barrier(uint64_t* counter, uint64_t target) {
@@ -214,100 +232,140 @@ __device__ __forceinline__ bool grid_barrier(uint64_t* counter, uint64_t target)
     }
 }
 
-// One tile's products: acc += W[16 rows of this warp] x B[NB * 8 tokens].
-// The K order inside a 128-byte row is permuted the same way for both
-// operands: lane (g, t) takes 16-byte pieces 2t and 2t+1 of its rows, whose
-// swizzled places are conflict-free for a quarter warp.  `b` points at this
-// lane's column g; block n of 8 columns is at +8 rows.
-__device__ __forceinline__ void load_a(uint4 (&a)[4], const uint8_t* tile, int row, int t) {
-    const uint8_t* r = tile + row * kTileRowBytes;
-    const int p0 = ((2 * t) ^ (row & 7)) * 16, p1 = ((2 * t + 1) ^ (row & 7)) * 16;
-    a[0] = lds16(r + p0);
-    a[1] = lds16(r + p1);
-    a[2] = lds16(r + 8 * kTileRowBytes + p0);
-    a[3] = lds16(r + 8 * kTileRowBytes + p1);
+// One tile's products: acc += W[16 rows of this warp] x B[NB * 8 tokens], over
+// this warp's half of the k-block.  The K order inside a 128-byte row is
+// permuted the same way for both operands: lane (g, t) of warp `half` takes
+// 16-byte piece p = 2t + half of its rows, whose swizzled places are
+// conflict-free for a quarter warp.
+__device__ __forceinline__ void load_a(uint4 (&a)[2], const uint8_t* tile, int row, int p) {
+    const uint8_t* r = tile + row * kTileRowBytes + (p ^ (row & 7)) * 16;
+    a[0] = lds16(r);
+    a[1] = lds16(r + 8 * kTileRowBytes);
 }
 
-// One lane's activations for one tile and a block of 8 tokens: 32 (bf16 tiles)
-// or 64 (e4m3 tiles) bytes of its column's row, from 32 t or 64 t.
+// One lane's activations for one tile and a block of 8 tokens: what meets its
+// piece, 16 (bf16) or 32 (f16, for 16 e4m3 codes) bytes of its column's row.
 template <bool FP8> struct BFrag {
-    uint4 v[FP8 ? 4 : 2];
+    uint4 v[FP8 ? 2 : 1];
 };
 
 template <bool FP8, int NB>
-__device__ __forceinline__ void tile_mma(float (&acc)[NB][4], const uint4 (&a)[4],
+__device__ __forceinline__ void load_b(BFrag<FP8> (&b)[NB], const uint8_t* rows, int row_bytes,
+                                       int p, int nb) {
+    constexpr int N = FP8 ? 2 : 1;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+        if (n < nb)
+#pragma unroll
+            for (int q = 0; q < N; ++q)
+                b[n].v[q] = lds16(rows + n * 8 * row_bytes + p * (N * 16) + q * 16);
+}
+
+template <bool FP8, int NB>
+__device__ __forceinline__ void tile_mma(float (&acc)[NB][4], const uint4 (&a)[2],
                                          const BFrag<FP8> (&b)[NB], int nb) {
     if constexpr (!FP8) {
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
             if (n < nb) {
-                const uint4 b0 = b[n].v[0], b1 = b[n].v[1];
-                mma_bf16(acc[n], a[0].x, a[2].x, a[0].y, a[2].y, b0.x, b0.y);
-                mma_bf16(acc[n], a[0].z, a[2].z, a[0].w, a[2].w, b0.z, b0.w);
-                mma_bf16(acc[n], a[1].x, a[3].x, a[1].y, a[3].y, b1.x, b1.y);
-                mma_bf16(acc[n], a[1].z, a[3].z, a[1].w, a[3].w, b1.z, b1.w);
+                const uint4 v = b[n].v[0];
+                mma_bf16(acc[n], a[0].x, a[1].x, a[0].y, a[1].y, v.x, v.y);
+                mma_bf16(acc[n], a[0].z, a[1].z, a[0].w, a[1].w, v.z, v.w);
             }
         }
     } else {
-        // 16 codes per piece: word q of a piece meets 8 bytes of b
-        const uint32_t lo[8] = {a[0].x, a[0].y, a[0].z, a[0].w, a[1].x, a[1].y, a[1].z, a[1].w};
-        const uint32_t hi[8] = {a[2].x, a[2].y, a[2].z, a[2].w, a[3].x, a[3].y, a[3].z, a[3].w};
+        // 16 codes a row: word q meets 8 bytes of b
+        const uint32_t lo[4] = {a[0].x, a[0].y, a[0].z, a[0].w};
+        const uint32_t hi[4] = {a[1].x, a[1].y, a[1].z, a[1].w};
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            uint32_t f[8];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                f[4 * q + 0] = e4m3x2_to_f16x2(lo[2 * p + q] & 0xffffu);
-                f[4 * q + 1] = e4m3x2_to_f16x2(hi[2 * p + q] & 0xffffu);
-                f[4 * q + 2] = e4m3x2_to_f16x2(lo[2 * p + q] >> 16);
-                f[4 * q + 3] = e4m3x2_to_f16x2(hi[2 * p + q] >> 16);
-            }
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t f0 = e4m3x2_to_f16x2(lo[q] & 0xffffu);
+            const uint32_t f1 = e4m3x2_to_f16x2(hi[q] & 0xffffu);
+            const uint32_t f2 = e4m3x2_to_f16x2(lo[q] >> 16);
+            const uint32_t f3 = e4m3x2_to_f16x2(hi[q] >> 16);
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 if (n < nb) {
-                    mma_f16(acc[n], f[0], f[1], f[2], f[3], b[n].v[p].x, b[n].v[p].y);
-                    mma_f16(acc[n], f[4], f[5], f[6], f[7], b[n].v[p].z, b[n].v[p].w);
+                    const uint4 v = b[n].v[q >> 1];
+                    mma_f16(acc[n], f0, f1, f2, f3, (q & 1) ? v.z : v.x, (q & 1) ? v.w : v.y);
                 }
             }
         }
     }
 }
 
-// This lane's columns of a slot's x slices.  Columns past the expert's count
-// are never read back; the last e4m3 k-block may hold 64 of its 128 columns
-// (`half`): the rest meets zero weights and must not be garbage.
-template <bool FP8, int NB>
-__device__ __forceinline__ void load_x(BFrag<FP8> (&b)[NB], const uint8_t* xs, int t, int nb,
-                                       bool half) {
-    constexpr int N = FP8 ? 4 : 2;
+// The two warps of a pair add their sums: on the `v`-th exchange warp v % 2 gets
+// the total (and returns true).  Two buffers: the pair's barrier of exchange
+// v + 1 is behind the reads of exchange v.
+template <int NB>
+__device__ __forceinline__ bool pair_sum(float (&acc)[NB][4], float4* red, int pair, int half,
+                                         int lane, int v) {
+    float4* buf = red + (((v & 1) * kPairs + pair) * NB) * 32 + lane;
+    const bool mine = (v & 1) == half;
+    if (!mine) {
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
-        if (n < nb)
-#pragma unroll
-            for (int p = 0; p < N; ++p) {
-                b[n].v[p] = lds16(xs + n * 8 * x_row_bytes<FP8>() + t * (N * 16) + p * 16);
-                if (FP8 && half && t >= 2) b[n].v[p] = make_uint4(0, 0, 0, 0);
-            }
-}
-
-template <bool FP8, int NB>
-__device__ __forceinline__ void load_h(BFrag<FP8> (&b)[NB], const uint8_t* hb, int t, int nb) {
-    constexpr int N = FP8 ? 4 : 2;
-#pragma unroll
-    for (int n = 0; n < NB; ++n)
-        if (n < nb)
-#pragma unroll
-            for (int p = 0; p < N; ++p)
-                b[n].v[p] = lds16(hb + n * 8 * h_row_bytes<FP8>() + t * (N * 16) + p * 16);
-}
-
-template <int EPL>
-__device__ __forceinline__ void route_tokens(const Args& g, Shared& s, int warp, int lane) {
-    for (int t = warp; t < g.T; t += kConsumerWarps) {
-        int* ids = s.ids + t * g.k;
-        warp_topk<EPL>(g.logits + static_cast<long>(t) * g.E, g.E, g.k, ids, s.w + t * g.k);
-        for (int j = lane; j < g.k; j += 32) atomicOr(&s.mask[ids[j]], 1u << t);
+        for (int n = 0; n < NB; ++n)
+            buf[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
     }
+    asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
+    if (mine) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            const float4 o = buf[n * 32];
+            acc[n][0] += o.x;
+            acc[n][1] += o.y;
+            acc[n][2] += o.z;
+            acc[n][3] += o.w;
+        }
+    }
+    return mine;
+}
+
+// Each token's top-k by counting: an expert's place is the number of keys above
+// its own (the keys are distinct), one thread per (token, expert), so that all k
+// selections take one pass.  The same order and, below, the same sums as
+// warp_topk: ids and weights are its bits.
+__device__ __forceinline__ void route_tokens(const Args& g, Shared& s, uint64_t* keys, int warp,
+                                             int lane) {
+    const int Ep = (g.E + 31) & ~31;
+    for (int f = threadIdx.x; f < g.T * Ep; f += kConsumers) {
+        const int t = f / Ep, e = f - t * Ep;
+        keys[f] = e < g.E ? select_key(__ldg(g.logits + t * g.E + e), e) : 0ull;
+    }
+    consumer_sync();
+    for (int f = threadIdx.x; f < g.T * Ep; f += kConsumers) {
+        const int t = f / Ep, e = f - t * Ep;
+        if (e >= g.E) continue;
+        const uint64_t own = keys[f];
+        const ulonglong2* row = reinterpret_cast<const ulonglong2*>(keys + t * Ep);
+        int place = 0;
+#pragma unroll 8
+        for (int i = 0; i < Ep / 2; ++i) {
+            const ulonglong2 v = row[i];
+            place += (v.x > own) + (v.y > own);
+        }
+        if (place < g.k) {
+            s.ids[t * g.k + place] = e;
+            s.w[t * g.k + place] = key_value(own);
+            atomicOr(&s.mask[e], 1u << t);
+        }
+    }
+    consumer_sync();
+    for (int t = warp; t < g.T; t += kConsumerWarps) {
+        float* w = s.w + t * g.k;
+        const float m = w[0];
+        __syncwarp();
+        float z = 0.0f;
+        for (int j = lane; j < g.k; j += 32) {
+            const float v = expf(w[j] - m);
+            w[j] = v;
+            z += v;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(kFullWarp, z, off);
+        for (int j = lane; j < g.k; j += 32) w[j] = w[j] / z;
+    }
+    fence_proxy_async_smem();   // the ring's copies come after the keys
 }
 
 // Ring position shared by the producer's and the consumers' loops.
@@ -339,6 +397,10 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+    return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
 // What h's first bf16 value leaves for the second: 16 bits of mantissa
 // together.  An infinite or NaN h is all in the first.
 __device__ __forceinline__ float rest(float h, float hi) {
@@ -346,7 +408,7 @@ __device__ __forceinline__ float rest(float h, float hi) {
 }
 
 // h of column c of active expert i, columns hc..hc+3: the gate/up partial sums
-// of all CTAs that hold tiles of the row tile, both groups', in ascending order.
+// of all CTAs that hold tiles of the row tile, in ascending order.
 __device__ __forceinline__ float4 h_quad(const Args& g, const Shared& s, int i, int c0, int cnt,
                                          int c, int hc, int G1, float per1, float sg, float su) {
     const int m = hc >> 6, l = hc & 63;
@@ -354,23 +416,20 @@ __device__ __forceinline__ float4 h_quad(const Args& g, const Shared& s, int i, 
     const int X0 = (i * g.mt_gu + m) * g.kb_gu;
     const int cf = owner(s.start1, G1, X0, per1);
     const float* q = g.p1 + ((static_cast<size_t>(c0) * g.mt_gu + m * cnt +
-                              static_cast<size_t>(cf) * g.T) * kGroups + c) * kTileRows + row;
-    const size_t step = static_cast<size_t>(g.T) * kGroups * kTileRows;
-    const int other = cnt * kTileRows;
+                              static_cast<size_t>(cf) * g.T) + c) * kTileRows + row;
+    const size_t step = static_cast<size_t>(g.T) * kTileRows;
     float4 gt = make_float4(0.f, 0.f, 0.f, 0.f), up = gt;
     for (int cc = cf;; ++cc, q += step) {
         const float4 g0 = __ldcg(reinterpret_cast<const float4*>(q));
-        const float4 g1 = __ldcg(reinterpret_cast<const float4*>(q + other));
         const float4 u0 = __ldcg(reinterpret_cast<const float4*>(q + 16));
-        const float4 u1 = __ldcg(reinterpret_cast<const float4*>(q + other + 16));
-        gt.x += g0.x + g1.x;
-        gt.y += g0.y + g1.y;
-        gt.z += g0.z + g1.z;
-        gt.w += g0.w + g1.w;
-        up.x += u0.x + u1.x;
-        up.y += u0.y + u1.y;
-        up.z += u0.z + u1.z;
-        up.w += u0.w + u1.w;
+        gt.x += g0.x;
+        gt.y += g0.y;
+        gt.z += g0.z;
+        gt.w += g0.w;
+        up.x += u0.x;
+        up.y += u0.y;
+        up.z += u0.z;
+        up.w += u0.w;
         if (s.start1[cc + 1] >= X0 + g.kb_gu) break;
     }
     auto act = [&](float a, float b) {
@@ -390,6 +449,7 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
     constexpr int BK = tile_k<FP8>();
     constexpr int CK = chunk_kb<FP8>();
     uint8_t* hbuf = smem + g.slots * SLOT;
+    float4* exch = reinterpret_cast<float4*>(hbuf + h_bytes<FP8, NB>());
     constexpr int kThreads = threads_for<FP8>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, cta = blockIdx.x;
@@ -413,12 +473,26 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
     for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) s.mask[e] = 0;
     __syncthreads();
 
-    // ---- routing (every CTA, all tokens)
+    // ---- routing (every CTA, all tokens); keys in the ring's memory, no copy
+    // is under way yet
     if (warp < kConsumerWarps) {
-        if (g.E <= 32) route_tokens<1>(g, s, warp, lane);
-        else if (g.E <= 64) route_tokens<2>(g, s, warp, lane);
-        else if (g.E <= 128) route_tokens<4>(g, s, warp, lane);
-        else route_tokens<8>(g, s, warp, lane);
+        route_tokens(g, s, reinterpret_cast<uint64_t*>(smem), warp, lane);
+    } else if (FP8 && warp >= kXWarp0) {
+        // meanwhile, for e4m3 layers: each token's f16 scale
+        for (int tk = warp - kXWarp0; tk < g.T; tk += kXWarps) {
+            const uint4* xr = reinterpret_cast<const uint4*>(g.x + static_cast<size_t>(tk) * g.H);
+            uint32_t m = 0;
+#pragma unroll 8
+            for (int v = lane; v < g.H / 8; v += 32) {
+                const uint4 q = __ldg(xr + v);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    m = max(m, max(finite_mag(bf16_lo(w[j])), finite_mag(bf16_hi(w[j]))));
+            }
+            m = __reduce_max_sync(kFullWarp, m);
+            if (lane == 0) s.xmul[tk] = f16_scale(m);
+        }
     }
     // a workspace that was never initialised would hang the barriers: every
     // CTA sees the same word and leaves
@@ -495,7 +569,7 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
             const __nv_bfloat16* x =
                 g.x + (lane < cnt ? static_cast<size_t>(s.tok[c0 + lane]) * g.H : 0);
             for (; X < end; ++X, w += kTileBytes) {
-                if (it >= g.slots && !mbar_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
+                if (it >= g.slots && !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
                     ok = false;
                 ok = __all_sync(kFullWarp, ok);
                 if (!ok) break;
@@ -527,7 +601,7 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                     const int hi = kb_hi(kbB, m, g.mt_dn, b);
                     for (int kb = kb_lo(kbA, m, g.mt_dn, a); kb < hi; ++kb) {
                         if (it >= g.slots &&
-                            !mbar_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
+                            !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
                             ok = false;
                         ok = __all_sync(kFullWarp, ok);
                         if (!ok) break;
@@ -559,11 +633,10 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
         // ---- e4m3 layers: two warps widen the x slices of the gate/up tiles
         // in place (bf16 -> scaled f16), every other token each, so that the
         // sixteen product warps need not each do it
-        asm volatile("bar.sync 2, %0;" ::"n"(kConsumers + kXWarps * 32) : "memory");   // xmul
         Ring ring(g.slots);
         for (int X = a1; X < b1; ++X, ring.next()) {
             const int i = X / S1;
-            if (!mbar_wait(&s.full[ring.slot], ring.phase, &s.abort)) fault(s, g.status);
+            if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort)) fault(s, g.status);
             const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
             uint8_t* xs = smem + ring.slot * SLOT + kTileBytes;
 #pragma unroll 2
@@ -584,36 +657,21 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
         // ---- consumers.  After a fault every wait returns at once, and the
         // loops run on to their ends, so all warps meet at the same barriers.
         const int gq = lane >> 2, t = lane & 3;
-        const int grp = warp >> 3, wrow = (warp & 7) * 16 + gq;   // first weight row
+        const int pair = warp & (kPairs - 1), half = warp >> 3;
+        const int wrow = pair * 16 + gq;               // first weight row
+        const int piece = 2 * t + half;
+        int exchanges = 0;
         Ring ring(g.slots);
         BFrag<FP8> bv[NB];
-        // while the first tiles are on their way: each token's f16 scale, and
-        // the CTAs of each expert's down tiles
-        if constexpr (FP8) {
-            for (int tk = warp; tk < g.T; tk += kConsumerWarps) {
-                const uint4* xr =
-                    reinterpret_cast<const uint4*>(g.x + static_cast<size_t>(tk) * g.H);
-                uint32_t m = 0;
-#pragma unroll 4
-                for (int v = lane; v < g.H / 8; v += 32) {
-                    const uint4 q = __ldg(xr + v);
-                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        m = max(m, max(finite_mag(bf16_lo(w[j])), finite_mag(bf16_hi(w[j]))));
-                }
-                m = __reduce_max_sync(kFullWarp, m);
-                if (lane == 0) s.xmul[tk] = f16_scale(m);
-            }
-            asm volatile("bar.arrive 2, %0;" ::"n"(kConsumers + kXWarps * 32) : "memory");
-        }
+        // while the first tiles are on their way: the CTAs of each expert's down
+        // tiles
         const float per2 = static_cast<float>(G2) / static_cast<float>(L2);
         for (int i = kConsumers - 1 - threadIdx.x; i < n_active; i += kConsumers) {
             const int cf = owner(s.start2, G2, i * S2, per2);
             s.first2[i] = cf;
             s.ncta2[i] = owner(s.start2, G2, (i + 1) * S2 - 1, per2) - cf + 1;
         }
-        // step 1: gate/up partial sums, one set per group (tiles in turn)
+        // step 1: gate/up partial sums
         for (int X = a1; X < b1;) {
             const int r = X / g.kb_gu;                 // row tile over all active experts
             const int i = r / g.mt_gu, m = r - i * g.mt_gu;
@@ -625,30 +683,32 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
             for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) acc[n][q] = 0.0f;
-            for (; X < end; ++X, ring.next()) {
-                if (!mbar_wait(FP8 ? &s.ready[ring.slot] : &s.full[ring.slot], ring.phase,
+            for (; X < end; ++X) {
+                if (!ring_wait(FP8 ? &s.ready[ring.slot] : &s.full[ring.slot], ring.phase,
                                &s.abort))
                     fault(s, g.status);
-                if (((X - a1) & (kGroups - 1)) != grp) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
-                    continue;
-                }
                 const uint8_t* tile = smem + ring.slot * SLOT;
-                uint4 a[4];
-                load_a(a, tile, wrow, t);
-                load_x<FP8, NB>(bv, tile + kTileBytes + gq * x_row_bytes<FP8>(), t, nb,
-                                (X - r * g.kb_gu + 1) * BK > g.H);
+                uint4 a[2];
+                load_a(a, tile, wrow, piece);
+                load_b<FP8, NB>(bv, tile + kTileBytes + gq * x_row_bytes<FP8>(),
+                                x_row_bytes<FP8>(), piece, nb);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
+                ring.next();
+                // the last e4m3 k-block may hold 64 of its 128 columns: the rest
+                // meets zero weights and must not be garbage
+                if (FP8 && (X - r * g.kb_gu + 1) * BK > g.H && t >= 2) {
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) bv[n] = BFrag<FP8>{};
+                }
                 tile_mma<FP8, NB>(acc, a, bv, nb);
             }
+            if (!pair_sum<NB>(acc, exch, pair, half, lane, exchanges++)) continue;
             // columns of 128 rows; segment (row tile r, CTA c) starts at column
             // sum of the counts before r + c * T: segments follow one another
             // with r or c or both growing, so no two overlap
-            float* p = g.p1 + ((static_cast<size_t>(c0) * g.mt_gu + m * cnt +
-                                static_cast<size_t>(cta) * g.T) * kGroups + grp * cnt) * kTileRows +
-                       wrow;
+            float* p = g.p1 + (static_cast<size_t>(c0) * g.mt_gu + m * cnt +
+                               static_cast<size_t>(cta) * g.T) * kTileRows + wrow;
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -728,46 +788,43 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                     }
                 }
                 consumer_sync();
-                int turn = 0;
+                // this lane's columns and their unscaling
+                float inv[NB][2];
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        inv[n][q] = FP8 ? scale_inv(f16_scale(s.hmax[n * 8 + 2 * t + q])) : 1.0f;
+                // later chunks of the same expert add to the columns that the
+                // same pair wrote: of several chunks the first has at least four
+                // k-blocks, so every row tile is in it
+                const bool first = kbA == kb_first;
                 for (int m = 0; m < g.mt_dn; ++m) {
                     const int lo = kb_lo(kbA, m, g.mt_dn, a), hi = kb_hi(kbB, m, g.mt_dn, b);
                     if (lo >= hi) continue;
-                    // the groups take row tiles in turn
-                    if ((turn++ & (kGroups - 1)) != grp) {
-                        for (int kb = lo; kb < hi; ++kb, ring.next()) {
-                            if (!mbar_wait(&s.full[ring.slot], ring.phase, &s.abort))
-                                fault(s, g.status);
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
-                        }
-                        continue;
-                    }
                     float acc[NB][4];
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
 #pragma unroll
                         for (int q = 0; q < 4; ++q) acc[n][q] = 0.0f;
                     for (int kb = lo; kb < hi; ++kb) {
-                        if (!mbar_wait(&s.full[ring.slot], ring.phase, &s.abort))
+                        if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort))
                             fault(s, g.status);
-                        uint4 w[4];
-                        load_a(w, smem + ring.slot * SLOT, wrow, t);
+                        uint4 w[2];
+                        load_a(w, smem + ring.slot * SLOT, wrow, piece);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
                         ring.next();
                         const uint8_t* hb =
                             hbuf + ((kb - kbA) * NB * 8 + gq) * h_row_bytes<FP8>();
-                        load_h<FP8, NB>(bv, hb, t, nb);
+                        load_b<FP8, NB>(bv, hb, h_row_bytes<FP8>(), piece, nb);
                         tile_mma<FP8, NB>(acc, w, bv, nb);
                         if constexpr (!FP8) {
-                            load_h<FP8, NB>(bv, hb + BK * 2, t, nb);
+                            load_b<FP8, NB>(bv, hb + BK * 2, h_row_bytes<FP8>(), piece, nb);
                             tile_mma<FP8, NB>(acc, w, bv, nb);
                         }
                     }
-                    // later chunks of the same expert add to the columns that
-                    // the same CTA wrote: of several chunks the first has at
-                    // least four k-blocks, so every row tile is in it
-                    const bool first = kbA == kb_first;
+                    if (!pair_sum<NB>(acc, exch, pair, half, lane, exchanges++)) continue;
                     float* d = p + static_cast<size_t>(m) * cnt * kTileRows;
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
@@ -776,8 +833,7 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                             const int col = n * 8 + 2 * t + (q & 1);
                             if (col < cnt) {
                                 float* dd = d + col * kTileRows + 8 * (q >> 1);
-                                float v = acc[n][q];
-                                if constexpr (FP8) v *= scale_inv(f16_scale(s.hmax[col]));
+                                const float v = acc[n][q] * inv[n][q & 1];
                                 __stcg(dd, first ? v : __ldcg(dd) + v);
                             }
                         }
@@ -795,22 +851,27 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
         consumer_sync();
 
         // step 3: out[t] = residual[t] + sum over the token's assignments and
-        // their CTAs, in ascending order of both; four columns a thread.  SPL
-        // warps of a CTA share an output's terms (each every SPL-th) when there
-        // are few outputs.
+        // their CTAs; four columns a thread.  When there are few outputs `spl`
+        // threads share one's terms: `sj` of them the assignments, sc = spl / sj
+        // the CTAs of each; lanes first (ls, so that 8 lanes still read 128
+        // consecutive bytes), then warps.
         const int hquads = g.H / 4, items = g.T * hquads;
         int spl = 1;
-        while (spl < kConsumerWarps && items * spl * 2 <= G * kConsumers) spl *= 2;
-        const int sub = warp % spl, per_cta = kConsumers / spl;
+        while (spl < 4 * kConsumerWarps && items * spl * 2 <= G * kConsumers) spl *= 2;
+        int sj = 1;
+        while (sj * 2 <= spl && sj * 2 <= g.k) sj *= 2;
+        const int sc = spl / sj, ls = spl < 4 ? spl : 4, lw = 32 / ls, ws = spl / ls;
+        const int sub = (warp % ws) * ls + lane / lw, per_cta = kConsumers / spl;
+        const int jsub = sub % sj, csub = sub / sj;
+        float4* red = reinterpret_cast<float4*>(smem);   // the ring has run dry
         const size_t step = static_cast<size_t>(g.T) * g.mt_dn * kTileRows;
         for (int item0 = cta * per_cta; item0 < items; item0 += G * per_cta) {
-            const int item = item0 + warp / spl * 32 + lane;
+            const int item = item0 + warp / ws * lw + lane % lw;
             const int tk = item / hquads, col = (item - tk * hquads) * 4;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             if (item < items) {
                 const int m = col / kTileRows, row = col - m * kTileRows;
-                int cum = 0;
-                for (int j = 0; j < g.k; ++j) {
+                for (int j = jsub; j < g.k; j += sj) {
                     const int e = s.ids[tk * g.k + j], i = s.rank[e];
                     const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
                     const int c = __popc(s.mask[e] & ((1u << tk) - 1u));
@@ -820,7 +881,7 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                                              static_cast<size_t>(m) * cnt + c) * kTileRows + row;
                     float4 part = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-                    for (int cc = (sub - cum) & (spl - 1); cc < n; cc += spl) {
+                    for (int cc = csub; cc < n; cc += sc) {
                         // does CTA cf + cc hold a tile of row tile m?  Its range
                         // within the expert starts at row tile `am` and has
                         // `len` tiles, the row tile fastest
@@ -830,15 +891,9 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                         const int len = (en > S2 ? S2 : en) - (st < 0 ? 0 : st);
                         int d = m - am;
                         d += d < 0 ? g.mt_dn : 0;
-                        if (d < len) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(q + cc * step));
-                            part.x += v.x;
-                            part.y += v.y;
-                            part.z += v.z;
-                            part.w += v.w;
-                        }
+                        if (d < len)
+                            part = add4(part, __ldcg(reinterpret_cast<const float4*>(q + cc * step)));
                     }
-                    cum += n;
                     float wt = s.w[tk * g.k + j];
                     if constexpr (FP8) wt *= __ldg(g.scales + e * 3 + 2);
                     sum.x += wt * part.x;
@@ -847,28 +902,26 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                     sum.w += wt * part.w;
                 }
             }
-            if (spl > 1) {
-                s.red[threadIdx.x] = sum;
+            for (int off = lw; off < 32; off *= 2) {
+                const float4 o = make_float4(__shfl_xor_sync(kFullWarp, sum.x, off),
+                                             __shfl_xor_sync(kFullWarp, sum.y, off),
+                                             __shfl_xor_sync(kFullWarp, sum.z, off),
+                                             __shfl_xor_sync(kFullWarp, sum.w, off));
+                sum = add4(sum, o);
+            }
+            if (ws > 1) {
+                red[threadIdx.x] = sum;
                 consumer_sync();
-                if (sub == 0) {
-                    for (int q = 1; q < spl; ++q) {
-                        const float4 v = s.red[threadIdx.x + 32 * q];
-                        sum.x += v.x;
-                        sum.y += v.y;
-                        sum.z += v.z;
-                        sum.w += v.w;
-                    }
-                }
+                if (sub == 0)
+                    for (int q = 1; q < ws; ++q) sum = add4(sum, red[threadIdx.x + 32 * q]);
                 consumer_sync();
             }
             if (sub == 0 && item < items) {
                 const size_t o = static_cast<size_t>(tk) * g.H + col;
                 if (g.residual) {
                     const uint2 r = *reinterpret_cast<const uint2*>(g.residual + o);
-                    sum.x += bf16_lo(r.x);
-                    sum.y += bf16_hi(r.x);
-                    sum.z += bf16_lo(r.y);
-                    sum.w += bf16_hi(r.y);
+                    sum = add4(sum, make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y),
+                                                bf16_hi(r.y)));
                 }
                 *reinterpret_cast<uint2*>(g.out + o) =
                     make_uint2(bf16x2(sum.x, sum.y), bf16x2(sum.z, sum.w));
@@ -919,13 +972,14 @@ cudaError_t launch(const Args& a, int grid, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     constexpr int dyn = kDynSmemMax;
     Args g = a;
-    int slots = (dyn - 128 - h_bytes<FP8, NB>()) / slot_bytes<FP8, NB>();
+    constexpr int rest = 128 + h_bytes<FP8, NB>() + exchange_bytes<NB>();
+    int slots = (dyn - rest) / slot_bytes<FP8, NB>();
     g.slots = slots > kMaxSlots ? kMaxSlots : slots;
     if (g.slots < 2) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads_for<FP8>());
-    cfg.dynamicSmemBytes = 128 + g.slots * slot_bytes<FP8, NB>() + h_bytes<FP8, NB>();
+    cfg.dynamicSmemBytes = rest + g.slots * slot_bytes<FP8, NB>();
     cfg.stream = s;
     // cooperative: the blocks wait on one another, so all must be resident
     cudaLaunchAttribute at[1];
@@ -944,7 +998,7 @@ Sizes sizes(bool fp8, int T, int k, int E, int H, int I, int grid) {
     const PackedGeom geo = packed_geom(fp8, E, H, I);
     const size_t A = static_cast<size_t>(T) * k, col = kTileRows * sizeof(float);
     Sizes z;
-    z.p1 = (A * geo.mt_gu + static_cast<size_t>(grid) * T) * kGroups * col;
+    z.p1 = (A * geo.mt_gu + static_cast<size_t>(grid) * T) * col;
     z.p2 = (A + static_cast<size_t>(grid) * T) * geo.mt_dn * col;
     z.total = sizeof(Header) + z.p1 + z.p2;
     return z;
