@@ -23,13 +23,17 @@
 //     routing weights, over all CTAs, the residual added and rounded once.
 //
 // The weights arrive as 16 KB tiles (the packed layout of the grouped GEMMs)
-// through a ring of bulk copies that one thread keeps full across the
-// barriers: while the CTAs exchange partial sums the first down tiles land.
-// The products are m16n8k16 warp MMAs, weight rows in the M slot, tokens in N:
-// at 1 to 16 tokens the tensor work is a few percent of the stream's time, and
-// the register path lets e4m3 weights be widened to bf16 exactly (the
-// activations stay bf16; nothing is quantised) and h enter as the sum of two
-// bf16 values (16 bits of mantissa), so the only coarse rounding is out's.
+// through a ring of bulk copies that one warp keeps full across the barriers:
+// while the CTAs exchange partial sums the first down tiles land.  The products
+// are m16n8k16 warp MMAs with the tokens in the M slot (16 of them at most) and
+// 8 weight rows of a tile per warp in N: at these sizes the tensor work is a few
+// percent of the stream's time, one warp reads a tile row whole, and the
+// register path lets e4m3 weights be widened exactly (nothing is quantised) and
+// h enter with more bits than bf16's 8, so the only coarse rounding is out's.
+// One tile is a chain of some 500 cycles of latency (barrier, loads, products),
+// so four groups of four warps take the tiles in turn, each with four
+// independent products a warp; sixteen warps on each tile left the stream at
+// 5.8 TB/s and every down tile of a small layer at 1000 cycles.
 //
 // All sums are in a fixed order: results do not depend on timing.
 #include <cstdint>
@@ -43,21 +47,19 @@ namespace moe {
 
 namespace {
 
-// Pairs of warps, one pair per 16 weight rows of a tile; the first takes the
-// even 16-byte pieces of each row's 128 bytes, the second the odd ones, and
-// their sums are added through shared memory at the end of a row tile.  (One
-// warp alone spends ~1800 cycles of latency on a tile that takes 700 to come
-// from HBM.)
-constexpr int kPairs = 8;
-constexpr int kConsumerWarps = 2 * kPairs;
+constexpr int kGroups = 4;
+constexpr int kGroupWarps = 4;          // 32 weight rows of a tile each
+constexpr int kConsumerWarps = kGroups * kGroupWarps;
 constexpr int kConsumers = kConsumerWarps * 32;
-// ... and one producer warp; e4m3 layers have two more that widen x (see there)
-constexpr int kXWarp0 = kConsumerWarps + 1;
-constexpr int kXWarps = 2;
+// ... a warp that copies the weight tiles, one that copies the gate/up tiles'
+// x slices (together the copies took longer than a tile's time) and, for e4m3
+// layers, two that widen those slices
+constexpr int kWeightWarp = kConsumerWarps, kXWarp = kConsumerWarps + 1;
+constexpr int kWidenWarp0 = kConsumerWarps + 2, kWidenWarps = 2;
 template <bool FP8> __host__ __device__ constexpr int threads_for() {
-    return kConsumers + 32 + (FP8 ? kXWarps * 32 : 0);
+    return (kConsumerWarps + 2 + (FP8 ? kWidenWarps : 0)) * 32;
 }
-constexpr int kMaxSlots = 12;
+constexpr int kMaxSlots = 12;           // a multiple of the groups: a slot stays with one
 constexpr int kSmemBytes = 227 * 1024;
 constexpr uint32_t kMagic = 0x4d6f4465u;
 
@@ -70,17 +72,15 @@ template <bool FP8> __host__ __device__ constexpr int h_row_bytes() {
     return tile_k<FP8>() * (FP8 ? 2 : 4) + 16;
 }
 // a token's x of one gate/up tile, padded likewise, and a ring slot: a weight
-// tile and the x slices of up to NB * 8 tokens
+// tile and the x slices of the tokens
 template <bool FP8> __host__ __device__ constexpr int x_row_bytes() { return tile_k<FP8>() * 2 + 16; }
-template <bool FP8, int NB> __host__ __device__ constexpr int slot_bytes() {
-    return kTileBytes + NB * 8 * x_row_bytes<FP8>();
+template <bool FP8> __host__ __device__ constexpr int slot_bytes(int T) {
+    return kTileBytes + T * x_row_bytes<FP8>();
 }
-template <bool FP8, int NB> __host__ __device__ constexpr int h_bytes() {
-    return chunk_kb<FP8>() * NB * 8 * h_row_bytes<FP8>();
-}
-// the warp pairs' exchange: [2][pair][NB][32] float4
-template <int NB> __host__ __device__ constexpr int exchange_bytes() {
-    return 2 * kPairs * NB * 32 * 16;
+// the h buffer, before it the groups' exchange of gate/up sums [group][T][128]
+template <bool FP8> __host__ __device__ constexpr int h_bytes(int T) {
+    const int h = chunk_kb<FP8>() * T * h_row_bytes<FP8>(), x = kGroups * T * kTileRows * 4;
+    return h > x ? h : x;
 }
 
 // Workspace header, zeroed but for the magic by moe_decode_workspace_init.
@@ -161,10 +161,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Two e4m3 codes (the low 16 bits) as two f16 values: exact, NaN stays NaN.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t v) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(v), __NV_E4M3);
-    return static_cast<uint32_t>(h.x) | (static_cast<uint32_t>(h.y) << 16);
+// Four e4m3 codes as two pairs of f16 values: exact, NaN stays NaN.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}\n"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
 }
 
 __device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
@@ -232,122 +236,132 @@ __device__ __forceinline__ bool grid_barrier(uint64_t* counter, uint64_t target)
     }
 }
 
-// One tile's products: acc += W[16 rows of this warp] x B[NB * 8 tokens], over
-// this warp's half of the k-block.  The K order inside a 128-byte row is
-// permuted the same way for both operands: lane (g, t) of warp `half` takes
-// 16-byte piece p = 2t + half of its rows, whose swizzled places are
-// conflict-free for a quarter warp.
-__device__ __forceinline__ void load_a(uint4 (&a)[2], const uint8_t* tile, int row, int p) {
-    const uint8_t* r = tile + row * kTileRowBytes + (p ^ (row & 7)) * 16;
-    a[0] = lds16(r);
-    a[1] = lds16(r + 8 * kTileRowBytes);
-}
-
-// One lane's activations for one tile and a block of 8 tokens: what meets its
-// piece, 16 (bf16) or 32 (f16, for 16 e4m3 codes) bytes of its column's row.
-template <bool FP8> struct BFrag {
-    uint4 v[FP8 ? 2 : 1];
+// One lane's part of a tile: D[16 tokens][32 weight rows of this warp] += act x W,
+// as four blocks of 8 weight rows.  The K order inside a 128-byte row is
+// permuted the same way for both operands: lane (g, t) takes 16-byte pieces 2t
+// and 2t+1 of weight row g of each block, whose swizzled places are
+// conflict-free for a quarter warp, and the matching 32 (bf16) or 64 (f16, for
+// 32 e4m3 codes) bytes of token rows g and g + 8.
+struct Wts {
+    uint4 v[4][2];
 };
-
-template <bool FP8, int NB>
-__device__ __forceinline__ void load_b(BFrag<FP8> (&b)[NB], const uint8_t* rows, int row_bytes,
-                                       int p, int nb) {
-    constexpr int N = FP8 ? 2 : 1;
+__device__ __forceinline__ void load_w(Wts& w, const uint8_t* rows, int g, int t) {
+    const uint8_t* r = rows + g * kTileRowBytes;
+    const int p0 = ((2 * t) ^ g) * 16, p1 = ((2 * t + 1) ^ g) * 16;
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
-        if (n < nb)
-#pragma unroll
-            for (int q = 0; q < N; ++q)
-                b[n].v[q] = lds16(rows + n * 8 * row_bytes + p * (N * 16) + q * 16);
+    for (int b = 0; b < 4; ++b) {
+        w.v[b][0] = lds16(r + b * 8 * kTileRowBytes + p0);
+        w.v[b][1] = lds16(r + b * 8 * kTileRowBytes + p1);
+    }
 }
 
-template <bool FP8, int NB>
-__device__ __forceinline__ void tile_mma(float (&acc)[NB][4], const uint4 (&a)[2],
-                                         const BFrag<FP8> (&b)[NB], int nb) {
+// Token rows: only real ones are read (the products of the others are never
+// looked at).
+template <bool FP8> struct Act {
+    uint4 v[FP8 ? 4 : 2];
+};
+template <bool FP8>
+__device__ __forceinline__ void load_act(Act<FP8>& a, const uint8_t* row, int t, bool real) {
+    constexpr int N = FP8 ? 4 : 2;
+    if (real)
+#pragma unroll
+        for (int q = 0; q < N; ++q) a.v[q] = lds16(row + t * (N * 16) + q * 16);
+}
+
+// a: rows g, b: rows g + 8
+template <bool FP8>
+__device__ __forceinline__ void tile_mma(float (&acc)[4][4], const Wts& w, const Act<FP8>& a,
+                                         const Act<FP8>& b) {
     if constexpr (!FP8) {
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            if (n < nb) {
-                const uint4 v = b[n].v[0];
-                mma_bf16(acc[n], a[0].x, a[1].x, a[0].y, a[1].y, v.x, v.y);
-                mma_bf16(acc[n], a[0].z, a[1].z, a[0].w, a[1].w, v.z, v.w);
-            }
+        for (int p = 0; p < 2; ++p) {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                mma_bf16(acc[n], a.v[p].x, b.v[p].x, a.v[p].y, b.v[p].y, w.v[n][p].x, w.v[n][p].y);
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                mma_bf16(acc[n], a.v[p].z, b.v[p].z, a.v[p].w, b.v[p].w, w.v[n][p].z, w.v[n][p].w);
         }
     } else {
-        // 16 codes a row: word q meets 8 bytes of b
-        const uint32_t lo[4] = {a[0].x, a[0].y, a[0].z, a[0].w};
-        const uint32_t hi[4] = {a[1].x, a[1].y, a[1].z, a[1].w};
+        // word q of 4 codes meets 8 bytes of the token rows
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const uint32_t f0 = e4m3x2_to_f16x2(lo[q] & 0xffffu);
-            const uint32_t f1 = e4m3x2_to_f16x2(hi[q] & 0xffffu);
-            const uint32_t f2 = e4m3x2_to_f16x2(lo[q] >> 16);
-            const uint32_t f3 = e4m3x2_to_f16x2(hi[q] >> 16);
+        for (int q = 0; q < 8; ++q) {
+            const uint4 x = a.v[q >> 1], y = b.v[q >> 1];
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-                if (n < nb) {
-                    const uint4 v = b[n].v[q >> 1];
-                    mma_f16(acc[n], f0, f1, f2, f3, (q & 1) ? v.z : v.x, (q & 1) ? v.w : v.y);
-                }
+            for (int n = 0; n < 4; ++n) {
+                const uint4 c = w.v[n][q >> 2];
+                uint32_t f0, f1;
+                e4m3x4_to_f16x4((q & 3) == 0 ? c.x : (q & 3) == 1 ? c.y : (q & 3) == 2 ? c.z : c.w,
+                                f0, f1);
+                if (q & 1) mma_f16(acc[n], x.z, y.z, x.w, y.w, f0, f1);
+                else mma_f16(acc[n], x.x, y.x, x.y, y.y, f0, f1);
             }
         }
     }
 }
 
-// The two warps of a pair add their sums: on the `v`-th exchange warp v % 2 gets
-// the total (and returns true).  Two buffers: the pair's barrier of exchange
-// v + 1 is behind the reads of exchange v.
-template <int NB>
-__device__ __forceinline__ bool pair_sum(float (&acc)[NB][4], float4* red, int pair, int half,
-                                         int lane, int v) {
-    float4* buf = red + (((v & 1) * kPairs + pair) * NB) * 32 + lane;
-    const bool mine = (v & 1) == half;
-    if (!mine) {
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-            buf[n * 32] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-    }
-    asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
-    if (mine) {
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const float4 o = buf[n * 32];
-            acc[n][0] += o.x;
-            acc[n][1] += o.y;
-            acc[n][2] += o.z;
-            acc[n][3] += o.w;
-        }
-    }
-    return mine;
-}
-
-// Each token's top-k by counting: an expert's place is the number of keys above
-// its own (the keys are distinct), one thread per (token, expert), so that all k
-// selections take one pass.  The same order and, below, the same sums as
-// warp_topk: ids and weights are its bits.
+// Routing of all tokens by the consumer warps.  A few tokens' keys (one pass of
+// the threads) are ranked by counting: an expert's place is the number of keys
+// above its own (keys are distinct), `parts` threads to a key.  The same order
+// and the same sums as warp_topk, which takes larger batches a warp per token:
+// ids and weights are its bits either way.
+template <bool FP8>
 __device__ __forceinline__ void route_tokens(const Args& g, Shared& s, uint64_t* keys, int warp,
                                              int lane) {
-    const int Ep = (g.E + 31) & ~31;
-    for (int f = threadIdx.x; f < g.T * Ep; f += kConsumers) {
-        const int t = f / Ep, e = f - t * Ep;
-        keys[f] = e < g.E ? select_key(__ldg(g.logits + t * g.E + e), e) : 0ull;
+    const int Ep = (g.E + 31) & ~31, n = g.T * Ep;
+    const bool counting = n <= kConsumers;
+    if (counting && threadIdx.x < n) {
+        const int t = threadIdx.x / Ep, e = threadIdx.x - t * Ep;
+        keys[threadIdx.x] = e < g.E ? select_key(__ldg(g.logits + t * g.E + e), e) : 0ull;
+    }
+    if constexpr (FP8) {
+        // each token's f16 scale, from the last warp down
+        const int tk = kConsumerWarps - 1 - warp;
+        if (tk < g.T) {
+            const uint4* xr = reinterpret_cast<const uint4*>(g.x + static_cast<size_t>(tk) * g.H);
+            uint32_t m = 0;
+#pragma unroll 8
+            for (int v = lane; v < g.H / 8; v += 32) {
+                const uint4 q = __ldg(xr + v);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    m = max(m, max(finite_mag(bf16_lo(w[j])), finite_mag(bf16_hi(w[j]))));
+            }
+            m = __reduce_max_sync(kFullWarp, m);
+            if (lane == 0) s.xmul[tk] = f16_scale(m);
+        }
+    }
+    if (!counting) {
+        for (int t = warp; t < g.T; t += kConsumerWarps) {
+            const float* row = g.logits + t * g.E;
+            int* ids = s.ids + t * g.k;
+            float* w = s.w + t * g.k;
+            if (g.E <= 32) warp_topk<1>(row, g.E, g.k, ids, w);
+            else if (g.E <= 128) warp_topk<4>(row, g.E, g.k, ids, w);
+            else warp_topk<8>(row, g.E, g.k, ids, w);
+            for (int j = lane; j < g.k; j += 32) atomicOr(&s.mask[ids[j]], 1u << t);
+        }
+        return;
     }
     consumer_sync();
-    for (int f = threadIdx.x; f < g.T * Ep; f += kConsumers) {
-        const int t = f / Ep, e = f - t * Ep;
-        if (e >= g.E) continue;
-        const uint64_t own = keys[f];
-        const ulonglong2* row = reinterpret_cast<const ulonglong2*>(keys + t * Ep);
-        int place = 0;
-#pragma unroll 8
-        for (int i = 0; i < Ep / 2; ++i) {
-            const ulonglong2 v = row[i];
-            place += (v.x > own) + (v.y > own);
-        }
-        if (place < g.k) {
-            s.ids[t * g.k + place] = e;
-            s.w[t * g.k + place] = key_value(own);
-            atomicOr(&s.mask[e], 1u << t);
+    int parts = 1;
+    while (parts < 16 && n * parts * 2 <= kConsumers) parts *= 2;
+    {
+        const int f = threadIdx.x / parts, part = threadIdx.x & (parts - 1);
+        if (f < n) {                      // whole warps: n * parts is a multiple of 32
+            const int t = f / Ep, e = f - t * Ep;
+            const uint64_t own = keys[f];
+            int place = 0;
+#pragma unroll 4
+            for (int i = part; i < Ep; i += parts) place += keys[t * Ep + i] > own;
+            for (int off = 1; off < parts; off *= 2)
+                place += __shfl_xor_sync(kFullWarp, place, off);
+            if (part == 0 && e < g.E && place < g.k) {
+                s.ids[t * g.k + place] = e;
+                s.w[t * g.k + place] = key_value(own);
+                atomicOr(&s.mask[e], 1u << t);
+            }
         }
     }
     consumer_sync();
@@ -368,29 +382,43 @@ __device__ __forceinline__ void route_tokens(const Args& g, Shared& s, uint64_t*
     fence_proxy_async_smem();   // the ring's copies come after the keys
 }
 
-// Ring position shared by the producer's and the consumers' loops.
+// Ring position shared by the copying and the product warps' loops.  The n-th
+// tile of a CTA is in slot n % slots and belongs to group n % 4; a group only
+// ever sees its own slots (slots is a multiple of 4), each use of them in turn.
 struct Ring {
-    int slot = 0;
+    int slot;
     uint32_t phase = 0;
     int slots;
-    __device__ __forceinline__ explicit Ring(int n) : slots(n) {}
-    __device__ __forceinline__ void next() {
-        if (++slot == slots) {
-            slot = 0;
+    __device__ __forceinline__ explicit Ring(int n, int first = 0) : slot(first), slots(n) {}
+    __device__ __forceinline__ void skip(int n) {       // n <= slots
+        slot += n;
+        if (slot >= slots) {
+            slot -= slots;
             phase ^= 1u;
         }
     }
 };
 
-// One expert's part of a CTA's range of down tiles: [a, b) in kb * MT + m.
-// The tiles are taken by chunks of k-blocks, within a chunk row tile by row
-// tile, so a row tile's sum over the chunk stays in registers.
-__device__ __forceinline__ int kb_lo(int kbA, int m, int MT, int a) {
-    return kbA + (kbA * MT + m < a ? 1 : 0);
-}
-__device__ __forceinline__ int kb_hi(int kbB, int m, int MT, int b) {
-    return kbB - ((kbB - 1) * MT + m >= b ? 1 : 0);
-}
+// A CTA's down tiles of one expert are a range of kb * MT + m, taken by chunks of
+// whole k-blocks (the first and last may be partial): [a, b).  Within a chunk a
+// row tile is visited once, for all its k-blocks: visit v takes tiles a + v,
+// a + v + MT, ... below b.  Four visits at a time, one per group, their tiles
+// interleaved in the ring; where a visit of the four has a tile less than the
+// first, or there is no fourth visit, the place stays empty but is passed on.
+struct Chunk {
+    int a, b, kb0, kb1, visits;
+    __device__ __forceinline__ Chunk(int from, int to, int MT, int CK) {
+        a = from;
+        kb0 = from / MT;
+        kb1 = kb0 + CK;
+        b = kb1 * MT < to ? kb1 * MT : to;
+        kb1 = (b - 1) / MT + 1;
+        visits = b - a < MT ? b - a : MT;
+    }
+    __device__ __forceinline__ int depth(int v0, int MT) const {   // tiles of visit v0
+        return (b - a - v0 + MT - 1) / MT;
+    }
+};
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
@@ -399,6 +427,17 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
 
 __device__ __forceinline__ float4 add4(float4 a, float4 b) {
     return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+// Stores, or adds to what the same lane stored before.
+__device__ __forceinline__ void put(float* d, float2 v, bool first) {
+    float2* p = reinterpret_cast<float2*>(d);
+    if (!first) {
+        const float2 o = __ldcg(p);
+        v.x += o.x;
+        v.y += o.y;
+    }
+    __stcg(p, v);
 }
 
 // What h's first bf16 value leaves for the second: 16 bits of mantissa
@@ -439,17 +478,16 @@ __device__ __forceinline__ float4 h_quad(const Args& g, const Shared& s, int i, 
     return make_float4(act(gt.x, up.x), act(gt.y, up.y), act(gt.z, up.z), act(gt.w, up.w));
 }
 
-template <bool FP8, int NB>
+template <bool FP8>
 __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Args g) {
     extern __shared__ uint8_t dsmem_raw[];
     __shared__ Shared s;
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(dsmem_raw) + 127) & ~static_cast<uintptr_t>(127));
-    constexpr int SLOT = slot_bytes<FP8, NB>();
+    const int slot_sz = slot_bytes<FP8>(g.T);
     constexpr int BK = tile_k<FP8>();
     constexpr int CK = chunk_kb<FP8>();
-    uint8_t* hbuf = smem + g.slots * SLOT;
-    float4* exch = reinterpret_cast<float4*>(hbuf + h_bytes<FP8, NB>());
+    uint8_t* hbuf = smem + g.slots * slot_sz;
     constexpr int kThreads = threads_for<FP8>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, cta = blockIdx.x;
@@ -462,13 +500,15 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
 #pragma unroll
         for (int i = 0; i < 2; ++i)
             target[i] = __ldcg(reinterpret_cast<const unsigned long long*>(&g.hdr->arrive[i][0]));
-        for (int i = 0; i < g.slots; ++i) {
-            mbar_init(&s.full[i], 1);
-            mbar_init(&s.empty[i], kConsumerWarps);
-            mbar_init(&s.ready[i], kXWarps);
-        }
-        fence_mbar_init();
         s.abort = 0;
+    }
+    // a slot is full when its tile's bytes are there and, for the gate/up tiles,
+    // the x slices that another warp's lanes copy
+    if (threadIdx.x < g.slots) {
+        mbar_init(&s.full[threadIdx.x], 1 + 32);
+        mbar_init(&s.empty[threadIdx.x], kGroupWarps);
+        mbar_init(&s.ready[threadIdx.x], kWidenWarps);
+        fence_mbar_init();
     }
     for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) s.mask[e] = 0;
     __syncthreads();
@@ -476,23 +516,7 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
     // ---- routing (every CTA, all tokens); keys in the ring's memory, no copy
     // is under way yet
     if (warp < kConsumerWarps) {
-        route_tokens(g, s, reinterpret_cast<uint64_t*>(smem), warp, lane);
-    } else if (FP8 && warp >= kXWarp0) {
-        // meanwhile, for e4m3 layers: each token's f16 scale
-        for (int tk = warp - kXWarp0; tk < g.T; tk += kXWarps) {
-            const uint4* xr = reinterpret_cast<const uint4*>(g.x + static_cast<size_t>(tk) * g.H);
-            uint32_t m = 0;
-#pragma unroll 8
-            for (int v = lane; v < g.H / 8; v += 32) {
-                const uint4 q = __ldg(xr + v);
-                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    m = max(m, max(finite_mag(bf16_lo(w[j])), finite_mag(bf16_hi(w[j]))));
-            }
-            m = __reduce_max_sync(kFullWarp, m);
-            if (lane == 0) s.xmul[tk] = f16_scale(m);
-        }
+        route_tokens<FP8>(g, s, reinterpret_cast<uint64_t*>(smem), warp, lane);
     }
     // a workspace that was never initialised would hang the barriers: every
     // CTA sees the same word and leaves
@@ -554,102 +578,129 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
     const int a1 = s.start1[cta], b1 = s.start1[cta + 1];
     const int a2 = s.start2[cta], b2 = s.start2[cta + 1];
 
-    if (warp == kConsumerWarps) {
-        // ---- producer warp: keeps the ring full through both products.  Lane
-        // 0 copies the weight tiles, lane c the x slice of token column c.
+    if (warp == kWeightWarp) {
+        // ---- one thread keeps the ring full of weight tiles through both
+        // products
         Ring ring(g.slots);
         int it = 0;
         bool ok = true;
-        for (int X = a1; X < b1 && ok;) {
+        for (int X = a1; lane == 0 && X < b1 && ok;) {
             const int i = X / S1, end = (i + 1) * S1 < b1 ? (i + 1) * S1 : b1;
-            const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
-            int r = X - i * S1, kb = r % g.kb_gu;
             const uint8_t* w =
-                g.w_gu + (static_cast<size_t>(s.expert[i]) * S1 + r) * kTileBytes;
-            const __nv_bfloat16* x =
-                g.x + (lane < cnt ? static_cast<size_t>(s.tok[c0 + lane]) * g.H : 0);
+                g.w_gu + (static_cast<size_t>(s.expert[i]) * S1 + (X - i * S1)) * kTileBytes;
             for (; X < end; ++X, w += kTileBytes) {
-                if (it >= g.slots && !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
+                if (it >= g.slots && !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
                     ok = false;
-                ok = __all_sync(kFullWarp, ok);
-                if (!ok) break;
-                uint8_t* dst = smem + ring.slot * SLOT;
-                const int left = (g.H - kb * BK) * 2;
-                const uint32_t xb = left < BK * 2 ? left : BK * 2;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&s.full[ring.slot], kTileBytes + cnt * xb);
-                    bulk_load(dst, w, kTileBytes, &s.full[ring.slot], kEvictFirst);
+                    break;
                 }
-                __syncwarp();
-                if (lane < cnt)
-                    bulk_load(dst + kTileBytes + lane * x_row_bytes<FP8>(), x + kb * BK, xb,
-                              &s.full[ring.slot], kEvictLast);
-                if (++kb == g.kb_gu) kb = 0;
-                ring.next();
+                mbar_arrive_expect_tx(&s.full[ring.slot], kTileBytes);
+                bulk_load(smem + ring.slot * slot_sz, w, kTileBytes, &s.full[ring.slot],
+                          kEvictFirst);
+                ring.skip(1);
                 ++it;
             }
         }
-        for (int X = a2; X < b2 && ok;) {
+        for (int X = a2; lane == 0 && X < b2 && ok;) {
             const int i = X / S2;
-            const int a = X - i * S2;
-            const int b = b2 - i * S2 < S2 ? b2 - i * S2 : S2;
+            const int to = b2 - i * S2 < S2 ? b2 - i * S2 : S2;
             const uint8_t* w = g.w_dn + static_cast<size_t>(s.expert[i]) * S2 * kTileBytes;
-            const int kb_end = (b - 1) / g.mt_dn + 1;
-            for (int kbA = a / g.mt_dn; kbA < kb_end && ok; kbA += CK) {
-                const int kbB = kbA + CK < kb_end ? kbA + CK : kb_end;
-                for (int m = 0; m < g.mt_dn && ok; ++m) {
-                    const int hi = kb_hi(kbB, m, g.mt_dn, b);
-                    for (int kb = kb_lo(kbA, m, g.mt_dn, a); kb < hi; ++kb) {
+            for (int from = X - i * S2; from < to && ok;) {
+                const Chunk ch(from, to, g.mt_dn, CK);
+                for (int v0 = 0; v0 < ch.visits && ok; v0 += kGroups) {
+                    const int places = ch.depth(v0, g.mt_dn) * kGroups;
+                    int kb = (ch.a + v0) / g.mt_dn, m = ch.a + v0 - kb * g.mt_dn;   // of visit v0
+                    for (int p = 0; p < places; ++p) {
                         if (it >= g.slots &&
-                            !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
+                            !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
                             ok = false;
-                        ok = __all_sync(kFullWarp, ok);
-                        if (!ok) break;
-                        if (lane == 0) {
-                            mbar_arrive_expect_tx(&s.full[ring.slot], kTileBytes);
-                            bulk_load(smem + ring.slot * SLOT,
-                                      w + (static_cast<size_t>(m) * g.kb_dn + kb) * kTileBytes,
-                                      kTileBytes, &s.full[ring.slot], kEvictFirst);
+                            break;
                         }
-                        ring.next();
+                        const int q = p & (kGroups - 1);
+                        const int L = (kb * g.mt_dn + m) + q;
+                        if (v0 + q < ch.visits && L < ch.b) {
+                            int tkb = kb, tm = m + q;
+                            while (tm >= g.mt_dn) {
+                                tm -= g.mt_dn;
+                                ++tkb;
+                            }
+                            mbar_arrive_expect_tx(&s.full[ring.slot], kTileBytes);
+                            mbar_arrive_n(&s.full[ring.slot], 32);   // (no x slice)
+                            bulk_load(smem + ring.slot * slot_sz,
+                                      w + (static_cast<size_t>(tm) * g.kb_dn + tkb) * kTileBytes,
+                                      kTileBytes, &s.full[ring.slot], kEvictFirst);
+                        } else {
+                            mbar_arrive_n(&s.full[ring.slot], 33);
+                        }
+                        if (q == kGroups - 1) ++kb;
+                        ring.skip(1);
                         ++it;
                     }
                 }
+                from = ch.b;
             }
-            X = i * S2 + b;
+            X = i * S2 + to;
         }
         if (!ok) {
-            if (lane == 0) fault(s, g.status);
+            fault(s, g.status);
             // this CTA's copies in flight (the last `slots`, or fewer) land
             // before its shared memory goes
             Ring back(g.slots);
             for (int j = 0; j < it; ++j) {
                 if (j >= it - g.slots)
                     mbar_wait(&s.full[back.slot], back.phase, nullptr, 10000000ull);
-                back.next();
+                back.skip(1);
             }
         }
-    } else if (FP8 && warp >= kXWarp0) {
+    } else if (warp == kXWarp) {
+        // ---- the x slices of the gate/up tiles, in 16-byte pieces, one per lane
+        // and turn (as bulk copies of a few hundred bytes each they kept the copy
+        // engine from the weights)
+        Ring ring(g.slots);
+        int it = 0;
+        constexpr int PIECES = BK / 8;                 // of a token's slice
+        const int q = lane % PIECES;
+        for (int X = a1; X < b1;) {
+            const int i = X / S1, end = (i + 1) * S1 < b1 ? (i + 1) * S1 : b1;
+            const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
+            int kb = (X - i * S1) % g.kb_gu;
+            for (; X < end; ++X) {
+                if (it >= g.slots && !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
+                    fault(s, g.status);
+                const uint32_t dst = smem_u32(smem + ring.slot * slot_sz + kTileBytes) + q * 16;
+                // (the last e4m3 k-block may hold 64 of its 128 columns: the rest
+                // is filled with zeros)
+                const int col = kb * BK + q * 8;
+                const bool in = col < g.H;
+                for (int c = lane / PIECES; c < cnt; c += 32 / PIECES)
+                    cp_async16(dst + c * x_row_bytes<FP8>(),
+                               g.x + static_cast<size_t>(s.tok[c0 + c]) * g.H + (in ? col : 0),
+                               in ? 16 : 0);
+                cp_async_arrive_noinc(&s.full[ring.slot]);
+                if (++kb == g.kb_gu) kb = 0;
+                ring.skip(1);
+                ++it;
+            }
+        }
+        cp_async_wait_all();
+    } else if (FP8 && warp >= kWidenWarp0) {
         // ---- e4m3 layers: two warps widen the x slices of the gate/up tiles
         // in place (bf16 -> scaled f16), every other token each, so that the
         // sixteen product warps need not each do it
         Ring ring(g.slots);
-        for (int X = a1; X < b1; ++X, ring.next()) {
+        for (int X = a1; X < b1; ++X, ring.skip(1)) {
             const int i = X / S1;
             if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort)) fault(s, g.status);
             const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
-            uint8_t* xs = smem + ring.slot * SLOT + kTileBytes;
+            uint8_t* xs = smem + ring.slot * slot_sz + kTileBytes;
 #pragma unroll 2
-            for (int c = warp - kXWarp0; c < cnt; c += kXWarps) {
-                // 4 values per lane; past H (the last k-block may hold 64 of
-                // its 128) whatever the slot held: not used
+            for (int c = warp - kWidenWarp0; c < cnt; c += kWidenWarps) {
+                // 4 values per lane
                 const float mul = s.xmul[s.tok[c0 + c]];
                 uint2* v = reinterpret_cast<uint2*>(xs + c * x_row_bytes<FP8>()) + lane;
                 const uint2 b = *v;
                 *v = make_uint2(f16x2(bf16_lo(b.x) * mul, bf16_hi(b.x) * mul),
                                 f16x2(bf16_lo(b.y) * mul, bf16_hi(b.y) * mul));
             }
-            fence_proxy_async_smem();   // a later copy into the slot stays later
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.ready[ring.slot]);
         }
@@ -657,12 +708,11 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
         // ---- consumers.  After a fault every wait returns at once, and the
         // loops run on to their ends, so all warps meet at the same barriers.
         const int gq = lane >> 2, t = lane & 3;
-        const int pair = warp & (kPairs - 1), half = warp >> 3;
-        const int wrow = pair * 16 + gq;               // first weight row
-        const int piece = 2 * t + half;
-        int exchanges = 0;
-        Ring ring(g.slots);
-        BFrag<FP8> bv[NB];
+        const int grp = warp / kGroupWarps, wrow = warp % kGroupWarps * 32;  // first weight row
+        Ring ring(g.slots, grp);
+        float* exch = reinterpret_cast<float*>(hbuf);    // [group][T][128]
+        // token rows g and g + 8; untouched registers stay 0
+        Act<FP8> xa = {}, xb = {};
         // while the first tiles are on their way: the CTAs of each expert's down
         // tiles
         const float per2 = static_cast<float>(G2) / static_cast<float>(L2);
@@ -677,72 +727,73 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
             const int i = r / g.mt_gu, m = r - i * g.mt_gu;
             const int end = (r + 1) * g.kb_gu < b1 ? (r + 1) * g.kb_gu : b1;
             const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
-            const int nb = NB == 1 ? 1 : (cnt + 7) >> 3;
-            float acc[NB][4];
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[n][q] = 0.0f;
+            float acc[4][4] = {};
             for (; X < end; ++X) {
+                if (((X - a1) & (kGroups - 1)) != grp) continue;
                 if (!ring_wait(FP8 ? &s.ready[ring.slot] : &s.full[ring.slot], ring.phase,
                                &s.abort))
                     fault(s, g.status);
-                const uint8_t* tile = smem + ring.slot * SLOT;
-                uint4 a[2];
-                load_a(a, tile, wrow, piece);
-                load_b<FP8, NB>(bv, tile + kTileBytes + gq * x_row_bytes<FP8>(),
-                                x_row_bytes<FP8>(), piece, nb);
+                const uint8_t* tile = smem + ring.slot * slot_sz;
+                const uint8_t* xs = tile + kTileBytes + gq * x_row_bytes<FP8>();
+                Wts w;
+                load_w(w, tile + wrow * kTileRowBytes, gq, t);
+                load_act<FP8>(xa, xs, t, gq < cnt);
+                if (cnt > 8) load_act<FP8>(xb, xs + 8 * x_row_bytes<FP8>(), t, gq + 8 < cnt);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
-                ring.next();
-                // the last e4m3 k-block may hold 64 of its 128 columns: the rest
-                // meets zero weights and must not be garbage
-                if (FP8 && (X - r * g.kb_gu + 1) * BK > g.H && t >= 2) {
-#pragma unroll
-                    for (int n = 0; n < NB; ++n) bv[n] = BFrag<FP8>{};
-                }
-                tile_mma<FP8, NB>(acc, a, bv, nb);
+                ring.skip(kGroups);
+                tile_mma<FP8>(acc, w, xa, xb);
             }
-            if (!pair_sum<NB>(acc, exch, pair, half, lane, exchanges++)) continue;
+            // the groups' sums of the row tile, added in group order
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                float* d = exch + (grp * g.T + gq) * kTileRows + wrow + 8 * n + 2 * t;
+                if (gq < cnt) *reinterpret_cast<float2*>(d) = make_float2(acc[n][0], acc[n][1]);
+                if (gq + 8 < cnt)
+                    *reinterpret_cast<float2*>(d + 8 * kTileRows) = make_float2(acc[n][2], acc[n][3]);
+            }
+            consumer_sync();
             // columns of 128 rows; segment (row tile r, CTA c) starts at column
             // sum of the counts before r + c * T: segments follow one another
             // with r or c or both growing, so no two overlap
             float* p = g.p1 + (static_cast<size_t>(c0) * g.mt_gu + m * cnt +
-                               static_cast<size_t>(cta) * g.T) * kTileRows + wrow;
+                               static_cast<size_t>(cta) * g.T) * kTileRows;
+            for (int f = threadIdx.x; f < cnt * kTileRows; f += kConsumers) {
+                float v = exch[f];
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int col = n * 8 + 2 * t + (q & 1);
-                    if (col < cnt) __stcg(p + col * kTileRows + 8 * (q >> 1), acc[n][q]);
-                }
+                for (int q = 1; q < kGroups; ++q) v += exch[q * g.T * kTileRows + f];
+                __stcg(p + f, v);
+            }
+            consumer_sync();
         }
         consumer_sync();
         if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[0][0], target[0]))
             fault(s, g.status);
         consumer_sync();
 
-        // step 2: h of this CTA's k-blocks, and the down partial sums
+        // step 2: h of this CTA's k-blocks, and the down partial sums.  The ring
+        // goes on where the gate/up tiles ended, so visit v0 + vq is this group's
+        const int vq = (grp - (b1 - a1)) & (kGroups - 1);
         const float per1 = static_cast<float>(G1) / static_cast<float>(L1);
         for (int X = a2; X < b2;) {
             const int i = X / S2, e = s.expert[i];
-            const int a = X - i * S2;
-            const int b = b2 - i * S2 < S2 ? b2 - i * S2 : S2;
+            const int from0 = X - i * S2;
+            const int to = b2 - i * S2 < S2 ? b2 - i * S2 : S2;
             const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
-            const int nb = NB == 1 ? 1 : (cnt + 7) >> 3;
-            const int kb_first = a / g.mt_dn, kb_end = (b - 1) / g.mt_dn + 1;
             float sg = 1.0f, su = 1.0f;
             if constexpr (FP8) {
                 sg = __ldg(g.scales + e * 3);
                 su = __ldg(g.scales + e * 3 + 1);
             }
             float* p = g.p2 + (static_cast<size_t>(c0) + static_cast<size_t>(cta) * g.T) *
-                                  g.mt_dn * kTileRows + wrow;
-            for (int kbA = kb_first; kbA < kb_end; kbA += CK) {
-                const int kbB = kbA + CK < kb_end ? kbA + CK : kb_end;
+                                  g.mt_dn * kTileRows +
+                       static_cast<size_t>(gq) * kTileRows + wrow + 2 * t;
+            for (int from = from0; from < to;) {
+                const Chunk ch(from, to, g.mt_dn, CK);
+                const int kbA = ch.kb0, kbB = ch.kb1;
                 // four columns of h a thread and turn (cols is a multiple of 64)
                 const int quads = (kbB - kbA) * (BK / 4);
-                constexpr int TURNS = chunk_kb<FP8>() * BK / 4 * NB * 8 / kConsumers;
+                constexpr int TURNS = chunk_kb<FP8>() * BK / 4 * kDecodeMaxT / kConsumers;
                 float4 hq[TURNS];
 #pragma unroll
                 for (int u = 0; u < TURNS; ++u) {
@@ -772,7 +823,7 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                     if (idx < quads * cnt) {
                         const int c = idx / quads, j = (idx - c * quads) * 4;
                         const int kl = j / BK, jj = j - kl * BK;
-                        uint8_t* d = hbuf + (kl * NB * 8 + c) * h_row_bytes<FP8>() + jj * 2;
+                        uint8_t* d = hbuf + (kl * g.T + c) * h_row_bytes<FP8>() + jj * 2;
                         const float4 h = hq[u];
                         if constexpr (FP8) {
                             const float mul = f16_scale(s.hmax[c]);
@@ -788,63 +839,70 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                     }
                 }
                 consumer_sync();
-                // this lane's columns and their unscaling
-                float inv[NB][2];
-#pragma unroll
-                for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        inv[n][q] = FP8 ? scale_inv(f16_scale(s.hmax[n * 8 + 2 * t + q])) : 1.0f;
+                // (e4m3) the unscaling of this lane's two tokens
+                float inv0 = 1.0f, inv1 = 1.0f;
+                if constexpr (FP8) {
+                    inv0 = scale_inv(f16_scale(s.hmax[gq]));
+                    inv1 = scale_inv(f16_scale(s.hmax[gq + 8]));
+                }
                 // later chunks of the same expert add to the columns that the
-                // same pair wrote: of several chunks the first has at least four
+                // same lane wrote: of several chunks the first has at least four
                 // k-blocks, so every row tile is in it
-                const bool first = kbA == kb_first;
-                for (int m = 0; m < g.mt_dn; ++m) {
-                    const int lo = kb_lo(kbA, m, g.mt_dn, a), hi = kb_hi(kbB, m, g.mt_dn, b);
-                    if (lo >= hi) continue;
-                    float acc[NB][4];
-#pragma unroll
-                    for (int n = 0; n < NB; ++n)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) acc[n][q] = 0.0f;
-                    for (int kb = lo; kb < hi; ++kb) {
+                const bool first = from == from0;
+                for (int v0 = 0; v0 < ch.visits; v0 += kGroups) {
+                    const int v = v0 + vq, depth = ch.depth(v0, g.mt_dn);
+                    int kb = (ch.a + v) / g.mt_dn;
+                    const int m = ch.a + v - kb * g.mt_dn;
+                    float acc[4][4] = {};
+                    for (int q = 0; q < depth; ++q, ++kb) {
                         if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort))
                             fault(s, g.status);
-                        uint4 w[2];
-                        load_a(w, smem + ring.slot * SLOT, wrow, piece);
+                        const bool real = v < ch.visits && kb * g.mt_dn + m < ch.b;
+                        Wts w;
+                        if (real) load_w(w, smem + ring.slot * slot_sz + wrow * kTileRowBytes, gq, t);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
-                        ring.next();
-                        const uint8_t* hb =
-                            hbuf + ((kb - kbA) * NB * 8 + gq) * h_row_bytes<FP8>();
-                        load_b<FP8, NB>(bv, hb, h_row_bytes<FP8>(), piece, nb);
-                        tile_mma<FP8, NB>(acc, w, bv, nb);
-                        if constexpr (!FP8) {
-                            load_b<FP8, NB>(bv, hb + BK * 2, h_row_bytes<FP8>(), piece, nb);
-                            tile_mma<FP8, NB>(acc, w, bv, nb);
+                        ring.skip(kGroups);
+                        if (!real) continue;
+                        const uint8_t* hr = hbuf + ((kb - kbA) * g.T + gq) * h_row_bytes<FP8>();
+                        load_act<FP8>(xa, hr, t, gq < cnt);
+                        if constexpr (FP8) {
+                            if (cnt > 8) load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>(), t, gq + 8 < cnt);
+                            tile_mma<FP8>(acc, w, xa, xb);
+                        } else if (cnt <= 8) {
+                            // hi in rows 0..7, lo in rows 8..15 of the same MMA
+                            load_act<FP8>(xb, hr + BK * 2, t, gq < cnt);
+                            tile_mma<FP8>(acc, w, xa, xb);
+                        } else {
+                            load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>(), t, gq + 8 < cnt);
+                            tile_mma<FP8>(acc, w, xa, xb);
+                            load_act<FP8>(xa, hr + BK * 2, t, gq < cnt);
+                            load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>() + BK * 2, t, gq + 8 < cnt);
+                            tile_mma<FP8>(acc, w, xa, xb);
                         }
                     }
-                    if (!pair_sum<NB>(acc, exch, pair, half, lane, exchanges++)) continue;
+                    if (v >= ch.visits) continue;
                     float* d = p + static_cast<size_t>(m) * cnt * kTileRows;
 #pragma unroll
-                    for (int n = 0; n < NB; ++n)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const int col = n * 8 + 2 * t + (q & 1);
-                            if (col < cnt) {
-                                float* dd = d + col * kTileRows + 8 * (q >> 1);
-                                const float v = acc[n][q] * inv[n][q & 1];
-                                __stcg(dd, first ? v : __ldcg(dd) + v);
-                            }
+                    for (int n = 0; n < 4; ++n) {
+                        float2 v0s = make_float2(acc[n][0] * inv0, acc[n][1] * inv0);
+                        float2 v1s = make_float2(acc[n][2] * inv1, acc[n][3] * inv1);
+                        if (!FP8 && cnt <= 8) {
+                            v0s.x += v1s.x;
+                            v0s.y += v1s.y;
                         }
+                        if (gq < cnt) put(d + 8 * n, v0s, first);
+                        if (gq + 8 < cnt) put(d + 8 * kTileRows + 8 * n, v1s, first);
+                    }
                 }
                 consumer_sync();   // hbuf is free, the chunk's sums are written
                 if constexpr (FP8) {
                     if (threadIdx.x < kDecodeMaxT) s.hmax[threadIdx.x] = 0;
                     consumer_sync();
                 }
+                from = ch.b;
             }
-            X = i * S2 + b;
+            X = i * S2 + to;
         }
         if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[1][0], target[1]))
             fault(s, g.status);
@@ -950,7 +1008,7 @@ __global__ void decode_ws_init_kernel(Header* h) {
 constexpr int kMaxDevices = 64;
 constexpr int kDynSmemMax = kSmemBytes - static_cast<int>(sizeof(Shared)) - 1024;
 
-template <bool FP8, int NB>
+template <bool FP8>
 cudaError_t opt_in_smem() {
     static std::once_flag once[kMaxDevices];
     static cudaError_t err[kMaxDevices];
@@ -959,27 +1017,27 @@ cudaError_t opt_in_smem() {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::call_once(once[dev], [dev] {
-        err[dev] = cudaFuncSetAttribute(decode_kernel<FP8, NB>,
+        err[dev] = cudaFuncSetAttribute(decode_kernel<FP8>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmemMax);
     });
     return err[dev];
 }
 
-template <bool FP8, int NB>
+template <bool FP8>
 cudaError_t launch(const Args& a, int grid, cudaStream_t s) {
-    auto kern = decode_kernel<FP8, NB>;
-    const cudaError_t e = opt_in_smem<FP8, NB>();
+    auto kern = decode_kernel<FP8>;
+    const cudaError_t e = opt_in_smem<FP8>();
     if (e != cudaSuccess) return e;
     constexpr int dyn = kDynSmemMax;
     Args g = a;
-    constexpr int rest = 128 + h_bytes<FP8, NB>() + exchange_bytes<NB>();
-    int slots = (dyn - rest) / slot_bytes<FP8, NB>();
+    const int rest = 128 + h_bytes<FP8>(a.T);
+    const int slots = (dyn - rest) / slot_bytes<FP8>(a.T) / kGroups * kGroups;
     g.slots = slots > kMaxSlots ? kMaxSlots : slots;
-    if (g.slots < 2) return cudaErrorInvalidValue;
+    if (g.slots < kGroups) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads_for<FP8>());
-    cfg.dynamicSmemBytes = rest + g.slots * slot_bytes<FP8, NB>();
+    cfg.dynamicSmemBytes = rest + g.slots * slot_bytes<FP8>(a.T);
     cfg.stream = s;
     // cooperative: the blocks wait on one another, so all must be resident
     cudaLaunchAttribute at[1];
@@ -1044,9 +1102,7 @@ cudaError_t launch_decode(const DecodeProblem& p, cudaStream_t s) {
     g.status = p.status ? p.status : &g.hdr->status;
     g.p1 = reinterpret_cast<float*>(static_cast<char*>(p.ws) + sizeof(Header));
     g.p2 = reinterpret_cast<float*>(static_cast<char*>(p.ws) + sizeof(Header) + z.p1);
-    // more than 8 tokens take two blocks of 8 columns
-    if (fp8) return p.T <= 8 ? launch<true, 1>(g, grid, s) : launch<true, 2>(g, grid, s);
-    return p.T <= 8 ? launch<false, 1>(g, grid, s) : launch<false, 2>(g, grid, s);
+    return fp8 ? launch<true>(g, grid, s) : launch<false>(g, grid, s);
 }
 
 }  // namespace moe
