@@ -356,6 +356,59 @@ MOE_API moe_status moe_decode_forward(const moe_decode_args* args, void* ws, siz
                                       moe_stream_t stream);
 
 /*
+ * Dense products around the layer: the router's logits, a shared expert's
+ * gate/up and down, the projections before and after.
+ *   z = x W^T + bias
+ *   out = act(z) + residual                                  (gated = 0)
+ *   out = act(z[:, :N]) * z[:, N:] + residual                (gated = 1)
+ * with fp32 sums, bias, activation and residual, rounded once to out's type.
+ *   x         device bf16 [M,K], rows ldx elements apart
+ *   w         device bf16 [N,K] (gated: [2N,K], gate rows then up rows), rows
+ *             ldw apart: output columns as rows, as checkpoints keep them
+ *   bias      device [N] (gated: [2N]) of bias_type, or NULL
+ *   residual  device [M,N] of out_type, rows ldr apart, or NULL; may be out
+ *             itself with the same stride
+ *   out       device [M,N] of out_type, rows ldo apart; must not overlap x or w
+ *   status    optional device status word
+ * Activations: NONE; RELU; SILU z/(1+e^-z); GELU z(1+erf(z/sqrt 2))/2;
+ * GELU_TANH, its tanh form z(1+tanh(sqrt(2/pi)(z+0.044715z^3)))/2.  A NaN stays
+ * a NaN through each.
+ * K, ldx and ldw are multiples of 8 (16-byte rows), x and w 16-byte aligned;
+ * out, residual and bias need their elements' alignment only (32-byte aligned
+ * rows are written fastest).  Bit-reproducible; no workspace.
+ * Errors: MOE_ERR_INVALID_ARG for bad sizes, strides, types or pointers,
+ * MOE_ERR_UNSUPPORTED for K, ldx or ldw not a multiple of 8.
+ */
+typedef enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_RELU = 1,
+    MOE_ACT_SILU = 2,
+    MOE_ACT_GELU = 3,
+    MOE_ACT_GELU_TANH = 4
+} moe_act;
+
+typedef enum { MOE_FLOAT_BF16 = 0, MOE_FLOAT_F32 = 1 } moe_float_type;
+
+typedef struct {
+    int M, N, K;
+    int act;                 /* a moe_act */
+    int gated;
+    const void* x;
+    const void* w;
+    int64_t ldx, ldw;
+    const void* bias;
+    int bias_type;           /* a moe_float_type */
+    const void* residual;
+    int64_t ldr;
+    void* out;
+    int64_t ldo;
+    int out_type;            /* a moe_float_type */
+    int32_t* status;
+} moe_linear_args;
+
+MOE_API moe_status moe_linear(const moe_linear_args* args, moe_stream_t stream);
+
+/*
  * Reads a device status word: synchronises the stream, then returns
  * MOE_OK or the code the device recorded (MOE_ERR_TIMEOUT, MOE_ERR_DEVICE).
  * Errors: MOE_ERR_INVALID_ARG for NULL, MOE_ERR_CUDA if the copy fails.

@@ -21,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libmoe_b200_debug.so" if DEBUG_CHECKS else "libm
 
 BF16, FP8_E4M3 = 0, 1
 COMBINE_AUTO, COMBINE_DETERMINISTIC, COMBINE_FUSED = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_SILU, ACT_GELU, ACT_GELU_TANH = 0, 1, 2, 3, 4
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
           3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_CUDA", 5: "MOE_ERR_TIMEOUT",
           6: "MOE_ERR_DEVICE"}
@@ -62,6 +63,13 @@ class DecodeArgs(ctypes.Structure):
                 ("out", P), ("ids", P), ("w", P), ("status", P)]
 
 
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("M", I32), ("N", I32), ("K", I32), ("act", I32), ("gated", I32), ("x", P),
+                ("w", P), ("ldx", ctypes.c_int64), ("ldw", ctypes.c_int64), ("bias", P),
+                ("bias_type", I32), ("residual", P), ("ldr", ctypes.c_int64), ("out", P),
+                ("ldo", ctypes.c_int64), ("out_type", I32), ("status", P)]
+
+
 class SplitCosts(ctypes.Structure):
     _fields_ = [("cpu_us", ctypes.c_double), ("cpu_us_per_token", ctypes.c_double),
                 ("xfer_us", ctypes.c_double), ("gpu_us", ctypes.c_double),
@@ -101,6 +109,7 @@ _SIGS = {
     "moe_decode_workspace_size": ([I32, I32, I32, I32, I32, I32], SZ),
     "moe_decode_workspace_init": ([P, SZ, P], I32),
     "moe_decode_forward": ([ctypes.POINTER(DecodeArgs), P, SZ, P], I32),
+    "moe_linear": ([ctypes.POINTER(LinearArgs), P], I32),
     "moe_check_status": ([P, P], I32),
     "moe_selftest_wait_timeout": ([P, I32, P], I32),
     # CPU/GPU split (include/moe_split.h)
@@ -407,6 +416,64 @@ def decode_forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int
         _check(lib().moe_decode_forward(ctypes.byref(a), _ptr(ws),
                                         0 if ws is None else ws.numel(), _stream(stream)),
                "moe_decode_forward")
+    return out
+
+
+_FLOAT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _rows(t, name, shape, dtype, dev):
+    """Checks a matrix argument of linear (rows may be apart) and returns its row stride."""
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    rs, cs = t.stride()
+    if cs != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: columns must be contiguous")
+    # the stride of a single row is of no account
+    return rs if shape[0] > 1 else (shape[1] + 7) // 8 * 8
+
+
+def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=None, out=None,
+           out_dtype=None, status=None, stream=None):
+    """act(x w^T + bias) + residual, or with ``gated`` act(z[:, :N]) * z[:, N:] + residual.
+
+    x bf16 [M, K] and w bf16 [N, K] (gated: [2N, K], gate rows then up rows), rows any multiple
+    of 8 elements apart; bias bf16 or f32 [rows of w]; residual and out of ``out_dtype`` (bf16,
+    the default, or f32).  ``out`` may be the residual."""
+    if x.dim() != 2 or w.dim() != 2:
+        raise ValueError("x and w: expected [M, K] and [N, K]")
+    if not x.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    dev, bf16 = x.device, torch.bfloat16
+    M, K = x.shape
+    rows = w.shape[0]
+    if gated and rows % 2:
+        raise ValueError("w: a gated product has an even number of rows")
+    N = rows // 2 if gated else rows
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else bf16
+    if out_dtype not in _FLOAT_TYPE:
+        raise ValueError(f"out_dtype: {out_dtype}, expected bfloat16 or float32")
+    ldx = _rows(x, "x", (M, K), bf16, dev)
+    ldw = _rows(w, "w", (rows, K), bf16, dev)
+    bias_type = 0
+    if bias is not None:
+        if bias.dtype not in _FLOAT_TYPE:
+            raise ValueError(f"bias: {bias.dtype}, expected bfloat16 or float32")
+        bias_type = _FLOAT_TYPE[bias.dtype]
+        _take(bias, "bias", (rows,), bias.dtype, dev)
+    ldr = _rows(residual, "residual", (M, N), out_dtype, dev) if residual is not None else 0
+    with _on_device(dev, stream):
+        out = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
+        ldo = _rows(out, "out", (M, N), out_dtype, dev)
+        a = LinearArgs(M, N, K, act, 1 if gated else 0, x.data_ptr(), w.data_ptr(), ldx, ldw,
+                       _ptr(bias), bias_type, _ptr(residual), ldr, out.data_ptr(), ldo,
+                       _FLOAT_TYPE[out_dtype], _ptr(status))
+        _check(lib().moe_linear(ctypes.byref(a), _stream(stream)), "moe_linear")
     return out
 
 

@@ -18,7 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["route_permute.cu", "elementwise.cu", "grouped_gemm.cu", "moe_api.cu", "noalloc.cu",
-           "split.cu", "decode.cu"]
+           "split.cu", "decode.cu", "linear.cu"]
 # host code of the CPU/GPU split (g++: the AVX512_BF16 kernel selects its
 # instruction set per function and checks the CPU at run time)
 HOST_SOURCES = ["host_ffn.cpp"]

@@ -212,6 +212,21 @@ size_t decode_ws_bytes(int fp8, int T, int k, int E, int H, int I);
 cudaError_t launch_decode_ws_init(void* ws, cudaStream_t s);
 cudaError_t launch_decode(const DecodeProblem& p, cudaStream_t s);
 
+// ---- dense products (linear.cu)
+struct LinearProblem {
+    int M, N, K, act, gated;      // act: a moe_act
+    const void* x;
+    const void* w;
+    long long ldx, ldw, ldr, ldo;
+    const void* bias;
+    int bias_f32;
+    const void* residual;
+    void* out;
+    int out_f32;
+    int32_t* status;
+};
+cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s);
+
 // ---- the bf16 grouped FFN (a3..a6) over E_sub consecutive segments of a
 // permutation (moe_api.cu): counts/offsets point at the first of them and
 // may start inside a larger permutation, whose other rows are left alone;

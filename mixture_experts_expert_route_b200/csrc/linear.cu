@@ -1,0 +1,919 @@
+// linear.cu -- the dense products around the MoE layer, with everything that
+// follows a product in its epilogue:
+//
+//   out = act(x W^T + bias) [* (x W_up^T + bias_up)] [+ residual]
+//
+// x [M,K] token rows, W [N,K] (or [2N,K]: gate rows, then up rows) as
+// checkpoints keep them, both bf16 and K-major, so both operands come straight
+// from the caller's tensors; sums, bias, activation and residual in fp32, one
+// rounding to the output type.  The router's logits (fp32 out), a shared
+// expert's two products, and the projections before and after the layer.
+//
+// Three kernels, by what bounds them:
+//   few   M <= 16: the stream of W.  Warp MMAs fed by 16-byte loads from global
+//         memory, no shared memory and no barrier in the way; K is split over
+//         warps, and over the blocks of a cluster, until about 16 warps per SM
+//         have loads in flight.
+//   tile  one 128 x BN tcgen05 tile per block; when there are fewer tiles than
+//         SMs, the blocks of a cluster split K and add their accumulators
+//         through distributed shared memory.
+//   pair  256 x BN tiles on CTA pairs (cta_group::2), persistent, two TMEM
+//         accumulators, so an epilogue runs under the next tile's products.
+// No kernel needs a workspace, and no sum depends on timing.
+#include <cstdint>
+#include <cstring>
+#include <mutex>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRowBytes = 128;           // one swizzle atom: 64 bf16 of K
+constexpr int kBK = 64;
+constexpr uint64_t kDrainLimitNs = 10000000ull;
+
+struct Args {
+    int M, N, K;
+    int act, gated;
+    const __nv_bfloat16* x;
+    const __nv_bfloat16* w;
+    long long ldx, ldw, ldr, ldo;        // elements
+    const void* bias;                    // bf16 or f32 [rows of W] or null
+    int bias_f32;
+    const void* residual;                // out's type, or null
+    void* out;
+    int out_f32;
+    int vec;                             // bytes that out's and residual's rows are aligned to: 32, 16 or 0
+    int32_t* status;
+};
+
+__device__ __forceinline__ float load_bias(const Args& g, int row) {
+    if (!g.bias) return 0.0f;
+    return g.bias_f32 ? __ldg(static_cast<const float*>(g.bias) + row)
+                      : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(g.bias) + row));
+}
+
+// The activations on fp32 (a NaN stays one).  erff, tanhf and expf are CUDA's,
+// within a few fp32 ulp.
+__device__ __forceinline__ float activate(float z, int act) {
+    switch (act) {
+        case MOE_ACT_RELU: return z < 0.0f ? 0.0f : z;
+        case MOE_ACT_SILU: return z / (1.0f + expf(-z));
+        case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
+        case MOE_ACT_GELU_TANH:
+            return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
+        default: return z;
+    }
+}
+
+__device__ __forceinline__ float load_res(const Args& g, long long row, int col) {
+    const long long o = row * g.ldr + col;
+    return g.out_f32 ? static_cast<const float*>(g.residual)[o]
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(g.residual)[o]);
+}
+
+__device__ __forceinline__ void store_one(const Args& g, long long row, int col, float v) {
+    if (g.residual) v += load_res(g, row, col);
+    const long long o = row * g.ldo + col;
+    if (g.out_f32) static_cast<float*>(g.out)[o] = v;
+    else static_cast<__nv_bfloat16*>(g.out)[o] = __float2bfloat16_rn(v);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// 32-byte accesses: one whole sector per lane
+__device__ __forceinline__ void ld32(const void* p, uint32_t (&r)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void st32(void* p, const uint32_t (&r)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+
+// 16 consecutive columns of one row, from column col (a multiple of 16).
+__device__ __forceinline__ void store16(const Args& g, long long row, int col, float (&v)[16]) {
+    if (g.vec != 32 || col + 16 > g.N) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (col + i < g.N) store_one(g, row, col + i, v[i]);
+        return;
+    }
+    uint32_t r[8];
+    if (g.out_f32) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (g.residual) {
+                ld32(static_cast<const float*>(g.residual) + row * g.ldr + col + 8 * h, r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[8 * h + i] += __uint_as_float(r[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(v[8 * h + i]);
+            st32(static_cast<float*>(g.out) + row * g.ldo + col + 8 * h, r);
+        }
+    } else {
+        if (g.residual) {
+            ld32(static_cast<const __nv_bfloat16*>(g.residual) + row * g.ldr + col, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[2 * i] += bf16_lo(r[i]);
+                v[2 * i + 1] += bf16_hi(r[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+        st32(static_cast<__nv_bfloat16*>(g.out) + row * g.ldo + col, r);
+    }
+}
+
+// Four consecutive columns (a multiple of 4).
+__device__ __forceinline__ void store4(const Args& g, long long row, int col, float4 v) {
+    if (g.vec < 16 || col + 4 > g.N) {
+        const float a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (col + i < g.N) store_one(g, row, col + i, a[i]);
+        return;
+    }
+    if (g.out_f32) {
+        if (g.residual) {
+            const float4 r = *reinterpret_cast<const float4*>(
+                static_cast<const float*>(g.residual) + row * g.ldr + col);
+            v.x += r.x;
+            v.y += r.y;
+            v.z += r.z;
+            v.w += r.w;
+        }
+        *reinterpret_cast<float4*>(static_cast<float*>(g.out) + row * g.ldo + col) = v;
+    } else {
+        if (g.residual) {
+            const uint2 r = *reinterpret_cast<const uint2*>(
+                static_cast<const __nv_bfloat16*>(g.residual) + row * g.ldr + col);
+            v.x += bf16_lo(r.x);
+            v.y += bf16_hi(r.x);
+            v.z += bf16_lo(r.y);
+            v.w += bf16_hi(r.y);
+        }
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.out) + row * g.ldo + col) =
+            make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+    }
+}
+
+// ------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t smem, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t a) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+
+// ================================================================= few
+// A warp takes 16 weight rows (gated: 8 gate rows and their 8 up rows) and a
+// range of 64-column steps of K.  m16n8k16 MMAs, tokens in M; the K order
+// inside a step is permuted the same way for both operands, so that lane (g, t)
+// reads 32 consecutive bytes of each of its rows.
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Weights are read once: past L1.
+__device__ __forceinline__ uint4 ld_stream(const uint4* p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+template <int MB>
+struct Step {
+    uint4 w[2][2];      // [block of 8 rows][16-byte piece]
+    uint4 x[MB][2];     // [token row g, g + 8][piece]
+};
+
+// MB: blocks of 8 tokens.  wk: warps of a block that share rows and split K.
+template <int MB>
+__global__ void __launch_bounds__(kFewThreads, 2)
+    linear_few_kernel(const Args g, int wk, int csize) {
+    __shared__ float sums[kFewWarps][16][16];     // [warp][token][row]
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int gq = lane >> 2, t = lane & 3;
+    const int wr = kFewWarps / wk;                // row groups of a block
+    const uint32_t rank = csize > 1 ? cluster_ctarank() : 0;
+    const int block = blockIdx.x / csize;
+    const int per = g.gated ? 8 : 16;             // output columns of a row group
+    const int col0 = (block * wr + warp / wk) * per;
+    const int steps = (g.K + kBK - 1) / kBK, parts = wk * csize;
+    const int part = static_cast<int>(rank) * wk + warp % wk;
+    const int s0 = static_cast<int>(static_cast<long long>(steps) * part / parts);
+    const int s1 = static_cast<int>(static_cast<long long>(steps) * (part + 1) / parts);
+
+    // this lane's rows; rows and tokens past the end read nothing
+    const int c0 = col0 + gq, c1 = g.gated ? col0 + gq : col0 + 8 + gq;
+    const bool ok0 = c0 < g.N, ok1 = c1 < g.N;
+    const __nv_bfloat16* w0 = g.w + (ok0 ? static_cast<long long>(c0) * g.ldw : 0) + 16 * t;
+    const __nv_bfloat16* w1 =
+        g.w + (ok1 ? (g.gated ? static_cast<long long>(g.N) + c1 : c1) * g.ldw : 0) + 16 * t;
+    const __nv_bfloat16* xr[MB];
+    bool okx[MB];
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+        okx[m] = m * 8 + gq < g.M;
+        xr[m] = g.x + (okx[m] ? static_cast<long long>(m * 8 + gq) * g.ldx : 0) + 16 * t;
+    }
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    auto load = [&](Step<MB>& st, int s) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const long long k = static_cast<long long>(s) * kBK + 8 * p;
+            const bool in = s < s1 && k + 16 * t < g.K;      // K is a multiple of 8
+            st.w[0][p] = in && ok0 ? ld_stream(reinterpret_cast<const uint4*>(w0 + k)) : zero;
+            st.w[1][p] = in && ok1 ? ld_stream(reinterpret_cast<const uint4*>(w1 + k)) : zero;
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+                st.x[m][p] = in && okx[m] ? __ldg(reinterpret_cast<const uint4*>(xr[m] + k)) : zero;
+        }
+    };
+    float acc[2][4] = {};
+    auto mul = [&](const Step<MB>& st) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const uint4 a = st.x[0][p], b = MB > 1 ? st.x[MB - 1][p] : zero;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                mma_bf16(acc[n], a.x, b.x, a.y, b.y, st.w[n][p].x, st.w[n][p].y);
+                mma_bf16(acc[n], a.z, b.z, a.w, b.w, st.w[n][p].z, st.w[n][p].w);
+            }
+        }
+    };
+    constexpr int DEPTH = MB == 1 ? 4 : 3;    // steps of loads in flight per warp
+    Step<MB> ring[DEPTH];
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) load(ring[d], s0 + d);
+    for (int s = s0; s < s1; s += DEPTH) {
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            mul(ring[d]);                     // (past the range: zeros)
+            load(ring[d], s + d + DEPTH);
+        }
+    }
+
+    // sums over the warps that share the rows, in order, then over the cluster
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+        *reinterpret_cast<float2*>(&sums[warp][gq][8 * n + 2 * t]) = make_float2(acc[n][0], acc[n][1]);
+        *reinterpret_cast<float2*>(&sums[warp][gq + 8][8 * n + 2 * t]) =
+            make_float2(acc[n][2], acc[n][3]);
+    }
+    __syncthreads();
+    if (wk > 1) {
+        for (int q = 0; q < wr; ++q) {     // 256 elements a row group, one a thread
+            float v = 0.0f;
+            for (int j = 0; j < wk; ++j) v += (&sums[q * wk + j][0][0])[threadIdx.x];
+            (&sums[q * wk][0][0])[threadIdx.x] = v;
+        }
+        __syncthreads();
+    }
+    if (csize > 1) cluster_sync();
+    // outputs of the block: wr row groups x M tokens x `per` columns, dealt over
+    // the cluster's blocks
+    const int total = wr * g.M * per;
+    for (int f = static_cast<int>(rank) * kFewThreads + threadIdx.x; f < total;
+         f += csize * kFewThreads) {
+        const int c = f % per, m = f / per % g.M, q = f / (per * g.M);
+        const int col = (block * wr + q) * per + c;
+        if (col >= g.N) continue;
+        const uint32_t a = smem_u32(&sums[q * wk][m][c]);
+        float z = 0.0f, up = 0.0f;
+        if (csize == 1) {
+            z = sums[q * wk][m][c];
+            if (g.gated) up = sums[q * wk][m][c + 8];
+        } else {
+            for (int r = 0; r < csize; ++r) {
+                z += ld_cluster(cluster_addr(a, r));
+                if (g.gated) up += ld_cluster(cluster_addr(a + 32, r));
+            }
+        }
+        z = activate(z + load_bias(g, col), g.act);
+        if (g.gated) z *= up + load_bias(g, g.N + col);
+        store_one(g, m, col, z);
+    }
+    if (csize > 1) cluster_sync();     // peers may still be reading this block's sums
+}
+
+// ================================================================= tile
+struct Maps {
+    CUtensorMap x;     // box 64 x 128 rows
+    CUtensorMap w;     // box 64 x rows of one weight copy
+};
+
+constexpr int kTileThreads = 256;
+constexpr int kTileM = 128;
+constexpr int kTileStages = 4;
+
+template <int BN>
+__host__ __device__ constexpr int tile_stage_bytes() { return (kTileM + BN) * kRowBytes; }
+template <int BN>
+__host__ __device__ constexpr int tile_smem_bytes() {
+    const int ring = kTileStages * tile_stage_bytes<BN>(), acc = kTileM * (BN + 4) * 4;
+    return 1024 + (ring > acc ? ring : acc);
+}
+
+struct TileCtl {
+    uint64_t full[kTileStages];
+    uint64_t empty[kTileStages];
+    uint64_t done;
+    uint32_t tmem;
+    int abort;
+    uint32_t issued;
+};
+
+template <int BN>
+__global__ void __launch_bounds__(kTileThreads)
+    linear_tile_kernel(const __grid_constant__ Maps maps, const Args g, int csize) {
+    extern __shared__ uint8_t dsmem_raw[];
+    __shared__ TileCtl ctl;
+    uint8_t* base = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    constexpr int STAGE = tile_stage_bytes<BN>(), S = kTileStages;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = csize > 1 ? cluster_ctarank() : 0;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&ctl.full[i], 1);
+            mbar_init(&ctl.empty[i], 1);
+        }
+        mbar_init(&ctl.done, 1);
+        fence_mbar_init();
+        ctl.abort = 0;
+        ctl.issued = 0;
+        tma_prefetch_desc(&maps.x);
+        tma_prefetch_desc(&maps.w);
+    }
+    if (warp == 2) {
+        tmem_alloc(&ctl.tmem, BN);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl.tmem;
+    pdl_wait();
+    pdl_trigger();
+
+    const int per = g.gated ? BN / 2 : BN;              // output columns of a tile
+    const int tiles_n = (g.N + per - 1) / per;
+    const int tile = blockIdx.x / csize;
+    const int m0 = tile / tiles_n * kTileM, n0 = tile % tiles_n * per;
+    const int KB = (g.K + kBK - 1) / kBK;
+    const int kb0 = static_cast<int>(static_cast<long long>(KB) * rank / csize);
+    const int kb1 = static_cast<int>(static_cast<long long>(KB) * (rank + 1) / csize);
+
+    if (warp == 0 && lane == 0) {
+        uint32_t issued = 0;
+        for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+            const uint32_t st = issued % S, use = issued / S;
+            if (use > 0 && !mbar_wait(&ctl.empty[st], (use - 1) & 1u, &ctl.abort)) {
+                report(g.status, MOE_ERR_TIMEOUT);
+                *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
+                break;
+            }
+            uint8_t* a = base + st * STAGE;
+            mbar_arrive_expect_tx(&ctl.full[st], STAGE);
+            tma_load_2d(a, &maps.x, &ctl.full[st], kb * kBK, m0, kEvictNormal);
+            uint8_t* b = a + kTileM * kRowBytes;
+            tma_load_2d(b, &maps.w, &ctl.full[st], kb * kBK, n0, kEvictNormal);
+            if (g.gated)
+                tma_load_2d(b + BN / 2 * kRowBytes, &maps.w, &ctl.full[st], kb * kBK, g.N + n0,
+                            kEvictNormal);
+        }
+        ctl.issued = issued;
+    } else if (warp == 1 && lane == 0) {
+        const uint32_t idesc = make_idesc<false>(kTileM, BN);
+        for (int kb = kb0; kb < kb1; ++kb) {
+            const uint32_t i = kb - kb0, st = i % S;
+            if (!mbar_wait(&ctl.full[st], (i / S) & 1u, &ctl.abort)) {
+                report(g.status, MOE_ERR_TIMEOUT);
+                *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t ad = sw128_desc(smem_u32(base + st * STAGE));
+            const uint64_t bd = sw128_desc(smem_u32(base + st * STAGE + kTileM * kRowBytes));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                umma<false>(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (i | kk) ? 1u : 0u);
+            umma_commit(&ctl.empty[st]);
+        }
+        umma_commit(&ctl.done);
+    }
+    __syncwarp();
+    // the accumulator is whole (or the wait ran out): every thread, so that
+    // none leaves while products read the ring
+    if (!mbar_wait(&ctl.done, 0, nullptr, 2 * kWaitLimitNs)) report(g.status, MOE_ERR_TIMEOUT);
+    tc_fence_after();
+    __syncthreads();
+    if (*reinterpret_cast<volatile int*>(&ctl.abort) && threadIdx.x == 0) {
+        // copies in flight land before the ring is written over
+        const uint32_t n = ctl.issued, first = n > S ? n - S : 0;
+        for (uint32_t i = first; i < n; ++i)
+            mbar_wait(&ctl.full[i % S], (i / S) & 1u, nullptr, kDrainLimitNs);
+    }
+    __syncthreads();
+
+    // accumulator -> shared memory, rows of BN + 4 floats (a lane per row: the 4
+    // keep 16-byte stores of 8 lanes on different banks)
+    constexpr int LD = BN + 4;
+    float* sacc = reinterpret_cast<float*>(base);
+    {
+        const int q = warp & 3, half = warp >> 2;
+        float* row = sacc + (32 * q + lane) * LD + half * (BN / 2);
+        if (kb1 > kb0) {
+#pragma unroll
+            for (int c = 0; c < BN / 2; c += 16) {
+                float v[16];
+                tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + half * (BN / 2) + c, v);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4)
+                    *reinterpret_cast<float4*>(row + c + i) =
+                        make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+            }
+        } else {
+            for (int c = 0; c < BN / 2; c += 4)
+                *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    tc_fence_before();
+    if (csize > 1) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == 2) tmem_dealloc(tmem, BN);
+
+    // out: four columns a thread, a row's threads side by side; the rows are
+    // dealt over the cluster's blocks, each adds the blocks' sums in rank order
+    const int quads = per / 4, rows = min(kTileM, g.M - m0);
+    const int r0 = rows * static_cast<int>(rank) / csize, r1 = rows * (static_cast<int>(rank) + 1) / csize;
+    const uint32_t s0 = smem_u32(sacc);
+    for (int f = threadIdx.x; f < (r1 - r0) * quads; f += kTileThreads) {
+        const int r = r0 + f / quads, c = f % quads * 4, col = n0 + c;
+        if (col >= g.N) continue;
+        float4 z, up = make_float4(0.f, 0.f, 0.f, 0.f);
+        const uint32_t off = (r * LD + c) * 4;
+        if (csize == 1) {
+            z = *reinterpret_cast<const float4*>(sacc + r * LD + c);
+            if (g.gated) up = *reinterpret_cast<const float4*>(sacc + r * LD + c + BN / 2);
+        } else {
+            z = up;
+            for (int q = 0; q < csize; ++q) {
+                const uint32_t a = cluster_addr(s0 + off, q);
+                const float4 v = ld_cluster4(a);
+                z.x += v.x;
+                z.y += v.y;
+                z.z += v.z;
+                z.w += v.w;
+                if (g.gated) {
+                    const float4 u = ld_cluster4(a + BN / 2 * 4);
+                    up.x += u.x;
+                    up.y += u.y;
+                    up.z += u.z;
+                    up.w += u.w;
+                }
+            }
+        }
+        float zz[4] = {z.x, z.y, z.z, z.w};
+        const float uu[4] = {up.x, up.y, up.z, up.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int cc = min(col + i, g.N - 1);
+            zz[i] = activate(zz[i] + load_bias(g, cc), g.act);
+            if (g.gated) zz[i] *= uu[i] + load_bias(g, g.N + cc);
+        }
+        store4(g, m0 + r, col, make_float4(zz[0], zz[1], zz[2], zz[3]));
+    }
+    if (csize > 1) cluster_sync();     // peers may still be reading this block's sums
+}
+
+// ================================================================= pair
+constexpr int kPairThreads = 384;
+constexpr int kEpiWarp0 = 4;                 // warps 4..11
+constexpr int kEpiThreads = 256;
+
+template <int BN> __host__ __device__ constexpr int pair_stage_bytes() {
+    return (128 + BN / 2) * kRowBytes;       // per CTA: 128 token rows, half of the weight rows
+}
+template <int BN> __host__ __device__ constexpr int pair_stages() { return BN == 256 ? 6 : 8; }
+template <int BN> __host__ __device__ constexpr int pair_smem_bytes() {
+    return 1024 + pair_stages<BN>() * pair_stage_bytes<BN>();
+}
+
+template <int BN>
+struct PairCtl {
+    uint64_t full[pair_stages<BN>()];
+    uint64_t empty[pair_stages<BN>()];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t drain;
+    uint32_t tmem;
+    int abort;
+    uint32_t prod_pos, mma_pos, mma_issued;
+    float bias[2][BN];
+};
+
+// Tile t of the rasterised order: groups of 8 row tiles, in a group column tile
+// by column tile, so that the tiles in flight share operands in L2.
+__device__ __forceinline__ void pair_tile(int t, int tm, int tn, int& m, int& n) {
+    const int per = 8 * tn, grp = t / per, first = grp * 8;
+    const int h = min(8, tm - first);
+    const int r = t - grp * per;
+    m = first + r % h;
+    n = r / h;
+}
+
+template <int BN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    linear_pair_kernel(const __grid_constant__ Maps maps, const Args g) {
+    extern __shared__ uint8_t dsmem_raw[];
+    __shared__ PairCtl<BN> ctl;
+    uint8_t* base = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    constexpr int STAGE = pair_stage_bytes<BN>(), S = pair_stages<BN>();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&ctl.full[i], 1);
+            mbar_init(&ctl.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.tfull[i], 1);
+            mbar_init(&ctl.tempty[i], 2 * (kEpiThreads / 32));
+        }
+        mbar_init(&ctl.drain, 1);
+        fence_mbar_init();
+        ctl.abort = 0;
+        ctl.prod_pos = ctl.mma_pos = ctl.mma_issued = 0;
+        tma_prefetch_desc(&maps.x);
+        tma_prefetch_desc(&maps.w);
+    }
+    if (warp == 2) {
+        tmem_alloc_pair(&ctl.tmem, 2 * BN);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync();          // the peer's barriers are initialised
+    const uint32_t tmem = ctl.tmem;
+    pdl_wait();
+    pdl_trigger();
+
+    const int per = g.gated ? BN / 2 : BN;
+    const int tm = (g.M + 255) / 256, tn = (g.N + per - 1) / per, tiles = tm * tn;
+    const int P = gridDim.x >> 1, p0 = blockIdx.x >> 1;
+    const int KB = (g.K + kBK - 1) / kBK;
+    auto raise = [&]() {
+        report(g.status, MOE_ERR_TIMEOUT);
+        *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // both CTAs copy their own rows; the copies complete on the rank-0
+            // CTA's barrier, which its thread arms for both.  Weight rows of a
+            // gated tile: the gate rows on rank 0, the up rows on rank 1.
+            uint32_t it = 0;
+            int st = 0;
+            uint32_t par = 1;
+            bool ok = true;
+            for (int t = p0; t < tiles && ok; t += P) {
+                int m, n;
+                pair_tile(t, tm, tn, m, n);
+                const int xrow = m * 256 + rank * 128;
+                const int wrow = g.gated ? rank * g.N + n * per : n * BN + rank * (BN / 2);
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    if (!mbar_wait(&ctl.empty[st], par, &ctl.abort)) {
+                        raise();
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* a = base + st * STAGE;
+                    if (rank == 0) mbar_arrive_expect_tx(&ctl.full[st], 2 * STAGE);
+                    tma_load_2d_pair(a, &maps.x, &ctl.full[st], kb * kBK, xrow, kEvictNormal);
+                    tma_load_2d_pair(a + 128 * kRowBytes, &maps.w, &ctl.full[st], kb * kBK, wrow,
+                                     kEvictNormal);
+                    if (++st == S) {
+                        st = 0;
+                        par ^= 1u;
+                    }
+                }
+            }
+            ctl.prod_pos = it;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = make_idesc<false>(256, BN);
+            const uint64_t a0 = sw128_desc(smem_u32(base));
+            const uint64_t b0 = sw128_desc(smem_u32(base + 128 * kRowBytes));
+            int st = 0;
+            uint32_t ph = 0, it = 0, i = 0;
+            bool ok = true;
+            ctl.mma_issued = 1;
+            for (int t = p0; t < tiles && ok; t += P, ++i) {
+                const int acc = i & 1;
+                if (!mbar_wait(&ctl.tempty[acc], ((i >> 1) & 1u) ^ 1u, &ctl.abort)) {
+                    raise();
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + acc * BN;
+                for (int kb = 0; kb < KB; ++kb, ++it) {
+                    if (!mbar_wait(&ctl.full[st], ph, &ctl.abort)) {
+                        raise();
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = a0 + static_cast<uint32_t>(st * (STAGE >> 4));
+                    const uint64_t bd = b0 + static_cast<uint32_t>(st * (STAGE >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        umma_pair<false>(d, ad + 2 * kk, bd + 2 * kk, idesc, (kb | kk) ? 1u : 0u);
+                    umma_commit_pair(&ctl.empty[st]);
+                    if (++st == S) {
+                        st = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (ok) umma_commit_pair(&ctl.tfull[acc]);
+            }
+            ctl.mma_pos = it;
+        }
+        __syncwarp();
+    } else if (warp >= kEpiWarp0) {
+        const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+        const int et = threadIdx.x - kEpiWarp0 * 32;
+        uint32_t i = 0;
+        for (int t = p0; t < tiles; t += P, ++i) {
+            const int acc = i & 1;
+            int m, n;
+            pair_tile(t, tm, tn, m, n);
+            const int n0 = n * per;
+            // this tile's bias, in accumulator column order
+            if (et < BN) {
+                const int c = n0 + (g.gated && et >= BN / 2 ? et - BN / 2 : et);
+                ctl.bias[acc][et] =
+                    c < g.N ? load_bias(g, g.gated && et >= BN / 2 ? g.N + c : c) : 0.0f;
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            // (after a fault the waits return at once and the loop runs on, so
+            // that all epilogue warps meet at the same barriers)
+            if (!mbar_wait(&ctl.tfull[acc], (i >> 1) & 1u, &ctl.abort)) raise();
+            tc_fence_after();
+            const long long row = static_cast<long long>(m) * 256 + rank * 128 + 32 * q + lane;
+            const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * BN;
+            const float* bias = ctl.bias[acc];
+            const int span = per / 2;         // this warp's output columns
+            for (int c = half * span; c < (half + 1) * span; c += 16) {
+                uint32_t r0[16], r1[16];
+                tmem_ld16_async(ta + c, r0);
+                if (g.gated) tmem_ld16_async(ta + BN / 2 + c, r1);
+                tmem_wait16(r0);
+                if (g.gated) tmem_wait16(r1);
+                float v[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v[j] = activate(__uint_as_float(r0[j]) + bias[c + j], g.act);
+                if (g.gated) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        v[j] *= __uint_as_float(r1[j]) + bias[BN / 2 + c + j];
+                }
+                if (row < g.M && n0 + c < g.N) store16(g, row, n0 + c, v);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_leader(&ctl.tempty[acc]);
+        }
+    }
+
+    __syncthreads();
+    if (*reinterpret_cast<volatile int*>(&ctl.abort)) {
+        // own products and copies in flight end (bounded) before the memory goes
+        if (warp == 1 && lane == 0 && ctl.mma_issued) {
+            umma_commit_pair_local(&ctl.drain);
+            mbar_wait(&ctl.drain, 0, nullptr, kDrainLimitNs);
+        }
+        if (warp == 0 && lane == 0 && rank == 0) {
+            for (uint32_t it = ctl.mma_pos; it < ctl.prod_pos; ++it)
+                mbar_wait(&ctl.full[it % S], (it / S) & 1u, nullptr, kDrainLimitNs);
+        }
+        __syncthreads();
+    }
+    cluster_sync();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 2 * BN);
+    }
+}
+
+// ---- host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// [rows, K] bf16 with row stride ld, copied in boxes of 64 columns x box_rows,
+// swizzled; columns past K and rows past the end read as zero.
+bool make_map(CUtensorMap* m, const void* ptr, int K, long long rows, long long ld, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    const cuuint32_t box[2] = {kBK, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr int kMaxDevices = 64;
+
+// More than 48 KB of dynamic shared memory, once per device and kernel.
+template <class K>
+cudaError_t opt_in(K kern, int bytes, std::once_flag* once, cudaError_t* err) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    std::call_once(once[dev], [&] {
+        err[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    });
+    return err[dev];
+}
+
+template <class... KArgs, class... A>
+cudaError_t launch(void (*kern)(KArgs...), long long grid, int threads, int smem, int cluster,
+                   cudaStream_t s, A... a) {
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(a)...);
+}
+
+cudaError_t launch_few(const Args& g, int sms, cudaStream_t s) {
+    const int per = g.gated ? 8 : 16;
+    const long long groups = (static_cast<long long>(g.N) + per - 1) / per;
+    const int steps = (g.K + kBK - 1) / kBK;
+    // K is split until there are 16 warps per SM, or 2 steps a warp
+    int split = 1;
+    while (split < 64 && groups * split * 2 <= 16LL * sms && steps >= split * 4) split *= 2;
+    const int wk = split < kFewWarps ? split : kFewWarps, csize = split / wk;
+    const long long grid = (groups + kFewWarps / wk - 1) / (kFewWarps / wk) * csize;
+    return g.M <= 8 ? launch(linear_few_kernel<1>, grid, kFewThreads, 0, csize, s, g, wk, csize)
+                    : launch(linear_few_kernel<2>, grid, kFewThreads, 0, csize, s, g, wk, csize);
+}
+
+template <int BN>
+cudaError_t launch_tile(const Args& g, int sms, cudaStream_t s) {
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t err[kMaxDevices];
+    cudaError_t e = opt_in(linear_tile_kernel<BN>, tile_smem_bytes<BN>(), once, err);
+    if (e != cudaSuccess) return e;
+    const int per = g.gated ? BN / 2 : BN;
+    const long long tiles = (static_cast<long long>(g.M) + kTileM - 1) / kTileM *
+                            ((static_cast<long long>(g.N) + per - 1) / per);
+    const int KB = (g.K + kBK - 1) / kBK;
+    // blocks of a cluster split K while there is room for them on the SMs (two
+    // blocks each at BN = 64) and each keeps at least 4 k-blocks
+    const int room = (BN == 64 ? 2 : 1) * sms;
+    int csize = 1;
+    while (csize < 8 && tiles * csize * 2 <= room && KB >= csize * 8) csize *= 2;
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    if (!make_map(&maps.x, g.x, g.K, g.M, g.ldx, kTileM) ||
+        !make_map(&maps.w, g.w, g.K, g.gated ? 2LL * g.N : g.N, g.ldw, g.gated ? BN / 2 : BN))
+        return cudaErrorInvalidValue;
+    return launch(linear_tile_kernel<BN>, tiles * csize, kTileThreads, tile_smem_bytes<BN>(), csize,
+                  s, maps, g, csize);
+}
+
+template <int BN>
+cudaError_t launch_pair(const Args& g, int sms, cudaStream_t s) {
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t err[kMaxDevices];
+    cudaError_t e = opt_in(linear_pair_kernel<BN>, pair_smem_bytes<BN>(), once, err);
+    if (e != cudaSuccess) return e;
+    const int per = g.gated ? BN / 2 : BN;
+    const long long tiles = (static_cast<long long>(g.M) + 255) / 256 *
+                            ((static_cast<long long>(g.N) + per - 1) / per);
+    if (tiles > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    if (!make_map(&maps.x, g.x, g.K, g.M, g.ldx, 128) ||
+        !make_map(&maps.w, g.w, g.K, g.gated ? 2LL * g.N : g.N, g.ldw, BN / 2))
+        return cudaErrorInvalidValue;
+    const long long pairs = tiles < sms / 2 ? tiles : sms / 2;
+    return launch(linear_pair_kernel<BN>, pairs * 2, kPairThreads, pair_smem_bytes<BN>(), 2, s, maps,
+                  g);
+}
+
+}  // namespace
+
+cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s) {
+    Args g{};
+    g.M = p.M;
+    g.N = p.N;
+    g.K = p.K;
+    g.act = p.act;
+    g.gated = p.gated;
+    g.x = static_cast<const __nv_bfloat16*>(p.x);
+    g.w = static_cast<const __nv_bfloat16*>(p.w);
+    g.ldx = p.ldx;
+    g.ldw = p.ldw;
+    g.ldr = p.ldr;
+    g.ldo = p.ldo;
+    g.bias = p.bias;
+    g.bias_f32 = p.bias_f32;
+    g.residual = p.residual;
+    g.out = p.out;
+    g.out_f32 = p.out_f32;
+    g.status = p.status;
+    const uintptr_t es = p.out_f32 ? 4 : 2;
+    const uintptr_t bits = reinterpret_cast<uintptr_t>(p.out) | (p.ldo * es) |
+                           (p.residual ? reinterpret_cast<uintptr_t>(p.residual) | (p.ldr * es) : 0);
+    g.vec = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0;
+    const int sms = device_sm_count();
+    if (p.M <= 16) return launch_few(g, sms, s);
+    // large products on CTA pairs, by the waves that 256- and 128-column tiles take
+    const int per = p.gated ? 128 : 256, pairs = sms / 2;
+    const long long tm = (static_cast<long long>(p.M) + 255) / 256;
+    const long long t256 = tm * ((static_cast<long long>(p.N) + per - 1) / per);
+    const long long t128 = tm * ((static_cast<long long>(p.N) + per / 2 - 1) / (per / 2));
+    if (t256 >= pairs) {
+        const long long w256 = (t256 + pairs - 1) / pairs * 2, w128 = (t128 + pairs - 1) / pairs;
+        return w128 * 10 < w256 * 9 ? launch_pair<128>(g, sms, s) : launch_pair<256>(g, sms, s);
+    }
+    return launch_tile<64>(g, sms, s);
+}
+
+}  // namespace moe

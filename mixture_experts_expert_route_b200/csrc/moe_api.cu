@@ -669,6 +669,35 @@ moe_status moe_decode_forward(const moe_decode_args* a, void* ws, size_t ws_byte
     return from_cuda(launch_decode(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream) {
+    if (!a) return MOE_ERR_INVALID_ARG;
+    if (a->M < 0 || a->N < 1 || a->K < 1) return MOE_ERR_INVALID_ARG;
+    if (a->act < MOE_ACT_NONE || a->act > MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
+    if (a->bias_type != MOE_FLOAT_BF16 && a->bias_type != MOE_FLOAT_F32) return MOE_ERR_INVALID_ARG;
+    if (a->out_type != MOE_FLOAT_BF16 && a->out_type != MOE_FLOAT_F32) return MOE_ERR_INVALID_ARG;
+    if (a->K % 8 != 0 || a->ldx % 8 != 0 || a->ldw % 8 != 0) return MOE_ERR_UNSUPPORTED;
+    // rows of W, tile indices and the products' columns are 32-bit
+    if (a->N > (1 << 29) || a->K > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+    if (a->M == 0) return MOE_OK;
+    if (!a->x || !a->w || !a->out) return MOE_ERR_INVALID_ARG;
+    if (a->ldx < a->K || a->ldw < a->K || a->ldo < a->N || (a->residual && a->ldr < a->N))
+        return MOE_ERR_INVALID_ARG;
+    // (a tensor map's row stride is below 2^40 bytes)
+    if (a->ldx > (1LL << 38) || a->ldw > (1LL << 38) || a->ldo > (1LL << 38) || a->ldr > (1LL << 38))
+        return MOE_ERR_UNSUPPORTED;
+    if (!aligned16(a->x) || !aligned16(a->w)) return MOE_ERR_INVALID_ARG;
+    const uintptr_t es = a->out_type == MOE_FLOAT_F32 ? 4 : 2;
+    const uintptr_t bs = a->bias_type == MOE_FLOAT_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(a->out) % es || reinterpret_cast<uintptr_t>(a->residual) % es ||
+        reinterpret_cast<uintptr_t>(a->bias) % bs)
+        return MOE_ERR_INVALID_ARG;
+    const LinearProblem p{a->M, a->N, a->K, a->act, a->gated ? 1 : 0, a->x, a->w, a->ldx, a->ldw,
+                          a->ldr, a->ldo, a->bias, a->bias_type == MOE_FLOAT_F32, a->residual,
+                          a->out, a->out_type == MOE_FLOAT_F32, a->status};
+    Range r("moe_linear");
+    return from_cuda(launch_linear(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 moe_status moe_check_status(const int32_t* dev_status, moe_stream_t stream) {
     if (!dev_status) return MOE_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -199,3 +199,42 @@ def test_decode_binding_refuses_host_tensors(L):
         L.decode_forward(0, x, torch.zeros((2, 8)), x, None, 8, 64, 2)
     with pytest.raises(ValueError):
         L.decode_forward(0, x[0], torch.zeros((2, 8)), x, None, 8, 64, 2)
+
+
+def _linear_args(L, **kw):
+    base = dict(M=4, N=64, K=128, act=0, gated=0, x=0x1000, w=0x1000, ldx=128, ldw=128, bias=None,
+                bias_type=0, residual=None, ldr=0, out=0x1000, ldo=64, out_type=0, status=None)
+    base.update(kw)
+    return L._lib.LinearArgs(*[base[f] for f, _ in L._lib.LinearArgs._fields_])
+
+
+def test_linear_argument_errors(L):
+    lib = L.lib()
+    INVALID, UNSUP = 1, 2
+
+    def call(**kw):
+        return lib.moe_linear(ctypes.byref(_linear_args(L, **kw)), None)
+
+    assert lib.moe_linear(None, None) == INVALID
+    assert call(M=-1) == INVALID and call(N=0) == INVALID and call(K=0) == INVALID
+    assert call(M=0, x=None, out=None) == 0                    # no-op
+    assert call(act=-1) == INVALID and call(act=5) == INVALID
+    assert call(bias_type=2) == INVALID and call(out_type=-1) == INVALID
+    assert call(K=100) == UNSUP                                # K % 8
+    assert call(ldx=132) == UNSUP and call(ldw=130) == UNSUP
+    assert call(ldx=120) == INVALID and call(ldw=64) == INVALID and call(ldo=63) == INVALID
+    assert call(residual=0x1000, ldr=32) == INVALID
+    for name in ("x", "w", "out"):
+        assert call(**{name: None}) == INVALID
+    assert call(x=0x1008) == INVALID and call(w=0x1002) == INVALID
+    assert call(out=0x1001) == INVALID and call(out=0x1002, out_type=1) == INVALID
+    assert call(residual=0x1001, ldr=64) == INVALID
+    assert call(bias=0x1002, bias_type=1) == INVALID
+
+
+def test_linear_binding_refuses(L):
+    x = torch.zeros((2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        L.linear(x, x)                                         # host tensors
+    with pytest.raises(ValueError):
+        L.linear(x[0], x)
