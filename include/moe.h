@@ -374,7 +374,7 @@ MOE_API moe_status moe_decode_forward(const moe_decode_args* args, void* ws, siz
  * GELU_TANH, its tanh form z(1+tanh(sqrt(2/pi)(z+0.044715z^3)))/2.  A NaN stays
  * a NaN through each.
  * K, ldx and ldw are multiples of 8 (16-byte rows), x and w 16-byte aligned;
- * out, residual and bias need their elements' alignment only (32-byte aligned
+ * out, residual and bias need their elements' alignment only (16-byte aligned
  * rows are written fastest).  Bit-reproducible; no workspace.
  * Errors: MOE_ERR_INVALID_ARG for bad sizes, strides, types or pointers,
  * MOE_ERR_UNSUPPORTED for K, ldx or ldw not a multiple of 8.

@@ -57,15 +57,26 @@ __device__ __forceinline__ float load_bias(const Args& g, int row) {
 }
 
 // The activations on fp32 (a NaN stays one).  erff, tanhf and expf are CUDA's,
-// within a few fp32 ulp.
-__device__ __forceinline__ float activate(float z, int act) {
-    switch (act) {
-        case MOE_ACT_RELU: return z < 0.0f ? 0.0f : z;
-        case MOE_ACT_SILU: return z / (1.0f + expf(-z));
-        case MOE_ACT_GELU: return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
-        case MOE_ACT_GELU_TANH:
-            return 0.5f * z * (1.0f + tanhf(0.79788456080286536f * (z + 0.044715f * z * z * z)));
-        default: return z;
+// within a few fp32 ulp.  One branch for all values: with a switch per value the
+// 16 copies of five activations' code left a CTA pair's epilogue waiting for
+// instructions, 19 us a tile with no activation at all.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+    if (act == MOE_ACT_NONE) return;
+    if (act == MOE_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
+    } else if (act == MOE_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = v[i] / (1.0f + expf(-v[i]));
+    } else if (act == MOE_ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678118654752f));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] = 0.5f * v[i] *
+                   (1.0f + tanhf(0.79788456080286536f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
     }
 }
 
@@ -193,8 +204,9 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
 // ================================================================= few
 // A warp takes 16 weight rows (gated: 8 gate rows and their 8 up rows) and a
 // range of 64-column steps of K.  m16n8k16 MMAs, tokens in M; the K order
-// inside a step is permuted the same way for both operands, so that lane (g, t)
-// reads 32 consecutive bytes of each of its rows.
+// inside a step is permuted the same way for both operands: lane (g, t) reads
+// 16-byte pieces t and t + 4 of its rows, so that each load of a warp covers
+// whole 32-byte sectors.
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
 
@@ -210,7 +222,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
 // Weights are read once: past L1.
 __device__ __forceinline__ uint4 ld_stream(const uint4* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+    asm("ld.global.nc.L1::no_allocate.L2::256B.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
@@ -241,54 +253,68 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     const int s0 = static_cast<int>(static_cast<long long>(steps) * part / parts);
     const int s1 = static_cast<int>(static_cast<long long>(steps) * (part + 1) / parts);
 
-    // this lane's rows; rows and tokens past the end read nothing
+    // this lane's rows.  Rows and tokens past the end read row 0: what they give
+    // is in columns and rows of the result that nobody looks at.
     const int c0 = col0 + gq, c1 = g.gated ? col0 + gq : col0 + 8 + gq;
-    const bool ok0 = c0 < g.N, ok1 = c1 < g.N;
-    const __nv_bfloat16* w0 = g.w + (ok0 ? static_cast<long long>(c0) * g.ldw : 0) + 16 * t;
+    const __nv_bfloat16* w0 = g.w + (c0 < g.N ? c0 : 0) * g.ldw + 8 * t;
     const __nv_bfloat16* w1 =
-        g.w + (ok1 ? (g.gated ? static_cast<long long>(g.N) + c1 : c1) * g.ldw : 0) + 16 * t;
+        g.w + (c1 < g.N ? (g.gated ? static_cast<long long>(g.N) + c1 : c1) : 0) * g.ldw + 8 * t;
     const __nv_bfloat16* xr[MB];
-    bool okx[MB];
 #pragma unroll
-    for (int m = 0; m < MB; ++m) {
-        okx[m] = m * 8 + gq < g.M;
-        xr[m] = g.x + (okx[m] ? static_cast<long long>(m * 8 + gq) * g.ldx : 0) + 16 * t;
-    }
-    const uint4 zero = make_uint4(0, 0, 0, 0);
+    for (int m = 0; m < MB; ++m)
+        xr[m] = g.x + (m * 8 + gq < g.M ? m * 8 + gq : 0) * g.ldx + 8 * t;
     auto load = [&](Step<MB>& st, int s) {
+        const long long k = static_cast<long long>(s) * kBK;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            const long long k = static_cast<long long>(s) * kBK + 8 * p;
-            const bool in = s < s1 && k + 16 * t < g.K;      // K is a multiple of 8
-            st.w[0][p] = in && ok0 ? ld_stream(reinterpret_cast<const uint4*>(w0 + k)) : zero;
-            st.w[1][p] = in && ok1 ? ld_stream(reinterpret_cast<const uint4*>(w1 + k)) : zero;
+            st.w[0][p] = ld_stream(reinterpret_cast<const uint4*>(w0 + k + 32 * p));
+            st.w[1][p] = ld_stream(reinterpret_cast<const uint4*>(w1 + k + 32 * p));
 #pragma unroll
             for (int m = 0; m < MB; ++m)
-                st.x[m][p] = in && okx[m] ? __ldg(reinterpret_cast<const uint4*>(xr[m] + k)) : zero;
+                st.x[m][p] = __ldg(reinterpret_cast<const uint4*>(xr[m] + k + 32 * p));
         }
     };
+    const uint4 zero = make_uint4(0, 0, 0, 0);
     float acc[2][4] = {};
     auto mul = [&](const Step<MB>& st) {
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const uint4 a = st.x[0][p], b = MB > 1 ? st.x[MB - 1][p] : zero;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < 2; ++n)
                 mma_bf16(acc[n], a.x, b.x, a.y, b.y, st.w[n][p].x, st.w[n][p].y);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
                 mma_bf16(acc[n], a.z, b.z, a.w, b.w, st.w[n][p].z, st.w[n][p].w);
-            }
         }
     };
     constexpr int DEPTH = MB == 1 ? 4 : 3;    // steps of loads in flight per warp
     Step<MB> ring[DEPTH];
+    const int full = min(s1, g.K / kBK);      // whole steps of this warp: [s0, full)
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) load(ring[d], s0 + d);
-    for (int s = s0; s < s1; s += DEPTH) {
+    for (int d = 0; d < DEPTH; ++d)
+        if (s0 + d < full) load(ring[d], s0 + d);
+    for (int s = s0; s < full; s += DEPTH) {
 #pragma unroll
         for (int d = 0; d < DEPTH; ++d) {
-            mul(ring[d]);                     // (past the range: zeros)
-            load(ring[d], s + d + DEPTH);
+            if (s + d < full) mul(ring[d]);
+            if (s + d + DEPTH < full) load(ring[d], s + d + DEPTH);
         }
+    }
+    if (s1 > full && s1 > s0) {
+        // the last step has K % 64 columns, whole 16-byte pieces of them
+        const long long k = static_cast<long long>(s1 - 1) * kBK;
+        Step<MB> st;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const bool in = k + 32 * p + 8 * t < g.K;
+            st.w[0][p] = in ? ld_stream(reinterpret_cast<const uint4*>(w0 + k + 32 * p)) : zero;
+            st.w[1][p] = in ? ld_stream(reinterpret_cast<const uint4*>(w1 + k + 32 * p)) : zero;
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+                st.x[m][p] = in ? __ldg(reinterpret_cast<const uint4*>(xr[m] + k + 32 * p)) : zero;
+        }
+        mul(st);
     }
 
     // sums over the warps that share the rows, in order, then over the cluster
@@ -327,9 +353,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 if (g.gated) up += ld_cluster(cluster_addr(a + 32, r));
             }
         }
-        z = activate(z + load_bias(g, col), g.act);
-        if (g.gated) z *= up + load_bias(g, g.N + col);
-        store_one(g, m, col, z);
+        float v[1] = {z + load_bias(g, col)};
+        activate(v, g.act);
+        if (g.gated) v[0] *= up + load_bias(g, g.N + col);
+        store_one(g, m, col, v[0]);
     }
     if (csize > 1) cluster_sync();     // peers may still be reading this block's sums
 }
@@ -342,19 +369,20 @@ struct Maps {
 
 constexpr int kTileThreads = 256;
 constexpr int kTileM = 128;
-constexpr int kTileStages = 4;
+// two blocks fit on an SM
+template <int BN> __host__ __device__ constexpr int tile_stages() { return BN == 64 ? 4 : 3; }
 
 template <int BN>
 __host__ __device__ constexpr int tile_stage_bytes() { return (kTileM + BN) * kRowBytes; }
 template <int BN>
 __host__ __device__ constexpr int tile_smem_bytes() {
-    const int ring = kTileStages * tile_stage_bytes<BN>(), acc = kTileM * (BN + 4) * 4;
+    const int ring = tile_stages<BN>() * tile_stage_bytes<BN>(), acc = kTileM * (BN + 4) * 4;
     return 1024 + (ring > acc ? ring : acc);
 }
 
 struct TileCtl {
-    uint64_t full[kTileStages];
-    uint64_t empty[kTileStages];
+    uint64_t full[4];
+    uint64_t empty[4];
     uint64_t done;
     uint32_t tmem;
     int abort;
@@ -362,13 +390,13 @@ struct TileCtl {
 };
 
 template <int BN>
-__global__ void __launch_bounds__(kTileThreads)
+__global__ void __launch_bounds__(kTileThreads, 2)
     linear_tile_kernel(const __grid_constant__ Maps maps, const Args g, int csize) {
     extern __shared__ uint8_t dsmem_raw[];
     __shared__ TileCtl ctl;
     uint8_t* base = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    constexpr int STAGE = tile_stage_bytes<BN>(), S = kTileStages;
+    constexpr int STAGE = tile_stage_bytes<BN>(), S = tile_stages<BN>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = csize > 1 ? cluster_ctarank() : 0;
     if (threadIdx.x == 0) {
@@ -515,11 +543,15 @@ __global__ void __launch_bounds__(kTileThreads)
         }
         float zz[4] = {z.x, z.y, z.z, z.w};
         const float uu[4] = {up.x, up.y, up.z, up.w};
+        if (g.bias) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int cc = min(col + i, g.N - 1);
-            zz[i] = activate(zz[i] + load_bias(g, cc), g.act);
-            if (g.gated) zz[i] *= uu[i] + load_bias(g, g.N + cc);
+            for (int i = 0; i < 4; ++i) zz[i] += load_bias(g, min(col + i, g.N - 1));
+        }
+        activate(zz, g.act);
+        if (g.gated) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                zz[i] *= uu[i] + (g.bias ? load_bias(g, g.N + min(col + i, g.N - 1)) : 0.0f);
         }
         store4(g, m0 + r, col, make_float4(zz[0], zz[1], zz[2], zz[3]));
     }
@@ -715,8 +747,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (g.gated) tmem_wait16(r1);
                 float v[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    v[j] = activate(__uint_as_float(r0[j]) + bias[c + j], g.act);
+                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r0[j]) + bias[c + j];
+                activate(v, g.act);
                 if (g.gated) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
@@ -843,11 +875,10 @@ cudaError_t launch_tile(const Args& g, int sms, cudaStream_t s) {
     const long long tiles = (static_cast<long long>(g.M) + kTileM - 1) / kTileM *
                             ((static_cast<long long>(g.N) + per - 1) / per);
     const int KB = (g.K + kBK - 1) / kBK;
-    // blocks of a cluster split K while there is room for them on the SMs (two
-    // blocks each at BN = 64) and each keeps at least 4 k-blocks
-    const int room = (BN == 64 ? 2 : 1) * sms;
+    // blocks of a cluster split K while all find room on the SMs, two each, and
+    // each keeps at least 4 k-blocks
     int csize = 1;
-    while (csize < 8 && tiles * csize * 2 <= room && KB >= csize * 8) csize *= 2;
+    while (csize < 8 && tiles * csize * 2 <= 2 * sms && KB >= csize * 8) csize *= 2;
     Maps maps;
     memset(&maps, 0, sizeof(maps));
     if (!make_map(&maps.x, g.x, g.K, g.M, g.ldx, kTileM) ||
@@ -904,15 +935,12 @@ cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s) {
     g.vec = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0;
     const int sms = device_sm_count();
     if (p.M <= 16) return launch_few(g, sms, s);
-    // large products on CTA pairs, by the waves that 256- and 128-column tiles take
-    const int per = p.gated ? 128 : 256, pairs = sms / 2;
-    const long long tm = (static_cast<long long>(p.M) + 255) / 256;
-    const long long t256 = tm * ((static_cast<long long>(p.N) + per - 1) / per);
-    const long long t128 = tm * ((static_cast<long long>(p.N) + per / 2 - 1) / (per / 2));
-    if (t256 >= pairs) {
-        const long long w256 = (t256 + pairs - 1) / pairs * 2, w128 = (t128 + pairs - 1) / pairs;
-        return w128 * 10 < w256 * 9 ? launch_pair<128>(g, sms, s) : launch_pair<256>(g, sms, s);
-    }
+    // CTA pairs once there is a 256 x 256 tile for each pair of SMs
+    const int per = p.gated ? 128 : 256;
+    const long long t256 = (static_cast<long long>(p.M) + 255) / 256 *
+                           ((static_cast<long long>(p.N) + per - 1) / per);
+    if (t256 >= sms / 2) return launch_pair<256>(g, sms, s);
+    if (p.M > 128) return launch_tile<128>(g, sms, s);
     return launch_tile<64>(g, sms, s);
 }
 
