@@ -352,19 +352,19 @@ def _on_device(dev: torch.device, stream=None):
     return torch.cuda.device(dev)
 
 
-def _take(t, name, shape, dtype, dev):
-    """Checks an argument tensor of the decode and linear entry points."""
+def _take(t, name, shape, dtype, idx):
+    """Address of an optional contiguous argument tensor of the decode entry point, checked."""
     if t is None:
         return None
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, expected {dev}")
-    if t.dtype != dtype:
+    if t.get_device() != idx:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{idx}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    return t
+    return t.data_ptr()
 
 
 def decode_workspace(dtype: int, T: int, k: int, E: int, H: int, I: int, device,
@@ -386,55 +386,55 @@ def decode_forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int
     """The whole layer for T <= 16 tokens (T * k <= 128) in one kernel:
     out = residual + sum_j w_j * FFN_{id_j}(x).  ``ws`` comes from decode_workspace
     and is reused from call to call (None: a new one for this call)."""
+    idx = x.get_device()
+    if idx < 0:
+        raise ValueError("expected a CUDA tensor")
     if x.dim() != 2:
         raise ValueError("x: expected [T, H]")
+    if stream is not None or idx != torch._C._cuda_getDevice():
+        with _on_device(x.device, stream):
+            return decode_forward(dtype, x, logits, packed, scales, E, I, k, residual, out, ids,
+                                  w, status, ws)
     T, H = x.shape
-    dev = x.device
-    if not x.is_cuda:
-        raise ValueError("expected a CUDA tensor")
     bf16, f32 = torch.bfloat16, torch.float32
-    _take(x, "x", (T, H), bf16, dev)
-    _take(logits, "logits", (T, E), f32, dev)
-    _take(residual, "residual", (T, H), bf16, dev)
-    _take(out, "out", (T, H), bf16, dev)
-    _take(ids, "ids", (T, k), torch.int32, dev)
-    _take(w, "w", (T, k), f32, dev)
-    _take(scales, "scales", (E, 3), f32, dev)
-    if packed.device != dev or (status is not None and status.device != dev):
-        raise ValueError(f"packed and status: expected on {dev}")
+    for t, name in ((packed, "packed"), (status, "status"), (ws, "ws")):
+        if t is not None and t.get_device() != idx:
+            raise ValueError(f"{name}: on {t.device}, expected cuda:{idx}")
     if packed.numel() < lib().moe_packed_weights_size(dtype, E, H, I):
         raise ValueError("packed: smaller than these sizes need")
-    with _on_device(dev, stream):
-        out = torch.empty((T, H), dtype=bf16, device=dev) if out is None else out
-        if ws is None and T > 0:
-            ws = decode_workspace(dtype, T, k, E, H, I, dev)
-        elif ws is not None and ws.device != dev:
-            raise ValueError(f"ws: on {ws.device}, expected {dev}")
-        a = DecodeArgs(dtype, T, k, E, H, I, x.data_ptr(), logits.data_ptr(),
-                       packed.data_ptr(), _ptr(scales), _ptr(residual), out.data_ptr(),
-                       _ptr(ids), _ptr(w), _ptr(status))
-        _check(lib().moe_decode_forward(ctypes.byref(a), _ptr(ws),
-                                        0 if ws is None else ws.numel(), _stream(stream)),
-               "moe_decode_forward")
+    if out is None:
+        out = x.new_empty((T, H))
+    if ws is None and T > 0:
+        ws = decode_workspace(dtype, T, k, E, H, I, x.device)
+    a = DecodeArgs(dtype, T, k, E, H, I, _take(x, "x", (T, H), bf16, idx),
+                   _take(logits, "logits", (T, E), f32, idx), packed.data_ptr(),
+                   _take(scales, "scales", (E, 3), f32, idx),
+                   _take(residual, "residual", (T, H), bf16, idx),
+                   _take(out, "out", (T, H), bf16, idx), _take(ids, "ids", (T, k), torch.int32, idx),
+                   _take(w, "w", (T, k), f32, idx), None if status is None else status.data_ptr())
+    code = lib().moe_decode_forward(ctypes.byref(a), None if ws is None else ws.data_ptr(),
+                                    0 if ws is None else ws.numel(),
+                                    torch._C._cuda_getCurrentRawStream(idx))
+    if code:
+        raise MoEError(code, "moe_decode_forward")
     return out
 
 
 _FLOAT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 
-def _rows(t, name, shape, dtype, dev):
+def _rows(t, name, rows, cols, dtype, idx):
     """Checks a matrix argument of linear (rows may be apart) and returns its row stride."""
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, expected {dev}")
-    if t.dtype != dtype:
+    if t.get_device() != idx:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{idx}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
-    rs, cs = t.stride()
-    if cs != 1 and shape[1] > 1:
+    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: columns must be contiguous")
     # the stride of a single row is of no account
-    return rs if shape[0] > 1 else (shape[1] + 7) // 8 * 8
+    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
 
 
 def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=None, out=None,
@@ -444,36 +444,48 @@ def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=N
     x bf16 [M, K] and w bf16 [N, K] (gated: [2N, K], gate rows then up rows), rows any multiple
     of 8 elements apart; bias bf16 or f32 [rows of w]; residual and out of ``out_dtype`` (bf16,
     the default, or f32).  ``out`` may be the residual."""
+    idx = x.get_device()
+    if idx < 0:
+        raise ValueError("expected a CUDA tensor")
     if x.dim() != 2 or w.dim() != 2:
         raise ValueError("x and w: expected [M, K] and [N, K]")
-    if not x.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    dev, bf16 = x.device, torch.bfloat16
+    if stream is not None or idx != torch._C._cuda_getDevice():
+        with _on_device(x.device, stream):
+            return linear(x, w, bias, act, gated, residual, out, out_dtype, status)
     M, K = x.shape
-    rows = w.shape[0]
+    rows = w.size(0)
     if gated and rows % 2:
         raise ValueError("w: a gated product has an even number of rows")
     N = rows // 2 if gated else rows
     if out_dtype is None:
-        out_dtype = out.dtype if out is not None else bf16
-    if out_dtype not in _FLOAT_TYPE:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    out_type = _FLOAT_TYPE.get(out_dtype)
+    if out_type is None:
         raise ValueError(f"out_dtype: {out_dtype}, expected bfloat16 or float32")
-    ldx = _rows(x, "x", (M, K), bf16, dev)
-    ldw = _rows(w, "w", (rows, K), bf16, dev)
-    bias_type = 0
+    ldx = _rows(x, "x", M, K, torch.bfloat16, idx)
+    ldw = _rows(w, "w", rows, K, torch.bfloat16, idx)
+    bias_type, bias_p, ldr, res_p = 0, None, 0, None
     if bias is not None:
-        if bias.dtype not in _FLOAT_TYPE:
+        bias_type = _FLOAT_TYPE.get(bias.dtype)
+        if bias_type is None:
             raise ValueError(f"bias: {bias.dtype}, expected bfloat16 or float32")
-        bias_type = _FLOAT_TYPE[bias.dtype]
-        _take(bias, "bias", (rows,), bias.dtype, dev)
-    ldr = _rows(residual, "residual", (M, N), out_dtype, dev) if residual is not None else 0
-    with _on_device(dev, stream):
-        out = torch.empty((M, N), dtype=out_dtype, device=dev) if out is None else out
-        ldo = _rows(out, "out", (M, N), out_dtype, dev)
-        a = LinearArgs(M, N, K, act, 1 if gated else 0, x.data_ptr(), w.data_ptr(), ldx, ldw,
-                       _ptr(bias), bias_type, _ptr(residual), ldr, out.data_ptr(), ldo,
-                       _FLOAT_TYPE[out_dtype], _ptr(status))
-        _check(lib().moe_linear(ctypes.byref(a), _stream(stream)), "moe_linear")
+        if bias.get_device() != idx or bias.dim() != 1 or bias.size(0) != rows \
+                or (rows > 1 and bias.stride(0) != 1):
+            raise ValueError(f"bias: expected [{rows}], contiguous, on cuda:{idx}")
+        bias_p = bias.data_ptr()
+    if residual is not None:
+        ldr = _rows(residual, "residual", M, N, out_dtype, idx)
+        res_p = residual.data_ptr()
+    if out is None:
+        out, ldo = x.new_empty((M, N), dtype=out_dtype), N
+    else:
+        ldo = _rows(out, "out", M, N, out_dtype, idx)
+    a = LinearArgs(M, N, K, act, 1 if gated else 0, x.data_ptr(), w.data_ptr(), ldx, ldw, bias_p,
+                   bias_type, res_p, ldr, out.data_ptr(), ldo, out_type,
+                   None if status is None else status.data_ptr())
+    code = lib().moe_linear(ctypes.byref(a), torch._C._cuda_getCurrentRawStream(idx))
+    if code:
+        raise MoEError(code, "moe_linear")
     return out
 
 
@@ -527,22 +539,22 @@ class MoELayer:
             return decode_workspace(self.dtype, T, self.k, self.E, self.H, self.I,
                                     self.device, stream)
         key = _stream(stream)
-        n = lib().moe_decode_workspace_size(self.dtype, T, self.k, self.E, self.H, self.I)
-        ws = self._decode_ws.get(key)
-        if ws is None or ws.numel() < n:
+        ws, room = self._decode_ws.get(key, (None, 0))
+        if T > room:
             ws = decode_workspace(self.dtype, T, self.k, self.E, self.H, self.I, self.device,
                                   stream)
-            self._decode_ws[key] = ws
+            self._decode_ws[key] = (ws, T)
         return ws
 
     def decode(self, x, logits, residual=None, out=None, ids=None, w=None, stream=None):
         """The layer for a few tokens in one kernel (see decode_forward)."""
+        if stream is not None or self.device.index != torch._C._cuda_getDevice():
+            with _on_device(self.device, stream):
+                return self.decode(x, logits, residual, out, ids, w)
         T = x.shape[0]
-        with _on_device(self.device, stream):
-            ws = self.decode_workspace(T, stream) if T > 0 else None
-            return decode_forward(self.dtype, x, logits, self.packed, self.scales, self.E,
-                                  self.I, self.k, residual=residual, out=out, ids=ids, w=w,
-                                  status=self.status, ws=ws, stream=stream)
+        return decode_forward(self.dtype, x, logits, self.packed, self.scales, self.E, self.I,
+                              self.k, residual, out, ids, w, self.status,
+                              self.decode_workspace(T) if T > 0 else None)
 
     def check(self) -> int:
         return check_status(self.status)

@@ -56,10 +56,18 @@ __device__ __forceinline__ float load_bias(const Args& g, int row) {
                       : __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(g.bias) + row));
 }
 
-// The activations on fp32 (a NaN stays one).  erff, tanhf and expf are CUDA's,
-// within a few fp32 ulp.  One branch for all values: with a switch per value the
-// 16 copies of five activations' code left a CTA pair's epilogue waiting for
-// instructions, 19 us a tile with no activation at all.
+// z / (1 + e^-y) with the fast exponential and division: off by a few fp32 ulp
+// where it counts (the exponential's error grows with |y|, but then the factor
+// is near 0 or 1), and a NaN, 0 or z at the ends as the exact form.
+__device__ __forceinline__ float times_sigmoid(float z, float y) {
+    return __fdividef(z, 1.0f + __expf(-y));
+}
+
+// The activations on fp32 (a NaN stays one).  GELU's tanh form is
+// z (1 + tanh u) / 2 = z / (1 + e^-2u), which cancels nothing.  One branch for
+// all of a thread's values: with a switch per value the 16 copies of five
+// activations' code left a CTA pair's epilogue waiting for instructions, 19 us a
+// tile with no activation at all; with IEEE divisions SiLU took 15 us a tile.
 template <int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act) {
     if (act == MOE_ACT_NONE) return;
@@ -68,15 +76,15 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
         for (int i = 0; i < N; ++i) v[i] = v[i] < 0.0f ? 0.0f : v[i];
     } else if (act == MOE_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = v[i] / (1.0f + expf(-v[i]));
+        for (int i = 0; i < N; ++i) v[i] = times_sigmoid(v[i], v[i]);
     } else if (act == MOE_ACT_GELU) {
 #pragma unroll
         for (int i = 0; i < N; ++i) v[i] = 0.5f * v[i] * (1.0f + erff(v[i] * 0.70710678118654752f));
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            v[i] = 0.5f * v[i] *
-                   (1.0f + tanhf(0.79788456080286536f * (v[i] + 0.044715f * v[i] * v[i] * v[i])));
+            v[i] = times_sigmoid(
+                v[i], 1.5957691216057308f * (v[i] + 0.044715f * v[i] * v[i] * v[i]));
     }
 }
 
@@ -112,36 +120,47 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&r)[8]) {
                  : "memory");
 }
 
-// 16 consecutive columns of one row, from column col (a multiple of 16).
-__device__ __forceinline__ void store16(const Args& g, long long row, int col, float (&v)[16]) {
-    if (g.vec != 32 || col + 16 > g.N) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (col + i < g.N) store_one(g, row, col + i, v[i]);
-        return;
+// 16 consecutive columns of one row, from column col (a multiple of 16), whole
+// 32-byte sectors at a time; `res` holds the residual's (see res16).
+__device__ __forceinline__ bool wide16(const Args& g, int col) {
+    return g.vec == 32 && col + 16 <= g.N;
+}
+__device__ __forceinline__ void res16(const Args& g, long long row, int col, uint32_t (&a)[8],
+                                      uint32_t (&b)[8]) {
+    if (g.out_f32) {
+        const float* p = static_cast<const float*>(g.residual) + row * g.ldr + col;
+        ld32(p, a);
+        ld32(p + 8, b);
+    } else {
+        ld32(static_cast<const __nv_bfloat16*>(g.residual) + row * g.ldr + col, a);
     }
+}
+__device__ __forceinline__ void add_res16(const Args& g, float (&v)[16], const uint32_t (&a)[8],
+                                          const uint32_t (&b)[8]) {
+    if (g.out_f32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] += __uint_as_float(a[i]);
+            v[8 + i] += __uint_as_float(b[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[2 * i] += bf16_lo(a[i]);
+            v[2 * i + 1] += bf16_hi(a[i]);
+        }
+    }
+}
+__device__ __forceinline__ void store16(const Args& g, long long row, int col, const float (&v)[16]) {
     uint32_t r[8];
     if (g.out_f32) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (g.residual) {
-                ld32(static_cast<const float*>(g.residual) + row * g.ldr + col + 8 * h, r);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[8 * h + i] += __uint_as_float(r[i]);
-            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(v[8 * h + i]);
             st32(static_cast<float*>(g.out) + row * g.ldo + col + 8 * h, r);
         }
     } else {
-        if (g.residual) {
-            ld32(static_cast<const __nv_bfloat16*>(g.residual) + row * g.ldr + col, r);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[2 * i] += bf16_lo(r[i]);
-                v[2 * i + 1] += bf16_hi(r[i]);
-            }
-        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
         st32(static_cast<__nv_bfloat16*>(g.out) + row * g.ldo + col, r);
@@ -288,7 +307,9 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                 mma_bf16(acc[n], a.z, b.z, a.w, b.w, st.w[n][p].z, st.w[n][p].w);
         }
     };
-    constexpr int DEPTH = MB == 1 ? 4 : 3;    // steps of loads in flight per warp
+    // steps of loads in flight per warp: as many as the registers hold (one more
+    // spilled, and took 27 us instead of 23 at M = 16, K = 14336, N = 4096)
+    constexpr int DEPTH = MB == 1 ? 3 : 2;
     Step<MB> ring[DEPTH];
     const int full = min(s1, g.K / kBK);      // whole steps of this warp: [s0, full)
 #pragma unroll
@@ -581,7 +602,7 @@ struct PairCtl {
     uint32_t tmem;
     int abort;
     uint32_t prod_pos, mma_pos, mma_issued;
-    float bias[2][BN];
+    alignas(16) float bias[2][BN];
 };
 
 // Tile t of the rasterised order: groups of 8 row tiles, in a group column tile
@@ -731,30 +752,75 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     c < g.N ? load_bias(g, g.gated && et >= BN / 2 ? g.N + c : c) : 0.0f;
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");
+            const long long row = static_cast<long long>(m) * 256 + rank * 128 + 32 * q + lane;
+            const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * BN;
+            const float4* bias = reinterpret_cast<const float4*>(ctl.bias[acc]);
+            const int span = per / 2;         // this warp's output columns
+            const int cb = half * span, ce = min((half + 1) * span, g.N - n0);
+            uint32_t qa[8], qb[8];
+            const bool res = g.residual != nullptr && row < g.M;
+            if (cb < ce && res && wide16(g, n0 + cb)) res16(g, row, n0 + cb, qa, qb);
             // (after a fault the waits return at once and the loop runs on, so
             // that all epilogue warps meet at the same barriers)
             if (!mbar_wait(&ctl.tfull[acc], (i >> 1) & 1u, &ctl.abort)) raise();
             tc_fence_after();
-            const long long row = static_cast<long long>(m) * 256 + rank * 128 + 32 * q + lane;
-            const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16) + acc * BN;
-            const float* bias = ctl.bias[acc];
-            const int span = per / 2;         // this warp's output columns
-            for (int c = half * span; c < (half + 1) * span; c += 16) {
-                uint32_t r0[16], r1[16];
-                tmem_ld16_async(ta + c, r0);
-                if (g.gated) tmem_ld16_async(ta + BN / 2 + c, r1);
+            // 16 columns at a time; the next ones' accumulators and residual are
+            // on their way while these are worked on
+            uint32_t r0[16], r1[16];
+            if (cb < ce) {
+                tmem_ld16_async(ta + cb, r0);
+                if (g.gated) tmem_ld16_async(ta + BN / 2 + cb, r1);
+            }
+            for (int c = cb; c < ce; c += 16) {
                 tmem_wait16(r0);
                 if (g.gated) tmem_wait16(r1);
-                float v[16];
+                float v[16], u[16], w[16];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r0[j]) + bias[c + j];
+                for (int j = 0; j < 4; ++j) {
+                    const float4 b = bias[c / 4 + j];
+                    v[4 * j] = __uint_as_float(r0[4 * j]) + b.x;
+                    v[4 * j + 1] = __uint_as_float(r0[4 * j + 1]) + b.y;
+                    v[4 * j + 2] = __uint_as_float(r0[4 * j + 2]) + b.z;
+                    v[4 * j + 3] = __uint_as_float(r0[4 * j + 3]) + b.w;
+                }
+                if (g.gated) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 b = bias[(BN / 2 + c) / 4 + j];
+                        u[4 * j] = __uint_as_float(r1[4 * j]) + b.x;
+                        u[4 * j + 1] = __uint_as_float(r1[4 * j + 1]) + b.y;
+                        u[4 * j + 2] = __uint_as_float(r1[4 * j + 2]) + b.z;
+                        u[4 * j + 3] = __uint_as_float(r1[4 * j + 3]) + b.w;
+                    }
+                }
+                const bool wide = wide16(g, n0 + c);
+                if (res && wide) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = 0.0f;
+                    add_res16(g, w, qa, qb);
+                }
+                if (c + 16 < ce) {
+                    tmem_ld16_async(ta + c + 16, r0);
+                    if (g.gated) tmem_ld16_async(ta + BN / 2 + c + 16, r1);
+                    if (res && wide16(g, n0 + c + 16)) res16(g, row, n0 + c + 16, qa, qb);
+                }
                 activate(v, g.act);
                 if (g.gated) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        v[j] *= __uint_as_float(r1[j]) + bias[BN / 2 + c + j];
+                    for (int j = 0; j < 16; ++j) v[j] *= u[j];
                 }
-                if (row < g.M && n0 + c < g.N) store16(g, row, n0 + c, v);
+                if (row >= g.M) continue;
+                if (wide) {
+                    if (res) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] += w[j];
+                    }
+                    store16(g, row, n0 + c, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (n0 + c + j < g.N) store_one(g, row, n0 + c + j, v[j]);
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -935,12 +1001,19 @@ cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s) {
     g.vec = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 0;
     const int sms = device_sm_count();
     if (p.M <= 16) return launch_few(g, sms, s);
-    // CTA pairs once there is a 256 x 256 tile for each pair of SMs
+    // Measured on B200 (us, pair / 128-wide / 64-wide tiles): M = 1024, K = N =
+    // 4096 (64 pair tiles) 32 / 44 / 61; M = 512, K = 7168, N = 2 x 2048 (32) 43 /
+    // 34 / 42; M = 128, K = 4096, N = 2 x 14336 54 / 50 / 62; M = 300, K = N = 2880
+    // (69 128-wide tiles) 23 / 15 / 14; M = 4096, K = 2048, N = 128 (32) 15 / 13 /
+    // 10.  So: pairs once half of them have a tile and its 256 rows are not half
+    // empty; else 128-wide tiles once there is one for every second SM.
     const int per = p.gated ? 128 : 256;
     const long long t256 = (static_cast<long long>(p.M) + 255) / 256 *
                            ((static_cast<long long>(p.N) + per - 1) / per);
-    if (t256 >= sms / 2) return launch_pair<256>(g, sms, s);
-    if (p.M > 128) return launch_tile<128>(g, sms, s);
+    if (p.M > 128 && t256 * 4 >= sms) return launch_pair<256>(g, sms, s);
+    const long long t128 = (static_cast<long long>(p.M) + 127) / 128 *
+                           ((static_cast<long long>(p.N) + per / 2 - 1) / (per / 2));
+    if (t128 * 2 >= sms) return launch_tile<128>(g, sms, s);
     return launch_tile<64>(g, sms, s);
 }
 
