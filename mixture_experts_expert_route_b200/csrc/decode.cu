@@ -126,8 +126,13 @@ struct Shared {
     int expert[kDecodeMaxAssign];       // active experts, ascending
     int base[kDecodeMaxAssign + 1];     // first column of an active expert
     int tok[kDecodeMaxAssign];          // column -> token
-    int first2[kDecodeMaxAssign];       // first CTA of an expert's down tiles
-    int ncta2[kDecodeMaxAssign];        // and how many
+    // an assignment's terms of the final sums: the first CTA with down tiles of
+    // its expert and how many there are, the column of its first partial sum,
+    // the expert's token count; the expert's first down tile, and the weight
+    // (with e4m3's down scale)
+    int4 term[kDecodeMaxAssign];
+    int term_tile[kDecodeMaxAssign];
+    float term_w[kDecodeMaxAssign];
     int start1[kMaxCtas + 1];           // first gate/up tile of each CTA
     int start2[kMaxCtas + 1];           // first down tile of each CTA
     int mod2[kMaxCtas];                 // its row tile
@@ -241,8 +246,7 @@ __device__ __forceinline__ bool grid_barrier(uint64_t* counter, uint64_t target)
     }
 }
 
-// One lane's part of a tile: D[16 tokens][32 weight rows of this warp] += act x W,
-// as four blocks of 8 weight rows.  The K order inside a 128-byte row is
+// One lane's part of a tile: 32 weight rows of this warp by 16 tokens.  The K order inside a 128-byte row is
 // permuted the same way for both operands: lane (g, t) takes 16-byte pieces 2t
 // and 2t+1 of weight row g of each block, whose swizzled places are
 // conflict-free for a quarter warp, and the matching 32 (bf16) or 64 (f16, for
@@ -273,35 +277,61 @@ __device__ __forceinline__ void load_act(Act<FP8>& a, const uint8_t* row, int t,
         for (int q = 0; q < N; ++q) a.v[q] = lds16(row + t * (N * 16) + q * 16);
 }
 
-// a: rows g, b: rows g + 8
-template <bool FP8>
-__device__ __forceinline__ void tile_mma(float (&acc)[4][4], const Wts& w, const Act<FP8>& a,
-                                         const Act<FP8>& b) {
+// bf16: D[16 tokens][32 weight rows of this warp] += act x W, four blocks of 8
+// weight rows in N; a: token rows g, b: token rows g + 8 (or h's low parts).
+__device__ __forceinline__ void tile_mma(float (&acc)[4][4], const Wts& w, const Act<false>& a,
+                                         const Act<false>& b, bool) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            mma_bf16(acc[n], a.v[p].x, b.v[p].x, a.v[p].y, b.v[p].y, w.v[n][p].x, w.v[n][p].y);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+            mma_bf16(acc[n], a.v[p].z, b.v[p].z, a.v[p].w, b.v[p].w, w.v[n][p].z, w.v[n][p].w);
+    }
+}
+
+// e4m3: D[32 weight rows][8 tokens] += W x act, two blocks of 16 weight rows in M
+// (the widened codes land in the registers that M wants), 8 tokens in N; acc[b]
+// for tokens 0..7, acc[2 + b] for 8..15 (`many`).  Word q of 4 codes meets 8
+// bytes of the token rows.
+__device__ __forceinline__ void tile_mma(float (&acc)[4][4], const Wts& w, const Act<true>& a,
+                                         const Act<true>& b, bool many) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        const uint4 x = a.v[q >> 1], y = b.v[q >> 1];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const uint4 c0 = w.v[2 * m][q >> 2], c1 = w.v[2 * m + 1][q >> 2];
+            uint32_t f0, f1, f2, f3;
+            e4m3x4_to_f16x4((q & 3) == 0 ? c0.x : (q & 3) == 1 ? c0.y : (q & 3) == 2 ? c0.z : c0.w,
+                            f0, f2);
+            e4m3x4_to_f16x4((q & 3) == 0 ? c1.x : (q & 3) == 1 ? c1.y : (q & 3) == 2 ? c1.z : c1.w,
+                            f1, f3);
+            mma_f16(acc[m], f0, f1, f2, f3, (q & 1) ? x.z : x.x, (q & 1) ? x.w : x.y);
+            if (many)
+                mma_f16(acc[2 + m], f0, f1, f2, f3, (q & 1) ? y.z : y.x, (q & 1) ? y.w : y.y);
+        }
+    }
+}
+
+// A lane's sums by (token, weight row of the warp's 32): calls f(token, row, v0,
+// v1), bf16 with two weight rows (row, row + 1), e4m3 with one (v0).
+template <bool FP8, class F>
+__device__ __forceinline__ void each_sum(const float (&acc)[4][4], int g, int t, F f) {
     if constexpr (!FP8) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-                mma_bf16(acc[n], a.v[p].x, b.v[p].x, a.v[p].y, b.v[p].y, w.v[n][p].x, w.v[n][p].y);
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-                mma_bf16(acc[n], a.v[p].z, b.v[p].z, a.v[p].w, b.v[p].w, w.v[n][p].z, w.v[n][p].w);
+        for (int n = 0; n < 4; ++n) {
+            f(g, 8 * n + 2 * t, acc[n][0], acc[n][1]);
+            f(g + 8, 8 * n + 2 * t, acc[n][2], acc[n][3]);
         }
     } else {
-        // word q of 4 codes meets 8 bytes of the token rows
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const uint4 x = a.v[q >> 1], y = b.v[q >> 1];
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                const uint4 c = w.v[n][q >> 2];
-                uint32_t f0, f1;
-                e4m3x4_to_f16x4((q & 3) == 0 ? c.x : (q & 3) == 1 ? c.y : (q & 3) == 2 ? c.z : c.w,
-                                f0, f1);
-                if (q & 1) mma_f16(acc[n], x.z, y.z, x.w, y.w, f0, f1);
-                else mma_f16(acc[n], x.x, y.x, x.y, y.y, f0, f1);
-            }
-        }
+            for (int i = 0; i < 4; ++i)
+                f(8 * (n >> 1) + 2 * t + (i & 1), 16 * (n & 1) + g + 8 * (i >> 1), acc[n][i], 0.0f);
     }
 }
 
@@ -434,15 +464,20 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
     return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// Stores, or adds to what the same lane stored before.
-__device__ __forceinline__ void put(float* d, float2 v, bool first) {
-    float2* p = reinterpret_cast<float2*>(d);
-    if (!first) {
-        const float2 o = __ldcg(p);
-        v.x += o.x;
-        v.y += o.y;
+// Stores one (e4m3) or two sums, or adds to what the same lane stored before.
+template <bool FP8>
+__device__ __forceinline__ void put(float* d, float v0, float v1, bool first) {
+    if constexpr (FP8) {
+        __stcg(d, first ? v0 : __ldcg(d) + v0);
+    } else {
+        float2* p = reinterpret_cast<float2*>(d);
+        if (!first) {
+            const float2 o = __ldcg(p);
+            v0 += o.x;
+            v1 += o.y;
+        }
+        __stcg(p, make_float2(v0, v1));
     }
-    __stcg(p, v);
 }
 
 // What h's first bf16 value leaves for the second: 16 bits of mantissa
@@ -483,7 +518,8 @@ __device__ __forceinline__ float4 h_quad(const Args& g, const Shared& s, int i, 
     return make_float4(act(gt.x, up.x), act(gt.y, up.y), act(gt.z, up.z), act(gt.w, up.w));
 }
 
-template <bool FP8>
+// MANY: more than 8 tokens, so that an expert may have more than 8
+template <bool FP8, bool MANY>
 __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Args g) {
     extern __shared__ uint8_t dsmem_raw[];
     __shared__ Shared s;
@@ -718,13 +754,22 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
         float* exch = reinterpret_cast<float*>(hbuf);    // [group][T][128]
         // token rows g and g + 8; untouched registers stay 0
         Act<FP8> xa = {}, xb = {};
-        // while the first tiles are on their way: the CTAs of each expert's down
-        // tiles
+        // while the first tiles are on their way: the optional outputs, and what
+        // the final sums will need of each assignment
         const float per2 = static_cast<float>(G2) / static_cast<float>(L2);
-        for (int i = kConsumers - 1 - threadIdx.x; i < n_active; i += kConsumers) {
+        for (int f = kConsumers - 1 - static_cast<int>(threadIdx.x); f < g.T * g.k; f += kConsumers) {
+            const int e = s.ids[f], tk = f / g.k, i = s.rank[e], c0 = s.base[i];
             const int cf = owner(s.start2, G2, i * S2, per2);
-            s.first2[i] = cf;
-            s.ncta2[i] = owner(s.start2, G2, (i + 1) * S2 - 1, per2) - cf + 1;
+            s.term[f] = make_int4(cf, owner(s.start2, G2, (i + 1) * S2 - 1, per2) - cf + 1,
+                                  (c0 + cf * g.T) * g.mt_dn +
+                                      __popc(s.mask[e] & ((1u << tk) - 1u)),
+                                  s.base[i + 1] - c0);
+            s.term_tile[f] = i * S2;
+            s.term_w[f] = FP8 ? s.w[f] * __ldg(g.scales + e * 3 + 2) : s.w[f];
+            if (cta == 0) {
+                if (g.ids) g.ids[f] = e;
+                if (g.w) g.w[f] = s.w[f];
+            }
         }
         // step 1: gate/up partial sums
         for (int X = a1; X < b1;) {
@@ -743,20 +788,20 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                 Wts w;
                 load_w(w, tile + wrow * kTileRowBytes, gq, t);
                 load_act<FP8>(xa, xs, t, gq < cnt);
-                if (cnt > 8) load_act<FP8>(xb, xs + 8 * x_row_bytes<FP8>(), t, gq + 8 < cnt);
+                if (MANY && cnt > 8) load_act<FP8>(xb, xs + 8 * x_row_bytes<FP8>(), t, gq + 8 < cnt);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
                 ring.skip(kGroups);
-                tile_mma<FP8>(acc, w, xa, xb);
+                tile_mma(acc, w, xa, xb, MANY && cnt > 8);
             }
             // the groups' sums of the row tile, added in group order
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                float* d = exch + (grp * g.T + gq) * kTileRows + wrow + 8 * n + 2 * t;
-                if (gq < cnt) *reinterpret_cast<float2*>(d) = make_float2(acc[n][0], acc[n][1]);
-                if (gq + 8 < cnt)
-                    *reinterpret_cast<float2*>(d + 8 * kTileRows) = make_float2(acc[n][2], acc[n][3]);
-            }
+            each_sum<FP8>(acc, gq, t, [&](int tk, int r, float v0, float v1) {
+                float* d = exch + (grp * g.T + tk) * kTileRows + wrow + r;
+                if (tk < cnt) {
+                    if constexpr (FP8) *d = v0;
+                    else *reinterpret_cast<float2*>(d) = make_float2(v0, v1);
+                }
+            });
             consumer_sync();
             // columns of 128 rows; segment (row tile r, CTA c) starts at column
             // sum of the counts before r + c * T: segments follow one another
@@ -792,7 +837,7 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
             }
             float* p = g.p2 + (static_cast<size_t>(c0) + static_cast<size_t>(cta) * g.T) *
                                   g.mt_dn * kTileRows +
-                       static_cast<size_t>(gq) * kTileRows + wrow + 2 * t;
+                       wrow;
             for (int from = from0; from < to;) {
                 const Chunk ch(from, to, g.mt_dn, CK);
                 const int kbA = ch.kb0, kbB = ch.kb1;
@@ -844,11 +889,12 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                     }
                 }
                 consumer_sync();
-                // (e4m3) the unscaling of this lane's two tokens
-                float inv0 = 1.0f, inv1 = 1.0f;
+                // (e4m3) the unscaling of this lane's tokens
+                float inv[4] = {1.0f, 1.0f, 1.0f, 1.0f};
                 if constexpr (FP8) {
-                    inv0 = scale_inv(f16_scale(s.hmax[gq]));
-                    inv1 = scale_inv(f16_scale(s.hmax[gq + 8]));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        inv[q] = scale_inv(f16_scale(s.hmax[8 * (q >> 1) + 2 * t + (q & 1)]));
                 }
                 // later chunks of the same expert add to the columns that the
                 // same lane wrote: of several chunks the first has at least four
@@ -872,33 +918,37 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                         const uint8_t* hr = hbuf + ((kb - kbA) * g.T + gq) * h_row_bytes<FP8>();
                         load_act<FP8>(xa, hr, t, gq < cnt);
                         if constexpr (FP8) {
-                            if (cnt > 8) load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>(), t, gq + 8 < cnt);
-                            tile_mma<FP8>(acc, w, xa, xb);
-                        } else if (cnt <= 8) {
+                            if (MANY && cnt > 8) load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>(), t, gq + 8 < cnt);
+                            tile_mma(acc, w, xa, xb, MANY && cnt > 8);
+                        } else if (!(MANY && cnt > 8)) {
                             // hi in rows 0..7, lo in rows 8..15 of the same MMA
                             load_act<FP8>(xb, hr + BK * 2, t, gq < cnt);
-                            tile_mma<FP8>(acc, w, xa, xb);
+                            tile_mma(acc, w, xa, xb, MANY && cnt > 8);
                         } else {
                             load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>(), t, gq + 8 < cnt);
-                            tile_mma<FP8>(acc, w, xa, xb);
+                            tile_mma(acc, w, xa, xb, MANY && cnt > 8);
                             load_act<FP8>(xa, hr + BK * 2, t, gq < cnt);
                             load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>() + BK * 2, t, gq + 8 < cnt);
-                            tile_mma<FP8>(acc, w, xa, xb);
+                            tile_mma(acc, w, xa, xb, MANY && cnt > 8);
                         }
                     }
                     if (v >= ch.visits) continue;
                     float* d = p + static_cast<size_t>(m) * cnt * kTileRows;
+                    if constexpr (FP8) {
 #pragma unroll
-                    for (int n = 0; n < 4; ++n) {
-                        float2 v0s = make_float2(acc[n][0] * inv0, acc[n][1] * inv0);
-                        float2 v1s = make_float2(acc[n][2] * inv1, acc[n][3] * inv1);
-                        if (!FP8 && cnt <= 8) {
-                            v0s.x += v1s.x;
-                            v0s.y += v1s.y;
+                        for (int n = 0; n < 4; ++n)
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) acc[n][q] *= inv[(n >> 1) * 2 + (q & 1)];
+                    } else if (!(MANY && cnt > 8)) {
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {       // hi + lo
+                            acc[n][0] += acc[n][2];
+                            acc[n][1] += acc[n][3];
                         }
-                        if (gq < cnt) put(d + 8 * n, v0s, first);
-                        if (gq + 8 < cnt) put(d + 8 * kTileRows + 8 * n, v1s, first);
                     }
+                    each_sum<FP8>(acc, gq, t, [&](int tk, int r, float v0, float v1) {
+                        if (tk < cnt) put<FP8>(d + tk * kTileRows + r, v0, v1, first);
+                    });
                 }
                 consumer_sync();   // hbuf is free, the chunk's sums are written
                 if constexpr (FP8) {
@@ -935,21 +985,21 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
             if (item < items) {
                 const int m = col / kTileRows, row = col - m * kTileRows;
                 for (int j = jsub; j < g.k; j += sj) {
-                    const int e = s.ids[tk * g.k + j], i = s.rank[e];
-                    const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
-                    const int c = __popc(s.mask[e] & ((1u << tk) - 1u));
-                    const int cf = s.first2[i], n = s.ncta2[i];
-                    const float* q = g.p2 + ((static_cast<size_t>(c0) +
-                                              static_cast<size_t>(cf) * g.T) * g.mt_dn +
-                                             static_cast<size_t>(m) * cnt + c) * kTileRows + row;
+                    const int f = tk * g.k + j;
+                    const int4 term = s.term[f];
+                    const int tile0 = s.term_tile[f];
+                    const float wt = s.term_w[f];
+                    const int cf = term.x, n = term.y;
+                    const float* q = g.p2 + (static_cast<size_t>(term.z) +
+                                             static_cast<size_t>(m) * term.w) * kTileRows + row;
                     float4 part = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
                     for (int cc = csub; cc < n; cc += sc) {
                         // does CTA cf + cc hold a tile of row tile m?  Its range
                         // within the expert starts at row tile `am` and has
                         // `len` tiles, the row tile fastest
-                        const int st = s.start2[cf + cc] - i * S2;
-                        const int en = s.start2[cf + cc + 1] - i * S2;
+                        const int st = s.start2[cf + cc] - tile0;
+                        const int en = s.start2[cf + cc + 1] - tile0;
                         const int am = st < 0 ? 0 : s.mod2[cf + cc];
                         const int len = (en > S2 ? S2 : en) - (st < 0 ? 0 : st);
                         int d = m - am;
@@ -957,8 +1007,6 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                         if (d < len)
                             part = add4(part, __ldcg(reinterpret_cast<const float4*>(q + cc * step)));
                     }
-                    float wt = s.w[tk * g.k + j];
-                    if constexpr (FP8) wt *= __ldg(g.scales + e * 3 + 2);
                     sum.x += wt * part.x;
                     sum.y += wt * part.y;
                     sum.z += wt * part.z;
@@ -990,12 +1038,6 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                     make_uint2(bf16x2(sum.x, sum.y), bf16x2(sum.z, sum.w));
             }
         }
-        if (cta == 0) {
-            for (int f = threadIdx.x; f < g.T * g.k; f += kConsumers) {
-                if (g.ids) g.ids[f] = s.ids[f];
-                if (g.w) g.w[f] = s.w[f];
-            }
-        }
     }
 }
 
@@ -1013,7 +1055,7 @@ __global__ void decode_ws_init_kernel(Header* h) {
 constexpr int kMaxDevices = 64;
 constexpr int kDynSmemMax = kSmemBytes - static_cast<int>(sizeof(Shared)) - 1024;
 
-template <bool FP8>
+template <bool FP8, bool MANY>
 cudaError_t opt_in_smem() {
     static std::once_flag once[kMaxDevices];
     static cudaError_t err[kMaxDevices];
@@ -1022,16 +1064,16 @@ cudaError_t opt_in_smem() {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     std::call_once(once[dev], [dev] {
-        err[dev] = cudaFuncSetAttribute(decode_kernel<FP8>,
+        err[dev] = cudaFuncSetAttribute(decode_kernel<FP8, MANY>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmemMax);
     });
     return err[dev];
 }
 
-template <bool FP8>
+template <bool FP8, bool MANY>
 cudaError_t launch(const Args& a, int grid, cudaStream_t s) {
-    auto kern = decode_kernel<FP8>;
-    const cudaError_t e = opt_in_smem<FP8>();
+    auto kern = decode_kernel<FP8, MANY>;
+    const cudaError_t e = opt_in_smem<FP8, MANY>();
     if (e != cudaSuccess) return e;
     constexpr int dyn = kDynSmemMax;
     Args g = a;
@@ -1107,7 +1149,8 @@ cudaError_t launch_decode(const DecodeProblem& p, cudaStream_t s) {
     g.status = p.status ? p.status : &g.hdr->status;
     g.p1 = reinterpret_cast<float*>(static_cast<char*>(p.ws) + sizeof(Header));
     g.p2 = reinterpret_cast<float*>(static_cast<char*>(p.ws) + sizeof(Header) + z.p1);
-    return fp8 ? launch<true>(g, grid, s) : launch<false>(g, grid, s);
+    if (p.T <= 8) return fp8 ? launch<true, false>(g, grid, s) : launch<false, false>(g, grid, s);
+    return fp8 ? launch<true, true>(g, grid, s) : launch<false, true>(g, grid, s);
 }
 
 }  // namespace moe

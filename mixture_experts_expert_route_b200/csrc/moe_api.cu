@@ -634,6 +634,9 @@ moe_status check_decode(moe_dtype dt, int T, int k, int E, int H, int I) {
     const long long act = static_cast<long long>(T) * k < E ? T * k : E;
     if (act * g.mt_gu * g.kb_gu > 0x7fffffffLL || act * g.mt_dn * g.kb_dn > 0x7fffffffLL)
         return MOE_ERR_UNSUPPORTED;
+    // and so are the columns of the partial sums
+    if ((static_cast<long long>(kDecodeMaxAssign) + kMaxCtas * T) * g.mt_dn > 0x7fffffffLL)
+        return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
 }
 }  // namespace
