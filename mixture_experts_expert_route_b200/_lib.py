@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -109,7 +110,7 @@ _SIGS = {
     "moe_decode_workspace_size": ([I32, I32, I32, I32, I32, I32], SZ),
     "moe_decode_workspace_init": ([P, SZ, P], I32),
     "moe_decode_forward": ([ctypes.POINTER(DecodeArgs), P, SZ, P], I32),
-    "moe_linear": ([ctypes.POINTER(LinearArgs), P], I32),
+    "moe_linear": ([P, P], I32),
     "moe_check_status": ([P, P], I32),
     "moe_selftest_wait_timeout": ([P, I32, P], I32),
     # CPU/GPU split (include/moe_split.h)
@@ -423,18 +424,24 @@ def decode_forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int
 _FLOAT_TYPE = {torch.bfloat16: 0, torch.float32: 1}
 
 
+# moe_linear_args as bytes: packing costs a third of filling a ctypes structure,
+# and a product of a few tokens takes the GPU no longer than its call
+_LINEAR_ARGS = struct.Struct("@iiiiiPPqqPiPqPqiP")
+
+
 def _rows(t, name, rows, cols, dtype, idx):
     """Checks a matrix argument of linear (rows may be apart) and returns its row stride."""
     if t.get_device() != idx:
         raise ValueError(f"{name}: on {t.device}, expected cuda:{idx}")
     if t.dtype is not dtype:
         raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
-    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
+    if t.shape != (rows, cols):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if cols > 1 and t.stride(1) != 1:
+    rs, cs = t.stride()
+    if cs != 1 and cols > 1:
         raise ValueError(f"{name}: columns must be contiguous")
     # the stride of a single row is of no account
-    return t.stride(0) if rows > 1 else (cols + 7) // 8 * 8
+    return rs if rows > 1 else (cols + 7) // 8 * 8
 
 
 def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=None, out=None,
@@ -452,38 +459,42 @@ def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=N
     if stream is not None or idx != torch._C._cuda_getDevice():
         with _on_device(x.device, stream):
             return linear(x, w, bias, act, gated, residual, out, out_dtype, status)
+    bf16 = torch.bfloat16
     M, K = x.shape
-    rows = w.size(0)
-    if gated and rows % 2:
-        raise ValueError("w: a gated product has an even number of rows")
-    N = rows // 2 if gated else rows
+    N = rows = w.shape[0]
+    if gated:
+        if rows % 2:
+            raise ValueError("w: a gated product has an even number of rows")
+        N = rows // 2
     if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.bfloat16
+        out_dtype = out.dtype if out is not None else bf16
     out_type = _FLOAT_TYPE.get(out_dtype)
     if out_type is None:
         raise ValueError(f"out_dtype: {out_dtype}, expected bfloat16 or float32")
-    ldx = _rows(x, "x", M, K, torch.bfloat16, idx)
-    ldw = _rows(w, "w", rows, K, torch.bfloat16, idx)
-    bias_type, bias_p, ldr, res_p = 0, None, 0, None
+    ldx = _rows(x, "x", M, K, bf16, idx)
+    ldw = _rows(w, "w", rows, K, bf16, idx)
+    bias_type = bias_p = ldr = res_p = status_p = 0
     if bias is not None:
         bias_type = _FLOAT_TYPE.get(bias.dtype)
         if bias_type is None:
             raise ValueError(f"bias: {bias.dtype}, expected bfloat16 or float32")
-        if bias.get_device() != idx or bias.dim() != 1 or bias.size(0) != rows \
-                or (rows > 1 and bias.stride(0) != 1):
+        if bias.get_device() != idx or bias.shape != (rows,) or not bias.is_contiguous():
             raise ValueError(f"bias: expected [{rows}], contiguous, on cuda:{idx}")
         bias_p = bias.data_ptr()
     if residual is not None:
         ldr = _rows(residual, "residual", M, N, out_dtype, idx)
         res_p = residual.data_ptr()
+    if status is not None:
+        if status.get_device() != idx:
+            raise ValueError(f"status: on {status.device}, expected cuda:{idx}")
+        status_p = status.data_ptr()
     if out is None:
         out, ldo = x.new_empty((M, N), dtype=out_dtype), N
     else:
         ldo = _rows(out, "out", M, N, out_dtype, idx)
-    a = LinearArgs(M, N, K, act, 1 if gated else 0, x.data_ptr(), w.data_ptr(), ldx, ldw, bias_p,
-                   bias_type, res_p, ldr, out.data_ptr(), ldo, out_type,
-                   None if status is None else status.data_ptr())
-    code = lib().moe_linear(ctypes.byref(a), torch._C._cuda_getCurrentRawStream(idx))
+    a = _LINEAR_ARGS.pack(M, N, K, act, gated, x.data_ptr(), w.data_ptr(), ldx, ldw, bias_p,
+                          bias_type, res_p, ldr, out.data_ptr(), ldo, out_type, status_p)
+    code = lib().moe_linear(a, torch._C._cuda_getCurrentRawStream(idx))
     if code:
         raise MoEError(code, "moe_linear")
     return out

@@ -238,3 +238,15 @@ def test_linear_binding_refuses(L):
         L.linear(x, x)                                         # host tensors
     with pytest.raises(ValueError):
         L.linear(x[0], x)
+
+
+def test_linear_packing_matches_the_structure(L):
+    """The binding packs moe_linear_args as bytes: every field where the C struct has it."""
+    vals = dict(M=1, N=2, K=3, act=4, gated=1, x=0x1000, w=0x2000, ldx=5, ldw=6, bias=0x3000,
+                bias_type=7, residual=0x4000, ldr=8, out=0x5000, ldo=9, out_type=10, status=0x6000)
+    s = L._lib.LinearArgs(*[vals[f] for f, _ in L._lib.LinearArgs._fields_])
+    packed = L._lib._LINEAR_ARGS.pack(*[vals[f] for f, _ in L._lib.LinearArgs._fields_])
+    assert len(packed) == ctypes.sizeof(s)
+    back = L._lib.LinearArgs.from_buffer_copy(packed)
+    for f, _ in L._lib.LinearArgs._fields_:
+        assert getattr(back, f) == getattr(s, f), f
