@@ -51,14 +51,10 @@ constexpr int kGroups = 4;
 constexpr int kGroupWarps = 4;          // 32 weight rows of a tile each
 constexpr int kConsumerWarps = kGroups * kGroupWarps;
 constexpr int kConsumers = kConsumerWarps * 32;
-// ... a warp that copies the weight tiles, one that copies the gate/up tiles'
-// x slices (together the copies took longer than a tile's time) and, for e4m3
-// layers, two that widen those slices
+// ... a warp that copies the weight tiles and one that copies the gate/up tiles'
+// x slices (together the copies took longer than a tile's time)
 constexpr int kWeightWarp = kConsumerWarps, kXWarp = kConsumerWarps + 1;
-constexpr int kWidenWarp0 = kConsumerWarps + 2, kWidenWarps = 2;
-template <bool FP8> __host__ __device__ constexpr int threads_for() {
-    return (kConsumerWarps + 2 + (FP8 ? kWidenWarps : 0)) * 32;
-}
+constexpr int kThreads = (kConsumerWarps + 2) * 32;
 constexpr int kMaxSlots = 12;           // a multiple of the groups: a slot stays with one
 constexpr int kSmemBytes = 227 * 1024;
 constexpr uint32_t kMagic = 0x4d6f4465u;
@@ -113,10 +109,16 @@ struct Args {
     int slots;
 };
 
+// One chunk's share of a batch's h: the active expert, the first column of h, the
+// first k-block of the h buffer, the first quad of the batch and the quads per
+// token.
+struct Piece {
+    int i, col, slot, quad, quads;
+};
+
 struct Shared {
     uint64_t full[kMaxSlots];
     uint64_t empty[kMaxSlots];
-    uint64_t ready[kMaxSlots];          // e4m3: the slot's x is widened to f16
     int abort;
     int ids[kDecodeMaxAssign];          // [T][k]
     float w[kDecodeMaxAssign];
@@ -137,7 +139,9 @@ struct Shared {
     int start2[kMaxCtas + 1];           // first down tile of each CTA
     int mod2[kMaxCtas];                 // its row tile
     float xmul[kDecodeMaxT];            // e4m3: power-of-two scale of a token's x
-    uint32_t hmax[kDecodeMaxT];         // e4m3: largest |h| of a column in the chunk
+    uint32_t hmax[8][kDecodeMaxT];      // e4m3: largest |h| of a chunk's column
+    Piece pieces[9];                    // of a batch, and the end
+    int n_pieces;
 };
 
 __device__ __forceinline__ void consumer_sync() {
@@ -147,6 +151,11 @@ __device__ __forceinline__ void consumer_sync() {
 __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n)
                  : "memory");
+}
+
+// The four warps of a group.
+__device__ __forceinline__ void group_sync(int grp) {
+    asm volatile("bar.sync %0, %1;" ::"r"(2 + grp), "n"(kGroupWarps * 32) : "memory");
 }
 
 __device__ __forceinline__ uint4 lds16(const uint8_t* p) {
@@ -318,17 +327,17 @@ __device__ __forceinline__ void tile_mma(float (&acc)[4][4], const Wts& w, const
 
 // A lane's sums by (token, weight row of the warp's 32): calls f(token, row, v0,
 // v1), bf16 with two weight rows (row, row + 1), e4m3 with one (v0).
-template <bool FP8, class F>
+template <bool FP8, bool MANY, class F>
 __device__ __forceinline__ void each_sum(const float (&acc)[4][4], int g, int t, F f) {
     if constexpr (!FP8) {
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             f(g, 8 * n + 2 * t, acc[n][0], acc[n][1]);
-            f(g + 8, 8 * n + 2 * t, acc[n][2], acc[n][3]);
+            if (MANY) f(g + 8, 8 * n + 2 * t, acc[n][2], acc[n][3]);
         }
     } else {
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < (MANY ? 4 : 2); ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 f(8 * (n >> 1) + 2 * t + (i & 1), 16 * (n & 1) + g + 8 * (i >> 1), acc[n][i], 0.0f);
@@ -441,17 +450,41 @@ struct Ring {
 // interleaved in the ring; where a visit of the four has a tile less than the
 // first, or there is no fourth visit, the place stays empty but is passed on.
 struct Chunk {
-    int a, b, kb0, kb1, visits;
-    __device__ __forceinline__ Chunk(int from, int to, int MT, int CK) {
-        a = from;
-        kb0 = from / MT;
-        kb1 = kb0 + CK;
-        b = kb1 * MT < to ? kb1 * MT : to;
-        kb1 = (b - 1) / MT + 1;
-        visits = b - a < MT ? b - a : MT;
-    }
-    __device__ __forceinline__ int depth(int v0, int MT) const {   // tiles of visit v0
-        return (b - a - v0 + MT - 1) / MT;
+    int i;               // active expert
+    int a, b, kb0, kb1;  // tiles, k-blocks
+    int kb, m, visits;   // the first visit's k-block and row tile, the visits
+    int slot;            // the k-block of the h buffer where the chunk's begin
+    bool first;          // of the expert's chunks in this CTA
+};
+
+// The chunks of a CTA in order, in batches that share the h buffer (CK
+// k-blocks): as many whole experts' ranges as fit, or CK k-blocks of one.
+struct Plan {
+    int X, end, a2, S2, MT, CK, left;
+    __device__ __forceinline__ Plan(int from, int to, int S2_, int MT_, int CK_)
+        : X(from), end(to), a2(from), S2(S2_), MT(MT_), CK(CK_), left(CK_) {}
+    __device__ __forceinline__ bool done() const { return X >= end; }
+    __device__ __forceinline__ void batch() { left = CK; }
+    __device__ __forceinline__ bool take(Chunk& c) {
+        if (X >= end) return false;
+        c.i = X / S2;
+        const int base = c.i * S2, to = min(end - base, S2);
+        c.a = X - base;
+        c.kb0 = c.a / MT;
+        c.kb1 = (to - 1) / MT + 1;
+        if (c.kb1 - c.kb0 > left) {
+            if (left < CK) return false;
+            c.kb1 = c.kb0 + CK;
+        }
+        c.b = min(c.kb1 * MT, to);
+        c.kb = c.kb0;
+        c.m = c.a - c.kb0 * MT;
+        c.visits = min(c.b - c.a, MT);
+        c.slot = CK - left;
+        c.first = X == a2 || c.a == 0;
+        left -= c.kb1 - c.kb0;
+        X = base + c.b;
+        return true;
     }
 };
 
@@ -512,15 +545,14 @@ __device__ __forceinline__ float4 h_quad(const Args& g, const Shared& s, int i, 
         if (s.start1[cc + 1] >= X0 + g.kb_gu) break;
     }
     auto act = [&](float a, float b) {
-        a *= sg;
-        return a / (1.0f + expf(-a)) * (b * su);
+        return silu(a * sg) * (b * su);   // silu: ~1e-6, far below out's rounding
     };
     return make_float4(act(gt.x, up.x), act(gt.y, up.y), act(gt.z, up.z), act(gt.w, up.w));
 }
 
 // MANY: more than 8 tokens, so that an expert may have more than 8
 template <bool FP8, bool MANY>
-__global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Args g) {
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
     extern __shared__ uint8_t dsmem_raw[];
     __shared__ Shared s;
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -529,7 +561,6 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
     constexpr int BK = tile_k<FP8>();
     constexpr int CK = chunk_kb<FP8>();
     uint8_t* hbuf = smem + g.slots * slot_sz;
-    constexpr int kThreads = threads_for<FP8>();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, cta = blockIdx.x;
 
@@ -548,7 +579,6 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
     if (threadIdx.x < g.slots) {
         mbar_init(&s.full[threadIdx.x], 1 + 32);
         mbar_init(&s.empty[threadIdx.x], kGroupWarps);
-        mbar_init(&s.ready[threadIdx.x], kWidenWarps);
         fence_mbar_init();
     }
     for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) s.mask[e] = 0;
@@ -613,7 +643,7 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
             s.start2[c] = st;
             if (c < G) s.mod2[c] = st % g.mt_dn;
         }
-        if (threadIdx.x < kDecodeMaxT) s.hmax[threadIdx.x] = 0;
+        for (int f = threadIdx.x; f < 8 * kDecodeMaxT; f += kThreads) (&s.hmax[0][0])[f] = 0;
     }
     __syncthreads();
     const int a1 = s.start1[cta], b1 = s.start1[cta + 1];
@@ -641,45 +671,42 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                 ++it;
             }
         }
-        for (int X = a2; lane == 0 && X < b2 && ok;) {
-            const int i = X / S2;
-            const int to = b2 - i * S2 < S2 ? b2 - i * S2 : S2;
-            const uint8_t* w = g.w_dn + static_cast<size_t>(s.expert[i]) * S2 * kTileBytes;
-            for (int from = X - i * S2; from < to && ok;) {
-                const Chunk ch(from, to, g.mt_dn, CK);
+        Plan plan(a2, b2, S2, g.mt_dn, CK);
+        Chunk ch;
+        while (lane == 0 && ok && !plan.done()) {
+            plan.batch();
+            while (ok && plan.take(ch)) {
+                const uint8_t* w = g.w_dn + static_cast<size_t>(s.expert[ch.i]) * S2 * kTileBytes;
+                int m0 = ch.m, kb0 = ch.kb;                    // of visit v0
                 for (int v0 = 0; v0 < ch.visits && ok; v0 += kGroups) {
-                    const int places = ch.depth(v0, g.mt_dn) * kGroups;
-                    int kb = (ch.a + v0) / g.mt_dn, m = ch.a + v0 - kb * g.mt_dn;   // of visit v0
-                    for (int p = 0; p < places; ++p) {
-                        if (it >= g.slots &&
-                            !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
-                            ok = false;
-                            break;
-                        }
-                        const int q = p & (kGroups - 1);
-                        const int L = (kb * g.mt_dn + m) + q;
-                        if (v0 + q < ch.visits && L < ch.b) {
-                            int tkb = kb, tm = m + q;
-                            while (tm >= g.mt_dn) {
-                                tm -= g.mt_dn;
-                                ++tkb;
+                    for (int L = ch.a + v0, d = 0; L < ch.b && ok; L += g.mt_dn, ++d) {
+                        int m = m0, kb = kb0 + d;
+                        for (int q = 0; q < kGroups; ++q) {
+                            if (it >= g.slots &&
+                                !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
+                                ok = false;
+                                break;
                             }
-                            mbar_arrive_expect_tx(&s.full[ring.slot], kTileBytes);
-                            mbar_arrive_n(&s.full[ring.slot], 32);   // (no x slice)
-                            bulk_load(smem + ring.slot * slot_sz,
-                                      w + (static_cast<size_t>(tm) * g.kb_dn + tkb) * kTileBytes,
-                                      kTileBytes, &s.full[ring.slot], kEvictFirst);
-                        } else {
-                            mbar_arrive_n(&s.full[ring.slot], 33);
+                            if (v0 + q < ch.visits && L + q < ch.b) {
+                                mbar_arrive_expect_tx(&s.full[ring.slot], kTileBytes);
+                                mbar_arrive_n(&s.full[ring.slot], 32);   // (no x slice)
+                                bulk_load(smem + ring.slot * slot_sz,
+                                          w + (static_cast<size_t>(m) * g.kb_dn + kb) * kTileBytes,
+                                          kTileBytes, &s.full[ring.slot], kEvictFirst);
+                            } else {
+                                mbar_arrive_n(&s.full[ring.slot], 33);
+                            }
+                            if (++m == g.mt_dn) {
+                                m = 0;
+                                ++kb;
+                            }
+                            ring.skip(1);
+                            ++it;
                         }
-                        if (q == kGroups - 1) ++kb;
-                        ring.skip(1);
-                        ++it;
                     }
+                    for (m0 += kGroups; m0 >= g.mt_dn; m0 -= g.mt_dn) ++kb0;
                 }
-                from = ch.b;
             }
-            X = i * S2 + to;
         }
         if (!ok) {
             fault(s, g.status);
@@ -723,28 +750,6 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
             }
         }
         cp_async_wait_all();
-    } else if (FP8 && warp >= kWidenWarp0) {
-        // ---- e4m3 layers: two warps widen the x slices of the gate/up tiles
-        // in place (bf16 -> scaled f16), every other token each, so that the
-        // sixteen product warps need not each do it
-        Ring ring(g.slots);
-        for (int X = a1; X < b1; ++X, ring.skip(1)) {
-            const int i = X / S1;
-            if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort)) fault(s, g.status);
-            const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
-            uint8_t* xs = smem + ring.slot * slot_sz + kTileBytes;
-#pragma unroll 2
-            for (int c = warp - kWidenWarp0; c < cnt; c += kWidenWarps) {
-                // 4 values per lane
-                const float mul = s.xmul[s.tok[c0 + c]];
-                uint2* v = reinterpret_cast<uint2*>(xs + c * x_row_bytes<FP8>()) + lane;
-                const uint2 b = *v;
-                *v = make_uint2(f16x2(bf16_lo(b.x) * mul, bf16_hi(b.x) * mul),
-                                f16x2(bf16_lo(b.y) * mul, bf16_hi(b.y) * mul));
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s.ready[ring.slot]);
-        }
     } else {
         // ---- consumers.  After a fault every wait returns at once, and the
         // loops run on to their ends, so all warps meet at the same barriers.
@@ -771,6 +776,23 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                 if (g.w) g.w[f] = s.w[f];
             }
         }
+        // the first batch's pieces of h, one per chunk, for the thread per four
+        // columns (see step 2)
+        Plan plan(a2, b2, S2, g.mt_dn, CK);
+        auto list_pieces = [&](Plan q) {
+            if (threadIdx.x != 0) return;
+            Chunk c;
+            int n = 0, quad = 0;
+            q.batch();
+            for (; q.take(c); ++n) {
+                const int quads = (c.kb1 - c.kb0) * (BK / 4);
+                s.pieces[n] = Piece{c.i, c.kb0 * BK, c.slot, quad, quads};
+                quad += quads * (s.base[c.i + 1] - s.base[c.i]);
+            }
+            s.pieces[n].quad = quad;
+            s.n_pieces = n;
+        };
+        list_pieces(plan);
         // step 1: gate/up partial sums
         for (int X = a1; X < b1;) {
             const int r = X / g.kb_gu;                 // row tile over all active experts
@@ -780,13 +802,23 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
             float acc[4][4] = {};
             for (; X < end; ++X) {
                 if (((X - a1) & (kGroups - 1)) != grp) continue;
-                if (!ring_wait(FP8 ? &s.ready[ring.slot] : &s.full[ring.slot], ring.phase,
-                               &s.abort))
-                    fault(s, g.status);
-                const uint8_t* tile = smem + ring.slot * slot_sz;
+                if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort)) fault(s, g.status);
+                uint8_t* tile = smem + ring.slot * slot_sz;
                 const uint8_t* xs = tile + kTileBytes + gq * x_row_bytes<FP8>();
                 Wts w;
                 load_w(w, tile + wrow * kTileRowBytes, gq, t);
+                if constexpr (FP8) {
+                    // x to scaled f16 in place, a warp of the group per token
+                    for (int c = warp % kGroupWarps; c < cnt; c += kGroupWarps) {
+                        const float mul = s.xmul[s.tok[c0 + c]];
+                        uint2* v = reinterpret_cast<uint2*>(tile + kTileBytes +
+                                                            c * x_row_bytes<FP8>()) + lane;
+                        const uint2 b = *v;
+                        *v = make_uint2(f16x2(bf16_lo(b.x) * mul, bf16_hi(b.x) * mul),
+                                        f16x2(bf16_lo(b.y) * mul, bf16_hi(b.y) * mul));
+                    }
+                    group_sync(grp);
+                }
                 load_act<FP8>(xa, xs, t, gq < cnt);
                 if (MANY && cnt > 8) load_act<FP8>(xb, xs + 8 * x_row_bytes<FP8>(), t, gq + 8 < cnt);
                 __syncwarp();
@@ -795,7 +827,7 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
                 tile_mma(acc, w, xa, xb, MANY && cnt > 8);
             }
             // the groups' sums of the row tile, added in group order
-            each_sum<FP8>(acc, gq, t, [&](int tk, int r, float v0, float v1) {
+            each_sum<FP8, MANY>(acc, gq, t, [&](int tk, int r, float v0, float v1) {
                 float* d = exch + (grp * g.T + tk) * kTileRows + wrow + r;
                 if (tk < cnt) {
                     if constexpr (FP8) *d = v0;
@@ -825,139 +857,147 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
         // goes on where the gate/up tiles ended, so visit v0 + vq is this group's
         const int vq = (grp - (b1 - a1)) & (kGroups - 1);
         const float per1 = static_cast<float>(G1) / static_cast<float>(L1);
-        for (int X = a2; X < b2;) {
-            const int i = X / S2, e = s.expert[i];
-            const int from0 = X - i * S2;
-            const int to = b2 - i * S2 < S2 ? b2 - i * S2 : S2;
-            const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
-            float sg = 1.0f, su = 1.0f;
-            if constexpr (FP8) {
-                sg = __ldg(g.scales + e * 3);
-                su = __ldg(g.scales + e * 3 + 1);
+        Chunk ch;
+        while (!plan.done()) {
+            // the batch's h, four columns a thread and turn: all chunks' quads in
+            // one sequence (a chunk's are a multiple of 16, of 32 for e4m3)
+            const int quads_all = s.pieces[s.n_pieces].quad;
+            constexpr int TURNS =
+                CK * BK / 4 * (MANY ? kDecodeMaxT : 8) / kConsumers;
+            float4 hq[TURNS];
+            int hp[TURNS], hc[TURNS];      // where: piece, and column << 16 | quad
+#pragma unroll
+            for (int u = 0; u < TURNS; ++u) {
+                const int idx = threadIdx.x + u * kConsumers;
+                hq[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (idx >= quads_all) continue;
+                int n = 0;
+                while (s.pieces[n + 1].quad <= idx) ++n;
+                const Piece pc = s.pieces[n];
+                const int r = idx - pc.quad, c = r / pc.quads, j = r - c * pc.quads;
+                hp[u] = n;
+                hc[u] = c << 16 | j;
+                if (pc.col + 4 * j < g.I) {
+                    float sg = 1.0f, su = 1.0f;
+                    const int c0 = s.base[pc.i];
+                    if constexpr (FP8) {
+                        const float inv = scale_inv(s.xmul[s.tok[c0 + c]]);
+                        sg = __ldg(g.scales + s.expert[pc.i] * 3) * inv;
+                        su = __ldg(g.scales + s.expert[pc.i] * 3 + 1) * inv;
+                    }
+                    hq[u] = h_quad(g, s, pc.i, c0, s.base[pc.i + 1] - c0, c, pc.col + 4 * j, G1,
+                                   per1, sg, su);
+                }
+                if constexpr (FP8) {
+                    // the largest |h| per column: a warp's quads are of one column
+                    const uint32_t m = __reduce_max_sync(
+                        kFullWarp, max(max(finite_mag(hq[u].x), finite_mag(hq[u].y)),
+                                       max(finite_mag(hq[u].z), finite_mag(hq[u].w))));
+                    if (lane == 0) atomicMax(&s.hmax[n][c], m);
+                }
             }
-            float* p = g.p2 + (static_cast<size_t>(c0) + static_cast<size_t>(cta) * g.T) *
-                                  g.mt_dn * kTileRows +
-                       wrow;
-            for (int from = from0; from < to;) {
-                const Chunk ch(from, to, g.mt_dn, CK);
-                const int kbA = ch.kb0, kbB = ch.kb1;
-                // four columns of h a thread and turn (cols is a multiple of 64)
-                const int quads = (kbB - kbA) * (BK / 4);
-                constexpr int TURNS = chunk_kb<FP8>() * BK / 4 * kDecodeMaxT / kConsumers;
-                float4 hq[TURNS];
+            if constexpr (FP8) consumer_sync();
 #pragma unroll
-                for (int u = 0; u < TURNS; ++u) {
-                    const int idx = threadIdx.x + u * kConsumers;
-                    hq[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (idx < quads * cnt) {
-                        const int c = idx / quads, hc = kbA * BK + (idx - c * quads) * 4;
-                        if (hc < g.I) {
-                            float inv = 1.0f;
-                            if constexpr (FP8) inv = scale_inv(s.xmul[s.tok[c0 + c]]);
-                            hq[u] = h_quad(g, s, i, c0, cnt, c, hc, G1, per1, sg * inv, su * inv);
-                        }
-                        if constexpr (FP8) {
-                            // the largest |h| per column: a warp's quads are of
-                            // one column (quads is a multiple of 32)
-                            const uint32_t m = __reduce_max_sync(
-                                kFullWarp, max(max(finite_mag(hq[u].x), finite_mag(hq[u].y)),
-                                               max(finite_mag(hq[u].z), finite_mag(hq[u].w))));
-                            if (lane == 0) atomicMax(&s.hmax[c], m);
-                        }
-                    }
+            for (int u = 0; u < TURNS; ++u) {
+                if (static_cast<int>(threadIdx.x) + u * kConsumers >= quads_all) continue;
+                const int c = hc[u] >> 16, j = (hc[u] & 0xffff) * 4;
+                const int kl = s.pieces[hp[u]].slot + j / BK, jj = j % BK;
+                uint8_t* d = hbuf + (kl * g.T + c) * h_row_bytes<FP8>() + jj * 2;
+                const float4 h = hq[u];
+                if constexpr (FP8) {
+                    const float mul = f16_scale(s.hmax[hp[u]][c]);
+                    *reinterpret_cast<uint2*>(d) =
+                        make_uint2(f16x2(h.x * mul, h.y * mul), f16x2(h.z * mul, h.w * mul));
+                } else {
+                    const uint32_t h0 = bf16x2(h.x, h.y), h1 = bf16x2(h.z, h.w);
+                    *reinterpret_cast<uint2*>(d) = make_uint2(h0, h1);
+                    *reinterpret_cast<uint2*>(d + BK * 2) =
+                        make_uint2(bf16x2(rest(h.x, bf16_lo(h0)), rest(h.y, bf16_hi(h0))),
+                                   bf16x2(rest(h.z, bf16_lo(h1)), rest(h.w, bf16_hi(h1))));
                 }
-                if constexpr (FP8) consumer_sync();
-#pragma unroll
-                for (int u = 0; u < TURNS; ++u) {
-                    const int idx = threadIdx.x + u * kConsumers;
-                    if (idx < quads * cnt) {
-                        const int c = idx / quads, j = (idx - c * quads) * 4;
-                        const int kl = j / BK, jj = j - kl * BK;
-                        uint8_t* d = hbuf + (kl * g.T + c) * h_row_bytes<FP8>() + jj * 2;
-                        const float4 h = hq[u];
-                        if constexpr (FP8) {
-                            const float mul = f16_scale(s.hmax[c]);
-                            *reinterpret_cast<uint2*>(d) = make_uint2(
-                                f16x2(h.x * mul, h.y * mul), f16x2(h.z * mul, h.w * mul));
-                        } else {
-                            const uint32_t h0 = bf16x2(h.x, h.y), h1 = bf16x2(h.z, h.w);
-                            *reinterpret_cast<uint2*>(d) = make_uint2(h0, h1);
-                            *reinterpret_cast<uint2*>(d + BK * 2) =
-                                make_uint2(bf16x2(rest(h.x, bf16_lo(h0)), rest(h.y, bf16_hi(h0))),
-                                           bf16x2(rest(h.z, bf16_lo(h1)), rest(h.w, bf16_hi(h1))));
-                        }
-                    }
-                }
-                consumer_sync();
+            }
+            consumer_sync();
+            plan.batch();
+            for (int n = 0; plan.take(ch); ++n) {
+                const int c0 = s.base[ch.i], cnt = s.base[ch.i + 1] - c0;
+                float* p = g.p2 + (static_cast<size_t>(c0) + static_cast<size_t>(cta) * g.T) *
+                                      g.mt_dn * kTileRows +
+                           wrow;
                 // (e4m3) the unscaling of this lane's tokens
                 float inv[4] = {1.0f, 1.0f, 1.0f, 1.0f};
                 if constexpr (FP8) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        inv[q] = scale_inv(f16_scale(s.hmax[8 * (q >> 1) + 2 * t + (q & 1)]));
+                    for (int q = 0; q < (MANY ? 4 : 2); ++q)
+                        inv[q] = scale_inv(f16_scale(s.hmax[n][8 * (q >> 1) + 2 * t + (q & 1)]));
                 }
-                // later chunks of the same expert add to the columns that the
-                // same lane wrote: of several chunks the first has at least four
-                // k-blocks, so every row tile is in it
-                const bool first = from == from0;
+                // this group's first visit's k-block (counted from the chunk's
+                // first) and row tile
+                int kb0 = 0, m = ch.m + vq;
+                for (; m >= g.mt_dn; m -= g.mt_dn) ++kb0;
                 for (int v0 = 0; v0 < ch.visits; v0 += kGroups) {
-                    const int v = v0 + vq, depth = ch.depth(v0, g.mt_dn);
-                    int kb = (ch.a + v) / g.mt_dn;
-                    const int m = ch.a + v - kb * g.mt_dn;
+                    const bool visit = v0 + vq < ch.visits;
                     float acc[4][4] = {};
-                    for (int q = 0; q < depth; ++q, ++kb) {
+                    const uint8_t* hr =
+                        hbuf + ((ch.slot + kb0) * g.T + gq) * h_row_bytes<FP8>();
+                    for (int L = ch.a + v0; L < ch.b;
+                         L += g.mt_dn, hr += g.T * h_row_bytes<FP8>()) {
                         if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort))
                             fault(s, g.status);
-                        const bool real = v < ch.visits && kb * g.mt_dn + m < ch.b;
+                        const bool real = visit && L + vq < ch.b;
                         Wts w;
                         if (real) load_w(w, smem + ring.slot * slot_sz + wrow * kTileRowBytes, gq, t);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
                         ring.skip(kGroups);
                         if (!real) continue;
-                        const uint8_t* hr = hbuf + ((kb - kbA) * g.T + gq) * h_row_bytes<FP8>();
                         load_act<FP8>(xa, hr, t, gq < cnt);
                         if constexpr (FP8) {
-                            if (MANY && cnt > 8) load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>(), t, gq + 8 < cnt);
+                            if (MANY && cnt > 8)
+                                load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>(), t, gq + 8 < cnt);
                             tile_mma(acc, w, xa, xb, MANY && cnt > 8);
                         } else if (!(MANY && cnt > 8)) {
                             // hi in rows 0..7, lo in rows 8..15 of the same MMA
                             load_act<FP8>(xb, hr + BK * 2, t, gq < cnt);
-                            tile_mma(acc, w, xa, xb, MANY && cnt > 8);
+                            tile_mma(acc, w, xa, xb, false);
                         } else {
                             load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>(), t, gq + 8 < cnt);
-                            tile_mma(acc, w, xa, xb, MANY && cnt > 8);
+                            tile_mma(acc, w, xa, xb, true);
                             load_act<FP8>(xa, hr + BK * 2, t, gq < cnt);
                             load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>() + BK * 2, t, gq + 8 < cnt);
-                            tile_mma(acc, w, xa, xb, MANY && cnt > 8);
+                            tile_mma(acc, w, xa, xb, true);
                         }
                     }
-                    if (v >= ch.visits) continue;
-                    float* d = p + static_cast<size_t>(m) * cnt * kTileRows;
-                    if constexpr (FP8) {
+                    if (visit) {
+                        float* d = p + static_cast<size_t>(m) * cnt * kTileRows;
+                        if constexpr (FP8) {
 #pragma unroll
-                        for (int n = 0; n < 4; ++n)
+                            for (int b = 0; b < (MANY ? 4 : 2); ++b)
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) acc[n][q] *= inv[(n >> 1) * 2 + (q & 1)];
-                    } else if (!(MANY && cnt > 8)) {
+                                for (int q = 0; q < 4; ++q)
+                                    acc[b][q] *= inv[(b >> 1) * 2 + (q & 1)];
+                        } else if (!(MANY && cnt > 8)) {
 #pragma unroll
-                        for (int n = 0; n < 4; ++n) {       // hi + lo
-                            acc[n][0] += acc[n][2];
-                            acc[n][1] += acc[n][3];
+                            for (int b = 0; b < 4; ++b) {       // hi + lo
+                                acc[b][0] += acc[b][2];
+                                acc[b][1] += acc[b][3];
+                            }
                         }
+                        // later chunks of an expert add to what this CTA wrote: of
+                        // several the first has CK k-blocks, so every row tile
+                        each_sum<FP8, MANY>(acc, gq, t, [&](int tk, int r, float v0s, float v1s) {
+                            if (tk < cnt) put<FP8>(d + tk * kTileRows + r, v0s, v1s, ch.first);
+                        });
                     }
-                    each_sum<FP8>(acc, gq, t, [&](int tk, int r, float v0, float v1) {
-                        if (tk < cnt) put<FP8>(d + tk * kTileRows + r, v0, v1, first);
-                    });
+                    for (m += kGroups; m >= g.mt_dn; m -= g.mt_dn) ++kb0;
                 }
-                consumer_sync();   // hbuf is free, the chunk's sums are written
-                if constexpr (FP8) {
-                    if (threadIdx.x < kDecodeMaxT) s.hmax[threadIdx.x] = 0;
-                    consumer_sync();
-                }
-                from = ch.b;
             }
-            X = i * S2 + to;
+            consumer_sync();   // hbuf is free, the batch's sums are written
+            if constexpr (FP8) {
+                for (int f = threadIdx.x; f < CK * kDecodeMaxT; f += kConsumers)
+                    (&s.hmax[0][0])[f] = 0;
+            }
+            list_pieces(plan);
+            consumer_sync();
         }
         if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[1][0], target[1]))
             fault(s, g.status);
@@ -969,17 +1009,17 @@ __global__ void __launch_bounds__(threads_for<FP8>(), 1) decode_kernel(const Arg
         // the CTAs of each; lanes first (ls, so that 8 lanes still read 128
         // consecutive bytes), then warps.
         const int hquads = g.H / 4, items = g.T * hquads;
-        int spl = 1;
-        while (spl < 4 * kConsumerWarps && items * spl * 2 <= G * kConsumers) spl *= 2;
-        int sj = 1;
-        while (sj * 2 <= spl && sj * 2 <= g.k) sj *= 2;
-        const int sc = spl / sj, ls = spl < 4 ? spl : 4, lw = 32 / ls, ws = spl / ls;
-        const int sub = (warp % ws) * ls + lane / lw, per_cta = kConsumers / spl;
-        const int jsub = sub % sj, csub = sub / sj;
+        int spl2 = 0;                                  // powers of two, as exponents
+        while ((1 << spl2) < 4 * kConsumerWarps && (items << (spl2 + 1)) <= G * kConsumers) ++spl2;
+        const int sj2 = min(spl2, 31 - __clz(g.k)), ls2 = min(spl2, 2), lw2 = 5 - ls2;
+        const int ws2 = spl2 - ls2, sj = 1 << sj2, sc = 1 << (spl2 - sj2);
+        const int lw = 1 << lw2, ws = 1 << ws2, per_cta = kConsumers >> spl2;
+        const int sub = ((warp & (ws - 1)) << ls2) + (lane >> lw2);
+        const int jsub = sub & (sj - 1), csub = sub >> sj2;
         float4* red = reinterpret_cast<float4*>(smem);   // the ring has run dry
         const size_t step = static_cast<size_t>(g.T) * g.mt_dn * kTileRows;
         for (int item0 = cta * per_cta; item0 < items; item0 += G * per_cta) {
-            const int item = item0 + warp / ws * lw + lane % lw;
+            const int item = item0 + ((warp >> ws2) << lw2) + (lane & (lw - 1));
             const int tk = item / hquads, col = (item - tk * hquads) * 4;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             if (item < items) {
@@ -1083,7 +1123,7 @@ cudaError_t launch(const Args& a, int grid, cudaStream_t s) {
     if (g.slots < kGroups) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads_for<FP8>());
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = rest + g.slots * slot_bytes<FP8>(a.T);
     cfg.stream = s;
     // cooperative: the blocks wait on one another, so all must be resident
