@@ -273,23 +273,24 @@ __device__ __forceinline__ void load_w(Wts& w, const uint8_t* rows, int g, int t
     }
 }
 
-// Token rows: only real ones are read (the products of the others are never
-// looked at).
+// Token rows.  A lane whose row is past the expert's count reads row 0 with the
+// lanes that own it (one broadcast); what it gives is never looked at.
 template <bool FP8> struct Act {
     uint4 v[FP8 ? 4 : 2];
 };
 template <bool FP8>
-__device__ __forceinline__ void load_act(Act<FP8>& a, const uint8_t* row, int t, bool real) {
+__device__ __forceinline__ Act<FP8> load_act(const uint8_t* row, int t) {
     constexpr int N = FP8 ? 4 : 2;
-    if (real)
+    Act<FP8> a;
 #pragma unroll
-        for (int q = 0; q < N; ++q) a.v[q] = lds16(row + t * (N * 16) + q * 16);
+    for (int q = 0; q < N; ++q) a.v[q] = lds16(row + t * (N * 16) + q * 16);
+    return a;
 }
 
 // bf16: D[16 tokens][32 weight rows of this warp] += act x W, four blocks of 8
 // weight rows in N; a: token rows g, b: token rows g + 8 (or h's low parts).
 __device__ __forceinline__ void tile_mma(float (&acc)[4][4], const Wts& w, const Act<false>& a,
-                                         const Act<false>& b, bool) {
+                                         const Act<false>& b) {
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
 #pragma unroll
@@ -303,10 +304,11 @@ __device__ __forceinline__ void tile_mma(float (&acc)[4][4], const Wts& w, const
 
 // e4m3: D[32 weight rows][8 tokens] += W x act, two blocks of 16 weight rows in M
 // (the widened codes land in the registers that M wants), 8 tokens in N; acc[b]
-// for tokens 0..7, acc[2 + b] for 8..15 (`many`).  Word q of 4 codes meets 8
-// bytes of the token rows.
+// for tokens 0..7, acc[2 + b] for 8..15 (BOTH).  Word q of 4 codes meets 8 bytes
+// of the token rows.
+template <bool BOTH>
 __device__ __forceinline__ void tile_mma(float (&acc)[4][4], const Wts& w, const Act<true>& a,
-                                         const Act<true>& b, bool many) {
+                                         const Act<true>& b) {
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
         const uint4 x = a.v[q >> 1], y = b.v[q >> 1];
@@ -319,7 +321,7 @@ __device__ __forceinline__ void tile_mma(float (&acc)[4][4], const Wts& w, const
             e4m3x4_to_f16x4((q & 3) == 0 ? c1.x : (q & 3) == 1 ? c1.y : (q & 3) == 2 ? c1.z : c1.w,
                             f1, f3);
             mma_f16(acc[m], f0, f1, f2, f3, (q & 1) ? x.z : x.x, (q & 1) ? x.w : x.y);
-            if (many)
+            if constexpr (BOTH)
                 mma_f16(acc[2 + m], f0, f1, f2, f3, (q & 1) ? y.z : y.x, (q & 1) ? y.w : y.y);
         }
     }
@@ -757,8 +759,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
         const int grp = warp / kGroupWarps, wrow = warp % kGroupWarps * 32;  // first weight row
         Ring ring(g.slots, grp);
         float* exch = reinterpret_cast<float*>(hbuf);    // [group][T][128]
-        // token rows g and g + 8; untouched registers stay 0
-        Act<FP8> xa = {}, xb = {};
         // while the first tiles are on their way: the optional outputs, and what
         // the final sums will need of each assignment
         const float per2 = static_cast<float>(G2) / static_cast<float>(L2);
@@ -799,12 +799,12 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
             const int i = r / g.mt_gu, m = r - i * g.mt_gu;
             const int end = (r + 1) * g.kb_gu < b1 ? (r + 1) * g.kb_gu : b1;
             const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
+            const int ra = gq < cnt ? gq : 0, rb = gq + 8 < cnt ? gq + 8 : 0;
             float acc[4][4] = {};
             for (; X < end; ++X) {
                 if (((X - a1) & (kGroups - 1)) != grp) continue;
                 if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort)) fault(s, g.status);
                 uint8_t* tile = smem + ring.slot * slot_sz;
-                const uint8_t* xs = tile + kTileBytes + gq * x_row_bytes<FP8>();
                 Wts w;
                 load_w(w, tile + wrow * kTileRowBytes, gq, t);
                 if constexpr (FP8) {
@@ -819,12 +819,20 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                     }
                     group_sync(grp);
                 }
-                load_act<FP8>(xa, xs, t, gq < cnt);
-                if (MANY && cnt > 8) load_act<FP8>(xb, xs + 8 * x_row_bytes<FP8>(), t, gq + 8 < cnt);
+                const uint8_t* xs = tile + kTileBytes;
+                const Act<FP8> xa = load_act<FP8>(xs + ra * x_row_bytes<FP8>(), t);
+                Act<FP8> xb = {};
+                if (MANY && (!FP8 || cnt > 8))
+                    xb = load_act<FP8>(xs + rb * x_row_bytes<FP8>(), t);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
                 ring.skip(kGroups);
-                tile_mma(acc, w, xa, xb, MANY && cnt > 8);
+                if constexpr (!FP8) {
+                    tile_mma(acc, w, xa, xb);
+                } else {
+                    if (MANY && cnt > 8) tile_mma<true>(acc, w, xa, xb);
+                    else tile_mma<false>(acc, w, xa, xa);
+                }
             }
             // the groups' sums of the row tile, added in group order
             each_sum<FP8, MANY>(acc, gq, t, [&](int tk, int r, float v0, float v1) {
@@ -923,6 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                 float* p = g.p2 + (static_cast<size_t>(c0) + static_cast<size_t>(cta) * g.T) *
                                       g.mt_dn * kTileRows +
                            wrow;
+                const int ra = gq < cnt ? gq : 0, rb = gq + 8 < cnt ? gq + 8 : 0;
                 // (e4m3) the unscaling of this lane's tokens
                 float inv[4] = {1.0f, 1.0f, 1.0f, 1.0f};
                 if constexpr (FP8) {
@@ -937,8 +946,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                 for (int v0 = 0; v0 < ch.visits; v0 += kGroups) {
                     const bool visit = v0 + vq < ch.visits;
                     float acc[4][4] = {};
-                    const uint8_t* hr =
-                        hbuf + ((ch.slot + kb0) * g.T + gq) * h_row_bytes<FP8>();
+                    const uint8_t* hr = hbuf + (ch.slot + kb0) * g.T * h_row_bytes<FP8>();
                     for (int L = ch.a + v0; L < ch.b;
                          L += g.mt_dn, hr += g.T * h_row_bytes<FP8>()) {
                         if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort))
@@ -950,21 +958,19 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                         if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
                         ring.skip(kGroups);
                         if (!real) continue;
-                        load_act<FP8>(xa, hr, t, gq < cnt);
+                        const uint8_t* ha = hr + ra * h_row_bytes<FP8>();
+                        const uint8_t* hb = hr + rb * h_row_bytes<FP8>();
+                        const Act<FP8> xa = load_act<FP8>(ha, t);
                         if constexpr (FP8) {
-                            if (MANY && cnt > 8)
-                                load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>(), t, gq + 8 < cnt);
-                            tile_mma(acc, w, xa, xb, MANY && cnt > 8);
+                            if (MANY && cnt > 8) tile_mma<true>(acc, w, xa, load_act<FP8>(hb, t));
+                            else tile_mma<false>(acc, w, xa, xa);
                         } else if (!(MANY && cnt > 8)) {
                             // hi in rows 0..7, lo in rows 8..15 of the same MMA
-                            load_act<FP8>(xb, hr + BK * 2, t, gq < cnt);
-                            tile_mma(acc, w, xa, xb, false);
+                            tile_mma(acc, w, xa, load_act<FP8>(ha + BK * 2, t));
                         } else {
-                            load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>(), t, gq + 8 < cnt);
-                            tile_mma(acc, w, xa, xb, true);
-                            load_act<FP8>(xa, hr + BK * 2, t, gq < cnt);
-                            load_act<FP8>(xb, hr + 8 * h_row_bytes<FP8>() + BK * 2, t, gq + 8 < cnt);
-                            tile_mma(acc, w, xa, xb, true);
+                            tile_mma(acc, w, xa, load_act<FP8>(hb, t));
+                            tile_mma(acc, w, load_act<FP8>(ha + BK * 2, t),
+                                     load_act<FP8>(hb + BK * 2, t));
                         }
                     }
                     if (visit) {
