@@ -319,9 +319,10 @@ MOE_API moe_status moe_forward(const moe_forward_args* args, void* ws, size_t ws
  * For decode steps: moe_forward's chain of kernels has a fixed cost that
  * outweighs the stream of a few small experts' weights.  Same routing (ids and
  * w bit for bit), same packed weights and scales.  It differs in precision
- * only: h enters the down product with 16 bits of mantissa instead of bf16's
- * 8, and for MOE_FP8_E4M3 the activations stay bf16 (moe_forward quantises
- * them); every sum is fp32 in a fixed order, out is rounded once.
+ * only: h enters the down product with 16 bits of mantissa (MOE_FP8_E4M3: 11)
+ * instead of bf16's 8, and for MOE_FP8_E4M3 no activation is quantised
+ * (moe_forward quantises x and h); every sum is fp32 in a fixed order, out is
+ * rounded once.
  *   x, out    device bf16 [T,H]; logits device f32 [T,E]
  *   residual  device bf16 [T,H] or NULL; may be out itself
  *   ids, w    optional device outputs [T,k]
@@ -377,7 +378,8 @@ MOE_API moe_status moe_decode_forward(const moe_decode_args* args, void* ws, siz
  * out, residual and bias need their elements' alignment only (16-byte aligned
  * rows are written fastest).  Bit-reproducible; no workspace.
  * Errors: MOE_ERR_INVALID_ARG for bad sizes, strides, types or pointers,
- * MOE_ERR_UNSUPPORTED for K, ldx or ldw not a multiple of 8.
+ * MOE_ERR_UNSUPPORTED for K, ldx or ldw not a multiple of 8, M > 2^30 or
+ * N > 2^29.
  */
 typedef enum {
     MOE_ACT_NONE = 0,

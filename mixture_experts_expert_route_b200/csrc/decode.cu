@@ -23,17 +23,30 @@
 //     routing weights, over all CTAs, the residual added and rounded once.
 //
 // The weights arrive as 16 KB tiles (the packed layout of the grouped GEMMs)
-// through a ring of bulk copies that one warp keeps full across the barriers:
+// through a ring of bulk copies that one thread keeps full across the barriers:
 // while the CTAs exchange partial sums the first down tiles land.  The products
-// are m16n8k16 warp MMAs with the tokens in the M slot (16 of them at most) and
-// 8 weight rows of a tile per warp in N: at these sizes the tensor work is a few
-// percent of the stream's time, one warp reads a tile row whole, and the
-// register path lets e4m3 weights be widened exactly (nothing is quantised) and
-// h enter with more bits than bf16's 8, so the only coarse rounding is out's.
+// are m16n8k16 warp MMAs: at these sizes the tensor work is a fifth of the
+// stream's time, and the register path lets the operands be widened.  bf16
+// layers: tokens in M (16 at most), weight rows in N, and h as the sum of two
+// bf16 values (16 bits), the low parts in the MMA's upper 8 rows while an expert
+// has at most 8 tokens.  e4m3 layers: weights and x to f16, both exact, h to
+// f16's 11 bits; nothing is quantised.  The only coarse rounding is out's.
+//
 // One tile is a chain of some 500 cycles of latency (barrier, loads, products),
-// so four groups of four warps take the tiles in turn, each with four
-// independent products a warp; sixteen warps on each tile left the stream at
-// 5.8 TB/s and every down tile of a small layer at 1000 cycles.
+// so four groups of four warps take the tiles in turn, 32 weight rows a warp;
+// with all sixteen warps on each tile the stream stayed at 5.8 TB/s and every
+// down tile of a small layer took 1000 cycles.
+//
+// Measured on one B200 (us; floor = the active experts' bytes at the copy's 6.53
+// TB/s; then moe_forward, whose chain of kernels costs ~28 us before the stream):
+//   bf16 E=128 H=2048 I=768 top-8     T = 1: 29-31 (11.6; 42)    T = 8: 86 (74; 99)
+//   bf16 E=8 H=4096 I=14336 top-2     T = 1: 117 (108; 123)      T = 8: 378 (371; 354)
+//   bf16 E=64 H=7168 I=2048 top-8     T = 1: 118 (108; 124)      T = 8: 566 (566; 528)
+//   e4m3 E=32 H=I=2880 top-4          T = 1: 35 (15; 49)         T = 8: 104 (79; 111)
+// Where T = 1's 30 us go (the first of them): 4 us routing and tables in every
+// CTA, 1.3 to the first tile, 8 of gate/up stream, 2.5 to the first barrier's
+// end under the down tiles' prefetch, 5 of h and down products, 1.3 for the
+// second barrier, 2.5 of final sums, 2.5 between launches.
 //
 // All sums are in a fixed order: results do not depend on timing.
 #include <cstdint>
@@ -79,7 +92,7 @@ template <bool FP8> __host__ __device__ constexpr int h_bytes(int T) {
     return h > x ? h : x;
 }
 
-// Workspace header, zeroed but for the magic by moe_decode_workspace_init.
+// Workspace header, made by moe_decode_workspace_init.
 // The arrival counters only grow, by one per CTA and launch, so each launch
 // finds them at a multiple of the grid (and they stay below the next one until
 // its own CTA arrives), and no launch has to reset them.
@@ -255,11 +268,11 @@ __device__ __forceinline__ bool grid_barrier(uint64_t* counter, uint64_t target)
     }
 }
 
-// One lane's part of a tile: 32 weight rows of this warp by 16 tokens.  The K order inside a 128-byte row is
-// permuted the same way for both operands: lane (g, t) takes 16-byte pieces 2t
-// and 2t+1 of weight row g of each block, whose swizzled places are
-// conflict-free for a quarter warp, and the matching 32 (bf16) or 64 (f16, for
-// 32 e4m3 codes) bytes of token rows g and g + 8.
+// One lane's part of a tile: 32 weight rows of this warp by 16 tokens.  The K
+// order inside a 128-byte row is permuted the same way for both operands: lane
+// (g, t) takes 16-byte pieces 2t and 2t+1 of weight row g of each block of 8,
+// whose swizzled places are conflict-free for a quarter warp, and the matching
+// 32 (bf16) or 64 (f16, for 32 e4m3 codes) bytes of token rows g and g + 8.
 struct Wts {
     uint4 v[4][2];
 };
@@ -566,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, cta = blockIdx.x;
 
-    // (looked at below, so that its latency hides behind the routing's loads)
+    // (used below, so that the loads' latency hides behind the routing's)
     const uint32_t magic = __ldcg(&g.hdr->magic);
     uint64_t target[2] = {0, 0};
     if (threadIdx.x == 0) {

@@ -680,7 +680,7 @@ moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream) {
     if (a->out_type != MOE_FLOAT_BF16 && a->out_type != MOE_FLOAT_F32) return MOE_ERR_INVALID_ARG;
     if (a->K % 8 != 0 || a->ldx % 8 != 0 || a->ldw % 8 != 0) return MOE_ERR_UNSUPPORTED;
     // rows of W, tile indices and the products' columns are 32-bit
-    if (a->N > (1 << 29) || a->K > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+    if (a->M > (1 << 30) || a->N > (1 << 29) || a->K > (1 << 30)) return MOE_ERR_UNSUPPORTED;
     if (a->M == 0) return MOE_OK;
     if (!a->x || !a->w || !a->out) return MOE_ERR_INVALID_ARG;
     if (a->ldx < a->K || a->ldw < a->K || a->ldo < a->N || (a->residual && a->ldr < a->N))

@@ -221,6 +221,7 @@ def test_linear_argument_errors(L):
     assert call(act=-1) == INVALID and call(act=5) == INVALID
     assert call(bias_type=2) == INVALID and call(out_type=-1) == INVALID
     assert call(K=100) == UNSUP                                # K % 8
+    assert call(M=(1 << 30) + 1) == UNSUP and call(N=(1 << 29) + 1) == UNSUP
     assert call(ldx=132) == UNSUP and call(ldw=130) == UNSUP
     assert call(ldx=120) == INVALID and call(ldw=64) == INVALID and call(ldo=63) == INVALID
     assert call(residual=0x1000, ldr=32) == INVALID

@@ -5,10 +5,10 @@ Tolerance of out, per element:
     |out - ref| <= 2^-8 |ref| + 2^-10 * mag
 2^-8 (half of bf16's eps) is the one rounding of out.  mag is the sum of magnitudes that an
 error in the sums is relative to, sum_j w_j sum_i (|h_i| + how g's and u's sums of magnitudes
-move h_i) |Wd_i|; its factor covers h's representation as hi + lo of two bf16 values (2^-17)
-and the fp32 sums: the products are exact, and n additions in any order, truncating ones of
+move h_i) |Wd_i|; its factor covers h's representation (hi + lo of two bf16 values, 2^-17; with
+e4m3 weights f16, 2^-12) and the fp32 sums: the products are exact, and n additions in any order, truncating ones of
 2^-23 included, are off by at most n 2^-23 of the sum of magnitudes: 2^-11 for the n <= 2^12
-terms here, twice (into h, and down).
+terms here at the very worst, into h and down.
 """
 import pytest
 import torch
