@@ -17,9 +17,20 @@
 //   tile  one 128 x BN tcgen05 tile per block; when there are fewer tiles than
 //         SMs, the blocks of a cluster split K and add their accumulators
 //         through distributed shared memory.
-//   pair  256 x BN tiles on CTA pairs (cta_group::2), persistent, two TMEM
+//   pair  256 x 256 tiles on CTA pairs (cta_group::2), persistent, two TMEM
 //         accumulators, so an epilogue runs under the next tile's products.
 // No kernel needs a workspace, and no sum depends on timing.
+//
+// Measured on one B200 in a graph (us; floor at the measured copy and bf16 GEMM
+// rates; cuBLAS = the plain product alone, no epilogue):
+//   few   M=1  K=7168 N=2x2048 gated    12.7  (floor 9.0 by bytes, cuBLAS 20)
+//         M=16 K=14336 N=4096 residual  22.9  (18, 22)
+//   tile  M=77 K=N=2880                 12    (2.7, 7)   latency: ~8 us of launch,
+//         first copies, cluster sum and store around 11 k-blocks a block
+//         M=512 K=7168 N=2x2048 gated   34    (18, 25)   shared memory: a 128-wide
+//         tile reads 1.5x what its MMAs take
+//   pair  M=8192 K=7168 N=2x2048 gated  330-390 (288 at the burst rate; cuBLAS
+//         369-372 in the same runs): the power cap; M=1024 K=N=4096 32 (21, 25)
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -584,25 +595,24 @@ constexpr int kPairThreads = 384;
 constexpr int kEpiWarp0 = 4;                 // warps 4..11
 constexpr int kEpiThreads = 256;
 
-template <int BN> __host__ __device__ constexpr int pair_stage_bytes() {
-    return (128 + BN / 2) * kRowBytes;       // per CTA: 128 token rows, half of the weight rows
-}
-template <int BN> __host__ __device__ constexpr int pair_stages() { return BN == 256 ? 6 : 8; }
-template <int BN> __host__ __device__ constexpr int pair_smem_bytes() {
-    return 1024 + pair_stages<BN>() * pair_stage_bytes<BN>();
-}
+// 256 columns: 128-column tiles are bound by the shared memory that feeds the
+// MMAs (581 us instead of 410 at M = 4096, K = 14336, N = 4096)
+constexpr int kPairN = 256;
+constexpr int kPairStageBytes = (128 + kPairN / 2) * kRowBytes;   // per CTA: 128 token rows,
+                                                                  // half of the weight rows
+constexpr int kPairStages = 6;
+constexpr int kPairSmemBytes = 1024 + kPairStages * kPairStageBytes;
 
-template <int BN>
 struct PairCtl {
-    uint64_t full[pair_stages<BN>()];
-    uint64_t empty[pair_stages<BN>()];
+    uint64_t full[kPairStages];
+    uint64_t empty[kPairStages];
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
     uint32_t tmem;
     int abort;
     uint32_t prod_pos, mma_pos, mma_issued;
-    alignas(16) float bias[2][BN];
+    alignas(16) float bias[2][kPairN];
 };
 
 // Tile t of the rasterised order: groups of 8 row tiles, in a group column tile
@@ -615,14 +625,13 @@ __device__ __forceinline__ void pair_tile(int t, int tm, int tn, int& m, int& n)
     n = r / h;
 }
 
-template <int BN>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ Maps maps, const Args g) {
     extern __shared__ uint8_t dsmem_raw[];
-    __shared__ PairCtl<BN> ctl;
+    __shared__ PairCtl ctl;
     uint8_t* base = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    constexpr int STAGE = pair_stage_bytes<BN>(), S = pair_stages<BN>();
+    constexpr int BN = kPairN, STAGE = kPairStageBytes, S = kPairStages;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     if (threadIdx.x == 0) {
@@ -954,23 +963,22 @@ cudaError_t launch_tile(const Args& g, int sms, cudaStream_t s) {
                   s, maps, g, csize);
 }
 
-template <int BN>
 cudaError_t launch_pair(const Args& g, int sms, cudaStream_t s) {
     static std::once_flag once[kMaxDevices];
     static cudaError_t err[kMaxDevices];
-    cudaError_t e = opt_in(linear_pair_kernel<BN>, pair_smem_bytes<BN>(), once, err);
+    cudaError_t e = opt_in(linear_pair_kernel, kPairSmemBytes, once, err);
     if (e != cudaSuccess) return e;
-    const int per = g.gated ? BN / 2 : BN;
+    const int per = g.gated ? kPairN / 2 : kPairN;
     const long long tiles = (static_cast<long long>(g.M) + 255) / 256 *
                             ((static_cast<long long>(g.N) + per - 1) / per);
     if (tiles > 0x3fffffffLL) return cudaErrorInvalidConfiguration;
     Maps maps;
     memset(&maps, 0, sizeof(maps));
     if (!make_map(&maps.x, g.x, g.K, g.M, g.ldx, 128) ||
-        !make_map(&maps.w, g.w, g.K, g.gated ? 2LL * g.N : g.N, g.ldw, BN / 2))
+        !make_map(&maps.w, g.w, g.K, g.gated ? 2LL * g.N : g.N, g.ldw, kPairN / 2))
         return cudaErrorInvalidValue;
     const long long pairs = tiles < sms / 2 ? tiles : sms / 2;
-    return launch(linear_pair_kernel<BN>, pairs * 2, kPairThreads, pair_smem_bytes<BN>(), 2, s, maps,
+    return launch(linear_pair_kernel, pairs * 2, kPairThreads, kPairSmemBytes, 2, s, maps,
                   g);
 }
 
@@ -1010,7 +1018,7 @@ cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s) {
     const int per = p.gated ? 128 : 256;
     const long long t256 = (static_cast<long long>(p.M) + 255) / 256 *
                            ((static_cast<long long>(p.N) + per - 1) / per);
-    if (p.M > 128 && t256 * 4 >= sms) return launch_pair<256>(g, sms, s);
+    if (p.M > 128 && t256 * 4 >= sms) return launch_pair(g, sms, s);
     const long long t128 = (static_cast<long long>(p.M) + 127) / 128 *
                            ((static_cast<long long>(p.N) + per / 2 - 1) / (per / 2));
     if (t128 * 2 >= sms) return launch_tile<128>(g, sms, s);
