@@ -83,13 +83,19 @@ template <bool FP8> __host__ __device__ constexpr int h_row_bytes() {
 // a token's x of one gate/up tile, padded likewise, and a ring slot: a weight
 // tile and the x slices of the tokens
 template <bool FP8> __host__ __device__ constexpr int x_row_bytes() { return tile_k<FP8>() * 2 + 16; }
-template <bool FP8> __host__ __device__ constexpr int slot_bytes(int T) {
-    return kTileBytes + T * x_row_bytes<FP8>();
+template <bool FP8> __host__ __device__ constexpr int slot_bytes(int rows) {
+    return kTileBytes + rows * x_row_bytes<FP8>();
 }
-// the h buffer, before it the groups' exchange of gate/up sums [group][T][128]
-template <bool FP8> __host__ __device__ constexpr int h_bytes(int T) {
-    const int h = chunk_kb<FP8>() * T * h_row_bytes<FP8>(), x = kGroups * T * kTileRows * 4;
+// the h buffer, before it the groups' exchange of gate/up sums [group][rows][128]
+template <bool FP8> __host__ __device__ constexpr int h_bytes(int rows) {
+    const int h = chunk_kb<FP8>() * rows * h_row_bytes<FP8>(), x = kGroups * rows * kTileRows * 4;
     return h > x ? h : x;
+}
+// slots beside it, a multiple of the groups (8 at 16 rows, 12 up to about 5);
+// `rows` is the most tokens that one expert has, known after the routing
+template <bool FP8> __host__ __device__ constexpr int slots_for(int rows, int smem) {
+    const int n = (smem - h_bytes<FP8>(rows)) / slot_bytes<FP8>(rows) / kGroups * kGroups;
+    return n < kMaxSlots ? n : kMaxSlots;
 }
 
 // Workspace header, made by moe_decode_workspace_init.
@@ -119,7 +125,7 @@ struct Args {
     Header* hdr;
     float* p1;                   // gate/up partial columns of 128 rows
     float* p2;                   // down partial columns of 128 rows
-    int slots;
+    int smem;                    // dynamic shared memory past its alignment
 };
 
 // One chunk's share of a batch's h: the active expert, the first column of h, the
@@ -138,6 +144,7 @@ struct Shared {
     uint32_t mask[kMaxExperts];         // tokens that chose an expert
     int rank[kMaxExperts];              // index among the active experts
     int scan[kMaxExperts / 32];
+    int most[kMaxExperts / 32];
     int expert[kDecodeMaxAssign];       // active experts, ascending
     int base[kDecodeMaxAssign + 1];     // first column of an active expert
     int tok[kDecodeMaxAssign];          // column -> token
@@ -359,16 +366,39 @@ __device__ __forceinline__ void each_sum(const float (&acc)[4][4], int g, int t,
     }
 }
 
-// Routing of all tokens by the consumer warps.  A few tokens' keys (one pass of
-// the threads) are ranked by counting: an expert's place is the number of keys
-// above its own (keys are distinct), `parts` threads to a key.  The same order
-// and the same sums as warp_topk, which takes larger batches a warp per token:
-// ids and weights are its bits either way.
+// Few enough keys for one pass of the threads.
+__device__ __forceinline__ bool routes_by_counting(const Args& g) {
+    return g.T * ((g.E + 31) & ~31) <= kConsumers;
+}
+
+// Routing of all tokens by the consumer warps.  A few tokens' keys are ranked by
+// counting: an expert's place is the number of keys above its own (keys are
+// distinct), `parts` threads to a key; s.w gets the selected logits, and
+// softmax_tokens makes them weights later, off the way to the first tiles.  The
+// same order and the same sums as warp_topk, which takes larger batches a warp
+// per token: ids and weights are its bits either way.
+__device__ __forceinline__ void softmax_tokens(const Args& g, Shared& s, int warp, int lane) {
+    for (int t = warp; t < g.T; t += kConsumerWarps) {
+        float* w = s.w + t * g.k;
+        const float m = w[0];
+        __syncwarp();
+        float z = 0.0f;
+        for (int j = lane; j < g.k; j += 32) {
+            const float v = expf(w[j] - m);
+            w[j] = v;
+            z += v;
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(kFullWarp, z, off);
+        for (int j = lane; j < g.k; j += 32) w[j] = w[j] / z;
+    }
+}
+
 template <bool FP8>
 __device__ __forceinline__ void route_tokens(const Args& g, Shared& s, uint64_t* keys, int warp,
                                              int lane) {
     const int Ep = (g.E + 31) & ~31, n = g.T * Ep;
-    const bool counting = n <= kConsumers;
+    const bool counting = routes_by_counting(g);
     if (counting && threadIdx.x < n) {
         const int t = threadIdx.x / Ep, e = threadIdx.x - t * Ep;
         keys[threadIdx.x] = e < g.E ? select_key(__ldg(g.logits + t * g.E + e), e) : 0ull;
@@ -422,21 +452,6 @@ __device__ __forceinline__ void route_tokens(const Args& g, Shared& s, uint64_t*
                 atomicOr(&s.mask[e], 1u << t);
             }
         }
-    }
-    consumer_sync();
-    for (int t = warp; t < g.T; t += kConsumerWarps) {
-        float* w = s.w + t * g.k;
-        const float m = w[0];
-        __syncwarp();
-        float z = 0.0f;
-        for (int j = lane; j < g.k; j += 32) {
-            const float v = expf(w[j] - m);
-            w[j] = v;
-            z += v;
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(kFullWarp, z, off);
-        for (int j = lane; j < g.k; j += 32) w[j] = w[j] / z;
     }
     fence_proxy_async_smem();   // the ring's copies come after the keys
 }
@@ -565,109 +580,33 @@ __device__ __forceinline__ float4 h_quad(const Args& g, const Shared& s, int i, 
     return make_float4(act(gt.x, up.x), act(gt.y, up.y), act(gt.z, up.z), act(gt.w, up.w));
 }
 
-// MANY: more than 8 tokens, so that an expert may have more than 8
+// What the routing leaves for the three steps.
+struct Run {
+    uint8_t* smem;           // the ring
+    uint8_t* hbuf;
+    int rows, slots, slot_sz;
+    int S1, S2, L1, L2, G1, G2;   // tiles per expert, in all; CTAs with tiles
+    uint64_t target[2];      // of the grid barriers
+};
+
+// The three steps.  MANY: an expert has more than 8 tokens.
 template <bool FP8, bool MANY>
-__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
-    extern __shared__ uint8_t dsmem_raw[];
-    __shared__ Shared s;
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(dsmem_raw) + 127) & ~static_cast<uintptr_t>(127));
-    const int slot_sz = slot_bytes<FP8>(g.T);
+__device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r_) {
     constexpr int BK = tile_k<FP8>();
     constexpr int CK = chunk_kb<FP8>();
-    uint8_t* hbuf = smem + g.slots * slot_sz;
+    uint8_t* const smem = r_.smem;
+    uint8_t* const hbuf = r_.hbuf;
+    const int rows = r_.rows, slots = r_.slots, slot_sz = r_.slot_sz;
+    const int S1 = r_.S1, S2 = r_.S2, L1 = r_.L1, L2 = r_.L2, G1 = r_.G1, G2 = r_.G2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = gridDim.x, cta = blockIdx.x;
-
-    // (used below, so that the loads' latency hides behind the routing's)
-    const uint32_t magic = __ldcg(&g.hdr->magic);
-    uint64_t target[2] = {0, 0};
-    if (threadIdx.x == 0) {
-        // the barriers' targets: the next multiples of the grid
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-            target[i] = __ldcg(reinterpret_cast<const unsigned long long*>(&g.hdr->arrive[i][0]));
-        s.abort = 0;
-    }
-    // a slot is full when its tile's bytes are there and, for the gate/up tiles,
-    // the x slices that another warp's lanes copy
-    if (threadIdx.x < g.slots) {
-        mbar_init(&s.full[threadIdx.x], 1 + 32);
-        mbar_init(&s.empty[threadIdx.x], kGroupWarps);
-        fence_mbar_init();
-    }
-    for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) s.mask[e] = 0;
-    __syncthreads();
-
-    // ---- routing (every CTA, all tokens); keys in the ring's memory, no copy
-    // is under way yet
-    if (warp < kConsumerWarps) {
-        route_tokens<FP8>(g, s, reinterpret_cast<uint64_t*>(smem), warp, lane);
-    }
-    // a workspace that was never initialised would hang the barriers: every
-    // CTA sees the same word and leaves
-    if (magic != kMagic) {
-        if (threadIdx.x == 0) report(g.status, MOE_ERR_DEVICE);
-        return;
-    }
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) target[i] = (target[i] / G + 1) * G;
-    }
-    __syncthreads();
-    // active experts in ascending order with their first columns: one scan of
-    // (active, count) pairs over the experts, a thread each
-    const int e_own = threadIdx.x;
-    const uint32_t mk = e_own < kMaxExperts ? s.mask[e_own] : 0u;
-    const int own = mk ? (1 << 16) | __popc(mk) : 0;
-    int inc = own;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(kFullWarp, inc, off);
-        if (lane >= off) inc += o;
-    }
-    if (lane == 31 && warp < kMaxExperts / 32) s.scan[warp] = inc;
-    __syncthreads();
-    int before = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i) {
-        const int v = s.scan[i];
-        if (i < warp) before += v;
-        all += v;
-    }
-    const int n_active = all >> 16;
-    if (mk) {
-        const int ex = before + inc - own;
-        const int i = ex >> 16, c0 = ex & 0xffff;
-        s.rank[e_own] = i;
-        s.expert[i] = e_own;
-        s.base[i] = c0;
-        int c = c0;
-        for (uint32_t m = mk; m; m &= m - 1) s.tok[c++] = __ffs(m) - 1;
-    }
-    if (threadIdx.x == 0) s.base[n_active] = all & 0xffff;
-    const int S1 = g.mt_gu * g.kb_gu, S2 = g.mt_dn * g.kb_dn;   // tiles per expert
-    const int L1 = n_active * S1, L2 = n_active * S2;
-    const int G1 = L1 < G ? L1 : G, G2 = L2 < G ? L2 : G;
-    {
-        // floor(L c / G) without 64-bit products
-        const int q1 = L1 / G1, r1 = L1 - q1 * G1, q2 = L2 / G2, r2 = L2 - q2 * G2;
-        for (int c = threadIdx.x; c <= G; c += kThreads) {
-            s.start1[c] = c < G1 ? q1 * c + r1 * c / G1 : L1;
-            const int st = c < G2 ? q2 * c + r2 * c / G2 : L2;
-            s.start2[c] = st;
-            if (c < G) s.mod2[c] = st % g.mt_dn;
-        }
-        for (int f = threadIdx.x; f < 8 * kDecodeMaxT; f += kThreads) (&s.hmax[0][0])[f] = 0;
-    }
-    __syncthreads();
     const int a1 = s.start1[cta], b1 = s.start1[cta + 1];
     const int a2 = s.start2[cta], b2 = s.start2[cta + 1];
 
     if (warp == kWeightWarp) {
         // ---- one thread keeps the ring full of weight tiles through both
         // products
-        Ring ring(g.slots);
+        Ring ring(slots);
         int it = 0;
         bool ok = true;
         for (int X = a1; lane == 0 && X < b1 && ok;) {
@@ -675,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
             const uint8_t* w =
                 g.w_gu + (static_cast<size_t>(s.expert[i]) * S1 + (X - i * S1)) * kTileBytes;
             for (; X < end; ++X, w += kTileBytes) {
-                if (it >= g.slots && !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
+                if (it >= slots && !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
                     ok = false;
                     break;
                 }
@@ -697,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                     for (int L = ch.a + v0, d = 0; L < ch.b && ok; L += g.mt_dn, ++d) {
                         int m = m0, kb = kb0 + d;
                         for (int q = 0; q < kGroups; ++q) {
-                            if (it >= g.slots &&
+                            if (it >= slots &&
                                 !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
                                 ok = false;
                                 break;
@@ -727,9 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
             fault(s, g.status);
             // this CTA's copies in flight (the last `slots`, or fewer) land
             // before its shared memory goes
-            Ring back(g.slots);
+            Ring back(slots);
             for (int j = 0; j < it; ++j) {
-                if (j >= it - g.slots)
+                if (j >= it - slots)
                     mbar_wait(&s.full[back.slot], back.phase, nullptr, 10000000ull);
                 back.skip(1);
             }
@@ -738,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
         // ---- the x slices of the gate/up tiles, in 16-byte pieces, one per lane
         // and turn (as bulk copies of a few hundred bytes each they kept the copy
         // engine from the weights)
-        Ring ring(g.slots);
+        Ring ring(slots);
         int it = 0;
         constexpr int PIECES = BK / 8;                 // of a token's slice
         const int q = lane % PIECES;
@@ -747,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
             const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
             int kb = (X - i * S1) % g.kb_gu;
             for (; X < end; ++X) {
-                if (it >= g.slots && !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
+                if (it >= slots && !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
                     fault(s, g.status);
                 const uint32_t dst = smem_u32(smem + ring.slot * slot_sz + kTileBytes) + q * 16;
                 // (the last e4m3 k-block may hold 64 of its 128 columns: the rest
@@ -770,10 +709,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
         // loops run on to their ends, so all warps meet at the same barriers.
         const int gq = lane >> 2, t = lane & 3;
         const int grp = warp / kGroupWarps, wrow = warp % kGroupWarps * 32;  // first weight row
-        Ring ring(g.slots, grp);
-        float* exch = reinterpret_cast<float*>(hbuf);    // [group][T][128]
-        // while the first tiles are on their way: the optional outputs, and what
-        // the final sums will need of each assignment
+        Ring ring(slots, grp);
+        float* exch = reinterpret_cast<float*>(hbuf);    // [group][rows][128]
+        // while the first tiles are on their way: the weights, the optional
+        // outputs, and what the final sums will need of each assignment
+        if (routes_by_counting(g)) {
+            softmax_tokens(g, s, warp, lane);
+            consumer_sync();
+        }
         const float per2 = static_cast<float>(G2) / static_cast<float>(L2);
         for (int f = kConsumers - 1 - static_cast<int>(threadIdx.x); f < g.T * g.k; f += kConsumers) {
             const int e = s.ids[f], tk = f / g.k, i = s.rank[e], c0 = s.base[i];
@@ -849,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
             }
             // the groups' sums of the row tile, added in group order
             each_sum<FP8, MANY>(acc, gq, t, [&](int tk, int r, float v0, float v1) {
-                float* d = exch + (grp * g.T + tk) * kTileRows + wrow + r;
+                float* d = exch + (grp * rows + tk) * kTileRows + wrow + r;
                 if (tk < cnt) {
                     if constexpr (FP8) *d = v0;
                     else *reinterpret_cast<float2*>(d) = make_float2(v0, v1);
@@ -864,13 +807,13 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
             for (int f = threadIdx.x; f < cnt * kTileRows; f += kConsumers) {
                 float v = exch[f];
 #pragma unroll
-                for (int q = 1; q < kGroups; ++q) v += exch[q * g.T * kTileRows + f];
+                for (int q = 1; q < kGroups; ++q) v += exch[q * rows * kTileRows + f];
                 __stcg(p + f, v);
             }
             consumer_sync();
         }
         consumer_sync();
-        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[0][0], target[0]))
+        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[0][0], r_.target[0]))
             fault(s, g.status);
         consumer_sync();
 
@@ -923,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                 if (static_cast<int>(threadIdx.x) + u * kConsumers >= quads_all) continue;
                 const int c = hc[u] >> 16, j = (hc[u] & 0xffff) * 4;
                 const int kl = s.pieces[hp[u]].slot + j / BK, jj = j % BK;
-                uint8_t* d = hbuf + (kl * g.T + c) * h_row_bytes<FP8>() + jj * 2;
+                uint8_t* d = hbuf + (kl * rows + c) * h_row_bytes<FP8>() + jj * 2;
                 const float4 h = hq[u];
                 if constexpr (FP8) {
                     const float mul = f16_scale(s.hmax[hp[u]][c]);
@@ -959,9 +902,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
                 for (int v0 = 0; v0 < ch.visits; v0 += kGroups) {
                     const bool visit = v0 + vq < ch.visits;
                     float acc[4][4] = {};
-                    const uint8_t* hr = hbuf + (ch.slot + kb0) * g.T * h_row_bytes<FP8>();
+                    const uint8_t* hr = hbuf + (ch.slot + kb0) * rows * h_row_bytes<FP8>();
                     for (int L = ch.a + v0; L < ch.b;
-                         L += g.mt_dn, hr += g.T * h_row_bytes<FP8>()) {
+                         L += g.mt_dn, hr += rows * h_row_bytes<FP8>()) {
                         if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort))
                             fault(s, g.status);
                         const bool real = visit && L + vq < ch.b;
@@ -1018,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
             list_pieces(plan);
             consumer_sync();
         }
-        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[1][0], target[1]))
+        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[1][0], r_.target[1]))
             fault(s, g.status);
         consumer_sync();
 
@@ -1100,6 +1043,111 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
     }
 }
 
+// MANY: the batch has more than 8 tokens, so that an expert may
+template <bool FP8, bool MANY>
+__global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
+    extern __shared__ uint8_t dsmem_raw[];
+    __shared__ Shared s;
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(dsmem_raw) + 127) & ~static_cast<uintptr_t>(127));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = gridDim.x;
+
+    // (used below, so that the loads' latency hides behind the routing's)
+    const uint32_t magic = __ldcg(&g.hdr->magic);
+    uint64_t target[2] = {0, 0};
+    if (threadIdx.x == 0) {
+        // the barriers' targets: the next multiples of the grid
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            target[i] = __ldcg(reinterpret_cast<const unsigned long long*>(&g.hdr->arrive[i][0]));
+        s.abort = 0;
+    }
+    // a slot is full when its tile's bytes are there and, for the gate/up tiles,
+    // the x slices that another warp's lanes copy
+    if (threadIdx.x < kMaxSlots) {
+        mbar_init(&s.full[threadIdx.x], 1 + 32);
+        mbar_init(&s.empty[threadIdx.x], kGroupWarps);
+        fence_mbar_init();
+    }
+    for (int e = threadIdx.x; e < kMaxExperts; e += kThreads) s.mask[e] = 0;
+    __syncthreads();
+
+    // ---- routing (every CTA, all tokens); keys in the ring's memory, no copy
+    // is under way yet
+    if (warp < kConsumerWarps) {
+        route_tokens<FP8>(g, s, reinterpret_cast<uint64_t*>(smem), warp, lane);
+    }
+    // a workspace that was never initialised would hang the barriers: every
+    // CTA sees the same word and leaves
+    if (magic != kMagic) {
+        if (threadIdx.x == 0) report(g.status, MOE_ERR_DEVICE);
+        return;
+    }
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) target[i] = (target[i] / G + 1) * G;
+    }
+    __syncthreads();
+    // active experts in ascending order with their first columns: one scan of
+    // (active, count) pairs over the experts, a thread each
+    const int e_own = threadIdx.x;
+    const uint32_t mk = e_own < kMaxExperts ? s.mask[e_own] : 0u;
+    const int own = mk ? (1 << 16) | __popc(mk) : 0;
+    int inc = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(kFullWarp, inc, off);
+        if (lane >= off) inc += o;
+    }
+    const int most_here = __reduce_max_sync(kFullWarp, own & 0xffff);
+    if (lane == 31 && warp < kMaxExperts / 32) {
+        s.scan[warp] = inc;
+        s.most[warp] = most_here;
+    }
+    __syncthreads();
+    int before = 0, all = 0, rows = 0;
+#pragma unroll
+    for (int i = 0; i < kMaxExperts / 32; ++i) {
+        const int v = s.scan[i];
+        if (i < warp) before += v;
+        all += v;
+        rows = max(rows, s.most[i]);
+    }
+    const int n_active = all >> 16;
+    const int slot_sz = slot_bytes<FP8>(rows), slots = slots_for<FP8>(rows, g.smem);
+    uint8_t* hbuf = smem + slots * slot_sz;
+    if (mk) {
+        const int ex = before + inc - own;
+        const int i = ex >> 16, c0 = ex & 0xffff;
+        s.rank[e_own] = i;
+        s.expert[i] = e_own;
+        s.base[i] = c0;
+        int c = c0;
+        for (uint32_t m = mk; m; m &= m - 1) s.tok[c++] = __ffs(m) - 1;
+    }
+    if (threadIdx.x == 0) s.base[n_active] = all & 0xffff;
+    const int S1 = g.mt_gu * g.kb_gu, S2 = g.mt_dn * g.kb_dn;   // tiles per expert
+    const int L1 = n_active * S1, L2 = n_active * S2;
+    const int G1 = L1 < G ? L1 : G, G2 = L2 < G ? L2 : G;
+    {
+        // floor(L c / G) without 64-bit products: whole tiles, and the remainder's
+        const int q1 = L1 / G1, r1 = L1 - q1 * G1, q2 = L2 / G2, r2 = L2 - q2 * G2;
+        for (int c = threadIdx.x; c <= G; c += kThreads) {
+            s.start1[c] = c < G1 ? q1 * c + static_cast<int>(static_cast<uint32_t>(r1 * c) / G1) : L1;
+            const int st =
+                c < G2 ? q2 * c + static_cast<int>(static_cast<uint32_t>(r2 * c) / G2) : L2;
+            s.start2[c] = st;
+            if (c < G) s.mod2[c] = st % g.mt_dn;
+        }
+        for (int f = threadIdx.x; f < 8 * kDecodeMaxT; f += kThreads) (&s.hmax[0][0])[f] = 0;
+    }
+    __syncthreads();
+    const Run r{smem, hbuf, rows, slots, slot_sz, S1, S2, L1, L2, G1, G2,
+                {target[0], target[1]}};
+    if (MANY && rows > 8) run_steps<FP8, true>(g, s, r);
+    else run_steps<FP8, false>(g, s, r);
+}
+
 __global__ void decode_ws_init_kernel(Header* h) {
     if (threadIdx.x == 0) {
         h->status = 0;
@@ -1134,16 +1182,13 @@ cudaError_t launch(const Args& a, int grid, cudaStream_t s) {
     auto kern = decode_kernel<FP8, MANY>;
     const cudaError_t e = opt_in_smem<FP8, MANY>();
     if (e != cudaSuccess) return e;
-    constexpr int dyn = kDynSmemMax;
     Args g = a;
-    const int rest = 128 + h_bytes<FP8>(a.T);
-    const int slots = (dyn - rest) / slot_bytes<FP8>(a.T) / kGroups * kGroups;
-    g.slots = slots > kMaxSlots ? kMaxSlots : slots;
-    if (g.slots < kGroups) return cudaErrorInvalidValue;
+    g.smem = kDynSmemMax - 128;
+    static_assert(slots_for<FP8>(kDecodeMaxT, kDynSmemMax - 128) >= kGroups, "a slot per group");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = rest + g.slots * slot_bytes<FP8>(a.T);
+    cfg.dynamicSmemBytes = kDynSmemMax;
     cfg.stream = s;
     // cooperative: the blocks wait on one another, so all must be resident
     cudaLaunchAttribute at[1];
