@@ -29,7 +29,7 @@
  *   - Limits: 1 <= k <= E <= 256; H and I multiples of 64; block_m a multiple
  *     of 16 (the token granularity of the tensor-core tiles).
  *   - Process-wide state is limited to two things: the per-device opt-in of
- *     the GEMM kernels to more than 48 KB of shared memory (set on the first
+ *     the larger kernels to more than 48 KB of shared memory (set on the first
  *     launch on each device, read-only afterwards), and the fixed scratch
  *     array of moe_align_permute_noalloc (see its entry).  The CPU/GPU split
  *     of moe_split.h adds its host thread pool (see there).  Apart from
@@ -330,9 +330,10 @@ MOE_API moe_status moe_forward(const moe_forward_args* args, void* ws, size_t ws
  *   ws        moe_decode_workspace_size bytes, made ready once by
  *             moe_decode_workspace_init before its first call; every call
  *             leaves it ready for the next, of any T, k or layer whose size
- *             fits.  Calls that may run at the same time need workspaces of
- *             their own.  A workspace that was not initialised is reported as
- *             MOE_ERR_DEVICE in the status word (out is not written).
+ *             fits, on the same device.  Calls that may run at the same time
+ *             need workspaces of their own.  A workspace that was not
+ *             initialised is reported as MOE_ERR_DEVICE in the status word
+ *             (out is not written); initialise it again after MOE_ERR_TIMEOUT.
  * The kernel is launched cooperatively: its blocks (one per SM) exchange
  * partial sums, with bounded waits (MOE_ERR_TIMEOUT in the status word).
  * Errors: as for moe_forward; T > 16 or T * k > 128 -> MOE_ERR_UNSUPPORTED.

@@ -558,13 +558,14 @@ class MoELayer:
         return ws
 
     def decodes(self, T: int) -> bool:
-        """Whether decode is the faster form for T tokens: within its limits, and the experts
-        they may activate stream in about 60 us.  Measured on B200, decode / call: E = 128
-        H = 2048 I = 768 top-8, T = 1 33 / 42 us, T = 8 90 / 99, T = 16 137 / 142; e4m3 E = 32
-        H = I = 2880 top-4, T = 1 38 / 48, T = 4 80 / 83, T = 12 152 / 130; E = 8 H = 4096
-        I = 14336 top-2, T = 1 122 / 124, T = 4 316 / 300."""
+        """Whether decode is the faster form for T tokens: within its limits, and at most 1 GiB
+        of experts that the tokens may activate.  Measured on B200, decode / call: E = 128
+        H = 2048 I = 768 top-8, T = 1 29 / 42 us, T = 8 87 / 99, T = 16 130 / 141; e4m3 E = 32
+        H = I = 2880 top-4, T = 1 33 / 48, T = 8 103 / 111, T = 16 145 / 141; E = 64 H = 7168
+        I = 2048 top-8, T = 1 118 / 124, T = 2 212 / 208, T = 4 364 / 345; E = 8 H = 4096
+        I = 14336 top-2, T = 1 117 / 123, T = 4 287 / 279."""
         n = self.packed.numel() // self.E * min(T * self.k, self.E)
-        return T <= DECODE_MAX_T and T * self.k <= DECODE_MAX_ASSIGN and n <= 400 << 20
+        return T <= DECODE_MAX_T and T * self.k <= DECODE_MAX_ASSIGN and n <= 1 << 30
 
     def decode(self, x, logits, residual=None, out=None, ids=None, w=None, stream=None):
         """The layer for a few tokens in one kernel (see decode_forward)."""

@@ -342,3 +342,26 @@ def test_full_size(H, I, E, k, T, dtype):
     err = (out.double() - ref).norm() / ref.norm()
     # half a step of bf16, uniform in it: at most 2^-8 / sqrt(3) = 0.00226
     assert float(err) < 2.0 ** -8 / 3 ** 0.5
+
+
+def test_binding_refuses():
+    moe = lib()
+    E, k, H, I = 8, 2, 64, 64
+    layer = moe.MoELayer(*_weights(E, H, I), k)
+    x, logits, res = _inputs(3, H, E)
+    for bad in (dict(x=x.float()), dict(logits=logits.double()), dict(logits=logits[:2]),
+                dict(residual=res[:2]), dict(residual=res.float()),
+                dict(x=torch.zeros((3, 2 * H), dtype=torch.bfloat16, device=DEV)[:, :H]),
+                dict(out=torch.zeros((3, H), device=DEV)),
+                dict(ids=torch.zeros((3, k), dtype=torch.int64, device=DEV)),
+                dict(w=torch.zeros((3, k + 1), device=DEV)), dict(logits=logits.cpu())):
+        with pytest.raises(ValueError):
+            layer.decode(**{**dict(x=x, logits=logits), **bad})
+    big = _inputs(17, H, E)
+    with pytest.raises(moe.MoEError):                     # more than 16 tokens
+        layer.decode(big[0], big[1])
+    with pytest.raises(moe.MoEError):                     # a workspace for fewer tokens
+        moe.decode_forward(BF16, *big[:2], layer.packed, None, E, I, k,
+                           ws=moe.decode_workspace(BF16, 1, k, E, H, I, DEV))
+    with pytest.raises(ValueError):                       # weights of a smaller layer
+        moe.decode_forward(BF16, x, logits, layer.packed[:-16384], None, E, I, k)

@@ -199,6 +199,8 @@ def test_refusals():
             moe.linear(**{**dict(x=x, w=w), **kw})
     with pytest.raises(moe.MoEError):                       # K % 8
         moe.linear(x[:, :60], w[:, :60])
+    with pytest.raises(moe.MoEError):                       # rows off a 16-byte boundary
+        moe.linear(torch.zeros((4, 72), dtype=BF, device=DEV)[:, 4:68], w)
     with pytest.raises(moe.MoEError):                       # a broadcast residual
         moe.linear(x, w, residual=torch.zeros((1, 16), device=DEV, dtype=BF).expand(4, 16))
     with pytest.raises(ValueError):
@@ -241,3 +243,25 @@ def test_streams_graphs_and_chains():
             xs.copy_(torch.randn((M, H), device=DEV).to(BF))
             gr.replay()
             assert torch.equal(o, chain(xs))
+
+
+def test_offsets_past_32_bits():
+    """x, then out and the residual, of more than 2^31 elements: the first and last rows."""
+    moe = lib()
+    M, K, N = 270000, 8192, 16
+    x = torch.empty((M, K), dtype=BF, device=DEV).normal_()
+    w = (torch.randn((N, K), device=DEV) / K ** 0.5).to(BF)
+    out = moe.linear(x, w, act=moe.ACT_RELU)
+    for rows in (slice(0, 300), slice(M - 300, M)):
+        c = dict(x=x[rows], w=w, bias=None, residual=None)
+        _check(out[rows], c, "relu", False)
+    del x, out
+    M, K, N = 70000, 64, 32768
+    x = torch.randn((M, K), device=DEV).to(BF)
+    w = (torch.randn((N, K), device=DEV) / K ** 0.5).to(BF)
+    res = torch.empty((M, N), dtype=BF, device=DEV).normal_()
+    rows = slice(M - 200, M)
+    keep = res[rows].clone()
+    out = moe.linear(x, w, residual=res, out=res)
+    assert out is res
+    _check(out[rows], dict(x=x[rows], w=w, bias=None, residual=keep), "none", False)
