@@ -339,6 +339,7 @@ def forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int, out=N
 
 
 DECODE_MAX_T, DECODE_MAX_ASSIGN = 16, 128     # tokens, T * k
+_DECODE_WS = {}    # (device index, stream) -> the workspace of MoELayer.decode calls there
 
 
 def _on_device(dev: torch.device, stream=None):
@@ -489,7 +490,7 @@ def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=N
             raise ValueError(f"status: on {status.device}, expected cuda:{idx}")
         status_p = status.data_ptr()
     if out is None:
-        out, ldo = x.new_empty((M, N), dtype=out_dtype), N
+        out, ldo = x.new_empty((M, N)) if out_type == 0 else x.new_empty((M, N), dtype=out_dtype), N
     else:
         ldo = _rows(out, "out", M, N, out_dtype, idx)
     a = _LINEAR_ARGS.pack(M, N, K, act, gated, x.data_ptr(), w.data_ptr(), ldx, ldw, bias_p,
@@ -525,7 +526,7 @@ class MoELayer:
         self.device = Wg.device
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._ws = {}
-        self._decode_ws = {}
+        self._decode_need = {}
 
     def workspace(self, T: int) -> torch.Tensor:
         if T not in self._ws:
@@ -542,19 +543,24 @@ class MoELayer:
                        combine=self.combine, stream=stream)
 
     def decode_workspace(self, T: int, stream=None) -> torch.Tensor:
-        """The workspace of decode calls on a stream (one per stream: calls on
-        different streams may overlap).  A call captured into a graph gets one of
-        its own, whose initialisation is captured with it: the graph may be
-        replayed on any stream, and outlive the cache."""
+        """The workspace of decode calls on a stream: one per device and stream, shared by all
+        layers (calls on one stream follow one another, on different streams they may
+        overlap).  A call captured into a graph gets one of its own, whose initialisation is
+        captured with it: the graph may be replayed on any stream, and outlive the cache."""
         if torch.cuda.is_current_stream_capturing():
             return decode_workspace(self.dtype, T, self.k, self.E, self.H, self.I,
                                     self.device, stream)
-        key = _stream(stream)
-        ws, room = self._decode_ws.get(key, (None, 0))
-        if T > room:
+        need = self._decode_need.get(T)
+        if need is None:
+            need = lib().moe_decode_workspace_size(self.dtype, T, self.k, self.E, self.H, self.I)
+            self._decode_need[T] = need
+        key = (self.device.index, _stream(stream) if stream is not None else
+               torch._C._cuda_getCurrentRawStream(self.device.index))
+        ws = _DECODE_WS.get(key)
+        if ws is None or need == 0 or ws.numel() < need:
             ws = decode_workspace(self.dtype, T, self.k, self.E, self.H, self.I, self.device,
                                   stream)
-            self._decode_ws[key] = (ws, T)
+            _DECODE_WS[key] = ws
         return ws
 
     def decodes(self, T: int) -> bool:

@@ -176,6 +176,7 @@ def test_repeats_bit_for_bit_and_shares_a_workspace(dtype):
             first.setdefault(T, out)
         moe.decode_forward(dtype, xo, lo, other.packed, other.scales, 8, 128, 2, ws=ws)
     assert layer.decode_workspace(5) is ws
+    assert other.decode_workspace(3) is ws            # one per stream, whichever layer asks
     assert layer.check() == 0
 
 
