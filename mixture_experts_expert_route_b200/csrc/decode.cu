@@ -68,6 +68,7 @@ constexpr int kConsumers = kConsumerWarps * 32;
 // x slices (together the copies took longer than a tile's time)
 constexpr int kWeightWarp = kConsumerWarps, kXWarp = kConsumerWarps + 1;
 constexpr int kThreads = (kConsumerWarps + 2) * 32;
+constexpr int kBarThread = 32;          // a consumer that stands at the grid barriers
 constexpr int kMaxSlots = 12;           // a multiple of the groups: a slot stays with one
 constexpr int kSmemBytes = 227 * 1024;
 constexpr uint32_t kMagic = 0x4d6f4465u;
@@ -109,9 +110,24 @@ struct Header {
     uint64_t arrive[2][8];      // one 64-byte line per barrier
 };
 
+// Division of tile numbers (up to kDecodeMaxTiles = 2^24, so exact as floats) by
+// a divisor known at the launch: the product with its reciprocal is off by less
+// than one.  A third of the latency of an integer division, of which the way to
+// the first tile and the way from a barrier to the next products have several.
+struct Divisor {
+    int d;
+    float inv;
+};
+__host__ __device__ __forceinline__ int operator/(int x, const Divisor& v) {
+    const int q = static_cast<int>(static_cast<float>(x) * v.inv), r = x - q * v.d;
+    return q + (r >= v.d ? 1 : 0) - (r < 0 ? 1 : 0);
+}
+Divisor divisor(int d) { return Divisor{d, 1.0f / static_cast<float>(d)}; }
+
 struct Args {
     int T, k, E, H, I;
     int mt_gu, kb_gu, mt_dn, kb_dn;
+    Divisor by_mt_gu, by_kb_gu, by_mt_dn, by_S1, by_S2, by_G, by_hquads;
     const uint8_t* w_gu;
     const uint8_t* w_dn;
     const float* scales;         // [E][3], e4m3
@@ -132,7 +148,8 @@ struct Args {
 // first k-block of the h buffer, the first quad of the batch and the quads per
 // token.
 struct Piece {
-    int i, col, slot, quad, quads;
+    int i, col, slot, quad;
+    Divisor quads;
 };
 
 struct Shared {
@@ -158,7 +175,8 @@ struct Shared {
     int start1[kMaxCtas + 1];           // first gate/up tile of each CTA
     int start2[kMaxCtas + 1];           // first down tile of each CTA
     int mod2[kMaxCtas];                 // its row tile
-    float xmul[kDecodeMaxT];            // e4m3: power-of-two scale of a token's x
+    uint32_t xmax[kDecodeMaxT];         // e4m3: a token's largest finite |x|
+    float xmul[kDecodeMaxT];            // ... and its power-of-two scale
     uint32_t hmax[8][kDecodeMaxT];      // e4m3: largest |h| of a chunk's column
     Piece pieces[9];                    // of a batch, and the end
     int n_pieces;
@@ -404,13 +422,15 @@ __device__ __forceinline__ void route_tokens(const Args& g, Shared& s, uint64_t*
         keys[threadIdx.x] = e < g.E ? select_key(__ldg(g.logits + t * g.E + e), e) : 0ull;
     }
     if constexpr (FP8) {
-        // each token's f16 scale, from the last warp down
-        const int tk = kConsumerWarps - 1 - warp;
+        // each token's largest |x|, from the last warp down; a few tokens have
+        // several warps each
+        const int p2 = g.T == 1 ? 3 : g.T == 2 ? 2 : g.T <= 4 ? 1 : 0;
+        const int u = kConsumerWarps - 1 - warp, tk = u >> p2, part = u & ((1 << p2) - 1);
         if (tk < g.T) {
             const uint4* xr = reinterpret_cast<const uint4*>(g.x + static_cast<size_t>(tk) * g.H);
             uint32_t m = 0;
 #pragma unroll 8
-            for (int v = lane; v < g.H / 8; v += 32) {
+            for (int v = part * 32 + lane; v < g.H / 8; v += 32 << p2) {
                 const uint4 q = __ldg(xr + v);
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -418,7 +438,7 @@ __device__ __forceinline__ void route_tokens(const Args& g, Shared& s, uint64_t*
                     m = max(m, max(finite_mag(bf16_lo(w[j])), finite_mag(bf16_hi(w[j]))));
             }
             m = __reduce_max_sync(kFullWarp, m);
-            if (lane == 0) s.xmul[tk] = f16_scale(m);
+            if (lane == 0) atomicMax(&s.xmax[tk], m);
         }
     }
     if (!counting) {
@@ -442,8 +462,12 @@ __device__ __forceinline__ void route_tokens(const Args& g, Shared& s, uint64_t*
             const int t = f / Ep, e = f - t * Ep;
             const uint64_t own = keys[f];
             int place = 0;
+            const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(keys + t * Ep);
 #pragma unroll 4
-            for (int i = part; i < Ep; i += parts) place += keys[t * Ep + i] > own;
+            for (int i = part; i < Ep / 2; i += parts) {
+                const ulonglong2 two = pairs[i];
+                place += (two.x > own) + (two.y > own);
+            }
             for (int off = 1; off < parts; off *= 2)
                 place += __shfl_xor_sync(kFullWarp, place, off);
             if (part == 0 && e < g.E && place < g.k) {
@@ -490,15 +514,16 @@ struct Chunk {
 // The chunks of a CTA in order, in batches that share the h buffer (CK
 // k-blocks): as many whole experts' ranges as fit, or CK k-blocks of one.
 struct Plan {
-    int X, end, a2, S2, MT, CK, left;
-    __device__ __forceinline__ Plan(int from, int to, int S2_, int MT_, int CK_)
-        : X(from), end(to), a2(from), S2(S2_), MT(MT_), CK(CK_), left(CK_) {}
+    int X, end, a2, CK, left;
+    Divisor S2, MT;
+    __device__ __forceinline__ Plan(int from, int to, const Args& g, int CK_)
+        : X(from), end(to), a2(from), CK(CK_), left(CK_), S2(g.by_S2), MT(g.by_mt_dn) {}
     __device__ __forceinline__ bool done() const { return X >= end; }
     __device__ __forceinline__ void batch() { left = CK; }
     __device__ __forceinline__ bool take(Chunk& c) {
         if (X >= end) return false;
         c.i = X / S2;
-        const int base = c.i * S2, to = min(end - base, S2);
+        const int base = c.i * S2.d, to = min(end - base, S2.d);
         c.a = X - base;
         c.kb0 = c.a / MT;
         c.kb1 = (to - 1) / MT + 1;
@@ -506,10 +531,10 @@ struct Plan {
             if (left < CK) return false;
             c.kb1 = c.kb0 + CK;
         }
-        c.b = min(c.kb1 * MT, to);
+        c.b = min(c.kb1 * MT.d, to);
         c.kb = c.kb0;
-        c.m = c.a - c.kb0 * MT;
-        c.visits = min(c.b - c.a, MT);
+        c.m = c.a - c.kb0 * MT.d;
+        c.visits = min(c.b - c.a, MT.d);
         c.slot = CK - left;
         c.first = X == a2 || c.a == 0;
         left -= c.kb1 - c.kb0;
@@ -586,7 +611,7 @@ struct Run {
     uint8_t* hbuf;
     int rows, slots, slot_sz;
     int S1, S2, L1, L2, G1, G2;   // tiles per expert, in all; CTAs with tiles
-    uint64_t target[2];      // of the grid barriers
+    uint64_t seen[2];        // (kBarThread) the grid barriers' counters
 };
 
 // The three steps.  MANY: an expert has more than 8 tokens.
@@ -610,7 +635,7 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
         int it = 0;
         bool ok = true;
         for (int X = a1; lane == 0 && X < b1 && ok;) {
-            const int i = X / S1, end = (i + 1) * S1 < b1 ? (i + 1) * S1 : b1;
+            const int i = X / g.by_S1, end = (i + 1) * S1 < b1 ? (i + 1) * S1 : b1;
             const uint8_t* w =
                 g.w_gu + (static_cast<size_t>(s.expert[i]) * S1 + (X - i * S1)) * kTileBytes;
             for (; X < end; ++X, w += kTileBytes) {
@@ -625,7 +650,7 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
                 ++it;
             }
         }
-        Plan plan(a2, b2, S2, g.mt_dn, CK);
+        Plan plan(a2, b2, g, CK);
         Chunk ch;
         while (lane == 0 && ok && !plan.done()) {
             plan.batch();
@@ -682,9 +707,9 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
         constexpr int PIECES = BK / 8;                 // of a token's slice
         const int q = lane % PIECES;
         for (int X = a1; X < b1;) {
-            const int i = X / S1, end = (i + 1) * S1 < b1 ? (i + 1) * S1 : b1;
+            const int i = X / g.by_S1, end = (i + 1) * S1 < b1 ? (i + 1) * S1 : b1;
             const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
-            int kb = (X - i * S1) % g.kb_gu;
+            int kb = X - X / g.by_kb_gu * g.kb_gu;
             for (; X < end; ++X) {
                 if (it >= slots && !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
                     fault(s, g.status);
@@ -734,7 +759,7 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
         }
         // the first batch's pieces of h, one per chunk, for the thread per four
         // columns (see step 2)
-        Plan plan(a2, b2, S2, g.mt_dn, CK);
+        Plan plan(a2, b2, g, CK);
         auto list_pieces = [&](Plan q) {
             if (threadIdx.x != 0) return;
             Chunk c;
@@ -742,17 +767,24 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
             q.batch();
             for (; q.take(c); ++n) {
                 const int quads = (c.kb1 - c.kb0) * (BK / 4);
-                s.pieces[n] = Piece{c.i, c.kb0 * BK, c.slot, quad, quads};
+                s.pieces[n] = Piece{c.i, c.kb0 * BK, c.slot, quad,
+                                    Divisor{quads, __frcp_rn(static_cast<float>(quads))}};
                 quad += quads * (s.base[c.i + 1] - s.base[c.i]);
             }
             s.pieces[n].quad = quad;
             s.n_pieces = n;
         };
         list_pieces(plan);
+        // the barriers' targets: the next multiples of the grid
+        uint64_t target[2] = {0, 0};
+        if (threadIdx.x == kBarThread) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) target[i] = (r_.seen[i] / G + 1) * G;
+        }
         // step 1: gate/up partial sums
         for (int X = a1; X < b1;) {
-            const int r = X / g.kb_gu;                 // row tile over all active experts
-            const int i = r / g.mt_gu, m = r - i * g.mt_gu;
+            const int r = X / g.by_kb_gu;               // row tile over all active experts
+            const int i = r / g.by_mt_gu, m = r - i * g.mt_gu;
             const int end = (r + 1) * g.kb_gu < b1 ? (r + 1) * g.kb_gu : b1;
             const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
             const int ra = gq < cnt ? gq : 0, rb = gq + 8 < cnt ? gq + 8 : 0;
@@ -813,7 +845,7 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
             consumer_sync();
         }
         consumer_sync();
-        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[0][0], r_.target[0]))
+        if (threadIdx.x == kBarThread && !grid_barrier(&g.hdr->arrive[0][0], target[0]))
             fault(s, g.status);
         consumer_sync();
 
@@ -838,7 +870,7 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
                 int n = 0;
                 while (s.pieces[n + 1].quad <= idx) ++n;
                 const Piece pc = s.pieces[n];
-                const int r = idx - pc.quad, c = r / pc.quads, j = r - c * pc.quads;
+                const int r = idx - pc.quad, c = r / pc.quads, j = r - c * pc.quads.d;
                 hp[u] = n;
                 hc[u] = c << 16 | j;
                 if (pc.col + 4 * j < g.I) {
@@ -961,10 +993,6 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
             list_pieces(plan);
             consumer_sync();
         }
-        if (threadIdx.x == 0 && !grid_barrier(&g.hdr->arrive[1][0], r_.target[1]))
-            fault(s, g.status);
-        consumer_sync();
-
         // step 3: out[t] = residual[t] + sum over the token's assignments and
         // their CTAs; four columns a thread.  When there are few outputs `spl`
         // threads share one's terms: `sj` of them the assignments, sc = spl / sj
@@ -978,11 +1006,26 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
         const int lw = 1 << lw2, ws = 1 << ws2, per_cta = kConsumers >> spl2;
         const int sub = ((warp & (ws - 1)) << ls2) + (lane >> lw2);
         const int jsub = sub & (sj - 1), csub = sub >> sj2;
+        // the first item's residual is on its way while the CTA waits
+        auto item_of = [&](int item0) {
+            return item0 + ((warp >> ws2) << lw2) + (lane & (lw - 1));
+        };
+        auto residual_of = [&](int item) {
+            return g.residual && sub == 0 && item < items
+                       ? __ldcg(reinterpret_cast<const uint2*>(g.residual) + item)
+                       : make_uint2(0u, 0u);
+        };
+        uint2 res = residual_of(item_of(cta * per_cta));
+        if (threadIdx.x == kBarThread && !grid_barrier(&g.hdr->arrive[1][0], target[1]))
+            fault(s, g.status);
+        consumer_sync();
+
         float4* red = reinterpret_cast<float4*>(smem);   // the ring has run dry
         const size_t step = static_cast<size_t>(g.T) * g.mt_dn * kTileRows;
         for (int item0 = cta * per_cta; item0 < items; item0 += G * per_cta) {
-            const int item = item0 + ((warp >> ws2) << lw2) + (lane & (lw - 1));
-            const int tk = item / hquads, col = (item - tk * hquads) * 4;
+            const int item = item_of(item0);
+            if (item0 != cta * per_cta) res = residual_of(item);
+            const int tk = item / g.by_hquads, col = (item - tk * hquads) * 4;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             if (item < items) {
                 const int m = col / kTileRows, row = col - m * kTileRows;
@@ -1031,11 +1074,9 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
             }
             if (sub == 0 && item < items) {
                 const size_t o = static_cast<size_t>(tk) * g.H + col;
-                if (g.residual) {
-                    const uint2 r = *reinterpret_cast<const uint2*>(g.residual + o);
-                    sum = add4(sum, make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y),
-                                                bf16_hi(r.y)));
-                }
+                if (g.residual)
+                    sum = add4(sum, make_float4(bf16_lo(res.x), bf16_hi(res.x), bf16_lo(res.y),
+                                                bf16_hi(res.y)));
                 *reinterpret_cast<uint2*>(g.out + o) =
                     make_uint2(bf16x2(sum.x, sum.y), bf16x2(sum.z, sum.w));
             }
@@ -1054,14 +1095,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
 
     // (used below, so that the loads' latency hides behind the routing's)
     const uint32_t magic = __ldcg(&g.hdr->magic);
-    uint64_t target[2] = {0, 0};
-    if (threadIdx.x == 0) {
-        // the barriers' targets: the next multiples of the grid
+    uint64_t seen[2] = {0, 0};
+    if (threadIdx.x == kBarThread) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-            target[i] = __ldcg(reinterpret_cast<const unsigned long long*>(&g.hdr->arrive[i][0]));
+            seen[i] = __ldcg(reinterpret_cast<const unsigned long long*>(&g.hdr->arrive[i][0]));
         s.abort = 0;
     }
+    if (threadIdx.x < kDecodeMaxT) s.xmax[threadIdx.x] = 0;
     // a slot is full when its tile's bytes are there and, for the gate/up tiles,
     // the x slices that another warp's lanes copy
     if (threadIdx.x < kMaxSlots) {
@@ -1082,10 +1123,6 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
     if (magic != kMagic) {
         if (threadIdx.x == 0) report(g.status, MOE_ERR_DEVICE);
         return;
-    }
-    if (threadIdx.x == 0) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) target[i] = (target[i] / G + 1) * G;
     }
     __syncthreads();
     // active experts in ascending order with their first columns: one scan of
@@ -1131,19 +1168,21 @@ __global__ void __launch_bounds__(kThreads, 1) decode_kernel(const Args g) {
     const int G1 = L1 < G ? L1 : G, G2 = L2 < G ? L2 : G;
     {
         // floor(L c / G) without 64-bit products: whole tiles, and the remainder's
-        const int q1 = L1 / G1, r1 = L1 - q1 * G1, q2 = L2 / G2, r2 = L2 - q2 * G2;
+        // (with fewer tiles than CTAs a tile each)
+        const int q1 = L1 / g.by_G, r1 = L1 - q1 * G, q2 = L2 / g.by_G, r2 = L2 - q2 * G;
         for (int c = threadIdx.x; c <= G; c += kThreads) {
-            s.start1[c] = c < G1 ? q1 * c + static_cast<int>(static_cast<uint32_t>(r1 * c) / G1) : L1;
-            const int st =
-                c < G2 ? q2 * c + static_cast<int>(static_cast<uint32_t>(r2 * c) / G2) : L2;
+            s.start1[c] = c < G1 ? (L1 < G ? c : q1 * c + r1 * c / g.by_G) : L1;
+            const int st = c < G2 ? (L2 < G ? c : q2 * c + r2 * c / g.by_G) : L2;
             s.start2[c] = st;
-            if (c < G) s.mod2[c] = st % g.mt_dn;
+            if (c < G) s.mod2[c] = st - st / g.by_mt_dn * g.mt_dn;
         }
+        if (FP8 && threadIdx.x < kDecodeMaxT)
+            s.xmul[threadIdx.x] = f16_scale(s.xmax[threadIdx.x]);
         for (int f = threadIdx.x; f < 8 * kDecodeMaxT; f += kThreads) (&s.hmax[0][0])[f] = 0;
     }
     __syncthreads();
     const Run r{smem, hbuf, rows, slots, slot_sz, S1, S2, L1, L2, G1, G2,
-                {target[0], target[1]}};
+                {seen[0], seen[1]}};
     if (MANY && rows > 8) run_steps<FP8, true>(g, s, r);
     else run_steps<FP8, false>(g, s, r);
 }
@@ -1240,6 +1279,13 @@ cudaError_t launch_decode(const DecodeProblem& p, cudaStream_t s) {
     g.kb_gu = geo.kb_gu;
     g.mt_dn = geo.mt_dn;
     g.kb_dn = geo.kb_dn;
+    g.by_mt_gu = divisor(g.mt_gu);
+    g.by_kb_gu = divisor(g.kb_gu);
+    g.by_mt_dn = divisor(g.mt_dn);
+    g.by_S1 = divisor(g.mt_gu * g.kb_gu);
+    g.by_S2 = divisor(g.mt_dn * g.kb_dn);
+    g.by_G = divisor(grid);
+    g.by_hquads = divisor(g.H / 4);
     g.w_gu = static_cast<const uint8_t*>(p.packed);
     g.w_dn = g.w_gu + geo.gu_bytes;
     g.scales = p.scales;

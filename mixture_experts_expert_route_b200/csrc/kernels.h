@@ -194,7 +194,8 @@ int device_sm_count();
 
 // ---- the whole layer for a few tokens (decode.cu)
 constexpr int kDecodeMaxT = 16;
-constexpr int kDecodeMaxAssign = 128;   // T * k
+constexpr int kDecodeMaxAssign = 128;       // T * k
+constexpr int kDecodeMaxTiles = 1 << 24;    // of the active experts in a product: 256 GiB
 struct DecodeProblem {
     int fp8, T, k, E, H, I;
     const void* x;

@@ -629,12 +629,13 @@ moe_status check_decode(moe_dtype dt, int T, int k, int E, int H, int I) {
     if (st != MOE_OK) return st;
     if (T > kDecodeMaxT || static_cast<long long>(T) * k > kDecodeMaxAssign)
         return MOE_ERR_UNSUPPORTED;
-    // tile indices over the active experts are 32-bit
+    // tile numbers over the active experts, and groups of four outputs
+    if (static_cast<long long>(T) * H / 4 > kDecodeMaxTiles) return MOE_ERR_UNSUPPORTED;
     const PackedGeom g = packed_geom(dt == MOE_FP8_E4M3, 1, H, I);
     const long long act = static_cast<long long>(T) * k < E ? T * k : E;
-    if (act * g.mt_gu * g.kb_gu > 0x7fffffffLL || act * g.mt_dn * g.kb_dn > 0x7fffffffLL)
+    if (act * g.mt_gu * g.kb_gu > kDecodeMaxTiles || act * g.mt_dn * g.kb_dn > kDecodeMaxTiles)
         return MOE_ERR_UNSUPPORTED;
-    // and so are the columns of the partial sums
+    // the columns of the partial sums are 32-bit
     if ((static_cast<long long>(kDecodeMaxAssign) + kMaxCtas * T) * g.mt_dn > 0x7fffffffLL)
         return MOE_ERR_UNSUPPORTED;
     return MOE_OK;
