@@ -180,6 +180,27 @@ def test_repeats_bit_for_bit_and_shares_a_workspace(dtype):
     assert layer.check() == 0
 
 
+@pytest.mark.parametrize("T,E,k,H,I,dtype", [(1, 8, 2, 2048, 3584, BF16), (1, 64, 8, 1024, 512, BF16),
+                                             (16, 32, 4, 1024, 768, BF16), (1, 32, 4, 1472, 1472, FP8),
+                                             (13, 32, 4, 1472, 1472, FP8), (3, 2, 1, 64, 64, BF16)])
+def test_no_partial_sum_is_read_before_it_is_written(T, E, k, H, I, dtype):
+    """With NaN in all of the workspace but its header every output is the same: each CTA waits
+    for the others' sums, and reads only sums of this call."""
+    moe = lib()
+    layer = moe.MoELayer(*_weights(E, H, I), k, dtype=dtype)
+    ws = moe.decode_workspace(dtype, T, k, E, H, I, torch.device(DEV))
+    for seed in range(8):
+        x, logits, res = _inputs(T, H, E, seed=seed)
+        args = (dtype, x, logits, layer.packed, layer.scales, E, I, k, res)
+        out = moe.decode_forward(*args, ws=ws)
+        for _ in range(4):
+            poisoned = torch.full_like(ws, 0xFF)
+            code = moe._lib.lib().moe_decode_workspace_init(
+                poisoned.data_ptr(), poisoned.numel(), torch.cuda.current_stream().cuda_stream)
+            assert code == 0
+            assert torch.equal(moe.decode_forward(*args, ws=poisoned), out)
+
+
 def test_residual_may_be_the_output():
     moe = lib()
     T, E, k, H, I = 5, 8, 2, 256, 192
