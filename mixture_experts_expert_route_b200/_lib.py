@@ -584,7 +584,11 @@ class MoELayer:
                               self.decode_workspace(T) if T > 0 else None)
 
     def check(self) -> int:
-        return check_status(self.status)
+        code = check_status(self.status)
+        if code == 5:       # a wait ran out: later decode calls get workspaces made anew
+            for key in [key for key in _DECODE_WS if key[0] == self.device.index]:
+                del _DECODE_WS[key]
+        return code
 
 
 class MoEBlock:

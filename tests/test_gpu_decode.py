@@ -201,6 +201,19 @@ def test_no_partial_sum_is_read_before_it_is_written(T, E, k, H, I, dtype):
             assert torch.equal(moe.decode_forward(*args, ws=poisoned), out)
 
 
+def test_a_timeout_makes_the_workspaces_anew():
+    """After MOE_ERR_TIMEOUT (here written by the host) decode calls do not use the old one."""
+    moe = lib()
+    layer = moe.MoELayer(*_weights(8, 256, 128), 2)
+    x, logits, _ = _inputs(3, 256, 8)
+    out, ws = layer.decode(x, logits), layer.decode_workspace(3)
+    assert layer.check() == 0 and layer.decode_workspace(3) is ws
+    layer.status.fill_(5)
+    assert layer.check() == 5 and layer.decode_workspace(3) is not ws
+    layer.status.zero_()
+    assert torch.equal(layer.decode(x, logits), out) and layer.check() == 0
+
+
 def test_residual_may_be_the_output():
     moe = lib()
     T, E, k, H, I = 5, 8, 2, 256, 192
