@@ -9,7 +9,7 @@
 // rounding to the output type.  The router's logits (fp32 out), a shared
 // expert's two products, and the projections before and after the layer.
 //
-// Three kernels, by what bounds them:
+// Four kernels, by what bounds them:
 //   few   M <= 16: the stream of W.  Warp MMAs fed by 16-byte loads from global
 //         memory, no shared memory and no barrier in the way; K is split over
 //         warps, and over the blocks of a cluster, until about 16 warps per SM
@@ -19,6 +19,7 @@
 //         through distributed shared memory.
 //   pair  256 x 256 tiles on CTA pairs (cta_group::2), persistent, two TMEM
 //         accumulators, so an epilogue runs under the next tile's products.
+//   split such a tile on a cluster of two pairs, half of a long K each.
 // No kernel needs a workspace, and no sum depends on timing.
 //
 // Measured on one B200 in a graph (us; floor at the measured copy and bf16 GEMM
@@ -27,8 +28,8 @@
 //         M=16 K=14336 N=4096 residual  22.9  (18, 22)
 //   tile  M=77 K=N=2880                 12    (2.7, 7)   latency: ~8 us of launch,
 //         first copies, cluster sum and store around 11 k-blocks a block
-//         M=512 K=7168 N=2x2048 gated   34    (18, 25)   shared memory: a 128-wide
-//         tile reads 1.5x what its MMAs take
+//   split M=512 K=7168 N=2x2048 gated   28    (18, 25)   128-wide tiles 34: they read
+//         1.5x the shared memory that their MMAs take
 //   pair  M=8192 K=7168 N=2x2048 gated  330-390 (288 at the burst rate; cuBLAS
 //         369-372 in the same runs): the power cap; M=1024 K=N=4096 32 (21, 25)
 #include <cstdint>
@@ -221,6 +222,11 @@ __device__ __forceinline__ float ld_cluster(uint32_t a) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
+}
+__device__ __forceinline__ void st_cluster4(uint32_t a, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w)
+                 : "memory");
 }
 __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
     float4 v;
@@ -857,6 +863,230 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
 }
 
+// ================================================================= split
+// The pair kernel's 256 x 256 tile, one per cluster of two pairs that split K:
+// for long products with too few such tiles for all pairs.  The CTAs of the same
+// 128 rows then finish half of the columns each: either pushes its sums of the
+// other's half into that one's ring, which has run dry.  The exchange costs 5 us
+// (16.5 us in all at M = 512, K = 2048, N = 4096, where the products take 5).
+constexpr int kSplitW = kPairN / 2;            // accumulator columns of a share
+constexpr int kSplitLD = kSplitW + 4;          // the 4 keep 16-byte stores of 8 lanes on
+                                               // different banks
+static_assert(128 * kSplitLD * 4 <= kPairStages * kPairStageBytes, "a share fits into the ring");
+__device__ __forceinline__ void umma_commit_pair_of(uint64_t* bar, int pair) {
+    const uint16_t mask = static_cast<uint16_t>(0x3 << (2 * pair));
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(mask)
+        : "memory");
+}
+
+// 16 finished columns of a row, without the pair kernel's overlap.
+__device__ __forceinline__ void finish16(const Args& g, long long row, int col, float (&v)[16],
+                                         const float (&u)[16]) {
+    activate(v, g.act);
+    if (g.gated) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] *= u[j];
+    }
+    if (row >= g.M) return;
+    if (wide16(g, col)) {
+        if (g.residual) {
+            uint32_t qa[8], qb[8];
+            res16(g, row, col, qa, qb);
+            add_res16(g, v, qa, qb);
+        }
+        store16(g, row, col, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (col + j < g.N) store_one(g, row, col + j, v[j]);
+    }
+}
+
+__global__ void __launch_bounds__(kPairThreads, 1)
+    linear_split_kernel(const __grid_constant__ Maps maps, const Args g) {
+    extern __shared__ uint8_t dsmem_raw[];
+    __shared__ PairCtl ctl;
+    uint8_t* base = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    constexpr int BN = kPairN, STAGE = kPairStageBytes, S = kPairStages;
+    constexpr int W = kSplitW, LD = kSplitLD;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank()), side = rank & 1, pair = rank >> 1;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&ctl.full[i], 1);
+            mbar_init(&ctl.empty[i], 1);
+        }
+        mbar_init(&ctl.tfull[0], 1);
+        mbar_init(&ctl.drain, 1);
+        fence_mbar_init();
+        ctl.abort = 0;
+        ctl.prod_pos = ctl.mma_pos = ctl.mma_issued = 0;
+        tma_prefetch_desc(&maps.x);
+        tma_prefetch_desc(&maps.w);
+    }
+    if (warp == 2) {
+        tmem_alloc_pair(&ctl.tmem, BN);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync();          // the peers' barriers are initialised
+    const uint32_t tmem = ctl.tmem;
+    pdl_wait();
+    pdl_trigger();
+
+    const int per = g.gated ? BN / 2 : BN;
+    const int tm = (g.M + 255) / 256, t = blockIdx.x / 4;
+    const int m = t % tm, n0 = t / tm * per;
+    const int KB = (g.K + kBK - 1) / kBK;
+    const int kb0 = pair ? KB / 2 : 0, kb1 = pair ? KB : KB / 2;
+    auto raise = [&]() {
+        report(g.status, MOE_ERR_TIMEOUT);
+        *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
+    };
+    const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
+    const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // as in the pair kernel
+            const int xrow = m * 256 + side * 128;
+            const int wrow = g.gated ? side * g.N + n0 : n0 + side * (BN / 2);
+            uint32_t it = 0;
+            int st = 0;
+            uint32_t par = 1;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                if (!mbar_wait(&ctl.empty[st], par, &ctl.abort)) {
+                    raise();
+                    break;
+                }
+                uint8_t* a = base + st * STAGE;
+                if (side == 0) mbar_arrive_expect_tx(&ctl.full[st], 2 * STAGE);
+                tma_load_2d_pair(a, &maps.x, &ctl.full[st], kb * kBK, xrow, kEvictNormal);
+                tma_load_2d_pair(a + 128 * kRowBytes, &maps.w, &ctl.full[st], kb * kBK, wrow,
+                                 kEvictNormal);
+                if (++st == S) {
+                    st = 0;
+                    par ^= 1u;
+                }
+            }
+            ctl.prod_pos = it;
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && side == 0) {
+            const uint32_t idesc = make_idesc<false>(256, BN);
+            const uint64_t a0 = sw128_desc(smem_u32(base));
+            const uint64_t b0 = sw128_desc(smem_u32(base + 128 * kRowBytes));
+            int st = 0;
+            uint32_t ph = 0, it = 0;
+            bool ok = true;
+            ctl.mma_issued = 1;
+            for (int kb = kb0; kb < kb1; ++kb, ++it) {
+                if (!mbar_wait(&ctl.full[st], ph, &ctl.abort)) {
+                    raise();
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t ad = a0 + static_cast<uint32_t>(st * (STAGE >> 4));
+                const uint64_t bd = b0 + static_cast<uint32_t>(st * (STAGE >> 4));
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_pair<false>(tmem, ad + 2 * kk, bd + 2 * kk, idesc, (it | kk) ? 1u : 0u);
+                umma_commit_pair_of(&ctl.empty[st], pair);
+                if (++st == S) {
+                    st = 0;
+                    ph ^= 1u;
+                }
+            }
+            if (ok) umma_commit_pair_of(&ctl.tfull[0], pair);
+            ctl.mma_pos = it;
+        }
+        __syncwarp();
+    } else if (warp >= kEpiWarp0) {
+        // the tile's bias, in accumulator column order
+        const int et = threadIdx.x - kEpiWarp0 * 32;
+        if (et < BN) {
+            const int c = n0 + (g.gated && et >= BN / 2 ? et - BN / 2 : et);
+            ctl.bias[0][et] = c < g.N ? load_bias(g, g.gated && et >= BN / 2 ? g.N + c : c) : 0.0f;
+        }
+        if (!mbar_wait(&ctl.tfull[0], 0, &ctl.abort)) raise();
+        tc_fence_after();
+    }
+    __syncthreads();
+    if (*reinterpret_cast<volatile int*>(&ctl.abort)) {
+        // own products and copies in flight end (bounded) before the ring is
+        // written over
+        if (warp == 1 && lane == 0 && ctl.mma_issued) {
+            umma_commit_pair_local(&ctl.drain);
+            mbar_wait(&ctl.drain, 0, nullptr, kDrainLimitNs);
+        }
+        if (warp == 0 && lane == 0 && side == 0) {
+            for (uint32_t it = ctl.mma_pos; it < ctl.prod_pos; ++it)
+                mbar_wait(&ctl.full[it % S], (it / S) & 1u, nullptr, kDrainLimitNs);
+        }
+        __syncthreads();
+    }
+    cluster_sync();          // every ring is idle
+    // accumulator column of column l of share j: a gated share's first half are
+    // gate columns, its second half their up columns
+    auto column = [&](int j, int l) {
+        return g.gated ? (l < W / 2 ? j * (W / 2) + l : BN / 2 + j * (W / 2) + l - W / 2) : j * W + l;
+    };
+    const int srow = 32 * q + lane;
+    float* const share = reinterpret_cast<float*>(base) + srow * LD;     // [128 rows][LD]
+    if (warp >= kEpiWarp0) {
+        const uint32_t dst = cluster_addr(smem_u32(share + half * (W / 2)), rank ^ 2);
+#pragma unroll
+        for (int c = 0; c < W / 2; c += 16) {
+            float v[16];
+            tmem_ld16(ta + column(pair ^ 1, half * (W / 2) + c), v);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+                st_cluster4(dst + (c + i) * 4, make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+        }
+    }
+    cluster_sync();          // both shares have arrived
+    if (warp >= kEpiWarp0) {
+        const int outs = g.gated ? W / 2 : W;              // output columns of a share
+        const long long row = static_cast<long long>(m) * 256 + side * 128 + srow;
+        auto total = [&](int l, float (&v)[16]) {
+            const int at = column(pair, l);
+            tmem_ld16(ta + at, v);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                const float4 o = *reinterpret_cast<const float4*>(share + l + i);
+                v[i] += o.x;
+                v[i + 1] += o.y;
+                v[i + 2] += o.z;
+                v[i + 3] += o.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] += ctl.bias[0][at + i];
+        };
+        for (int l = half * (outs / 2); l < (half + 1) * (outs / 2); l += 16) {
+            const int col = n0 + pair * outs + l;
+            if (col >= g.N) break;
+            float v[16], u[16];
+            total(l, v);
+            if (g.gated) total(l + W / 2, u);
+            finish16(g, row, col, v, u);
+        }
+    }
+    tc_fence_before();
+    cluster_sync();          // both CTAs of a pair have read their accumulators
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, BN);
+    }
+}
+
 // ---- host side
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -982,6 +1212,46 @@ cudaError_t launch_pair(const Args& g, int sms, cudaStream_t s) {
                   g);
 }
 
+// Clusters of four CTAs of the split kernel that run at the same time, per device
+// (0: none; 33 on a B200, whose GPCs are no multiples of four SMs).
+int split_clusters() {
+    static std::once_flag once[kMaxDevices];
+    static int count[kMaxDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+    std::call_once(once[dev], [&] {
+        if (cudaFuncSetAttribute(linear_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kPairSmemBytes) != cudaSuccess)
+            return;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(4);
+        cfg.blockDim = dim3(kPairThreads);
+        cfg.dynamicSmemBytes = kPairSmemBytes;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = 4;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, linear_split_kernel, &cfg) == cudaSuccess)
+            count[dev] = n;
+        else
+            cudaGetLastError();     // (the other kernels take the product)
+    });
+    return count[dev];
+}
+
+cudaError_t launch_split(const Args& g, long long tiles, cudaStream_t s) {
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    if (!make_map(&maps.x, g.x, g.K, g.M, g.ldx, 128) ||
+        !make_map(&maps.w, g.w, g.K, g.gated ? 2LL * g.N : g.N, g.ldw, kPairN / 2))
+        return cudaErrorInvalidValue;
+    return launch(linear_split_kernel, tiles * 4, kPairThreads, kPairSmemBytes, 4, s, maps, g);
+}
+
 }  // namespace
 
 cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s) {
@@ -1019,6 +1289,13 @@ cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s) {
     const long long t256 = (static_cast<long long>(p.M) + 255) / 256 *
                            ((static_cast<long long>(p.N) + per - 1) / per);
     if (p.M > 128 && t256 * 4 >= sms) return launch_pair(g, sms, s);
+    // Fewer such tiles: two pairs to each, where all are resident and K is long
+    // enough to pay for their exchange (us, split / 128-wide): M = 512, K = 7168,
+    // N = 2 x 2048 (32) 28 / 34; K = N = 4096 23 / 27; M = 256, K = N = 7168 (28)
+    // 29 / 36; M = 512, K = 2048, N = 4096 16.5 / 16.8; with 16 tiles, M = 256,
+    // K = N = 4096 19 / 17.
+    if (p.M > 128 && t256 > 16 && p.K >= 4096 && t256 <= split_clusters())
+        return launch_split(g, t256, s);
     const long long t128 = (static_cast<long long>(p.M) + 127) / 128 *
                            ((static_cast<long long>(p.N) + per / 2 - 1) / (per / 2));
     if (t128 * 2 >= sms) return launch_tile<128>(g, sms, s);

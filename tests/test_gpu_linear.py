@@ -107,6 +107,34 @@ def test_pair_sizes(M, N, K, gated):
         _check(_run(moe, c, act, gated, out), c, act, gated)
 
 
+# 17 to 33 such tiles and a long K: two CTA pairs to a tile
+SPLIT_SIZES = [(257, 2300, 4096, False), (257, 1200, 4104, True), (700, 1500, 4136, False),
+               (129, 6001, 5000, False), (600, 799, 4096, True), (512, 2048, 4160, True)]
+
+
+@pytest.mark.parametrize("M,N,K,gated", SPLIT_SIZES)
+def test_split_sizes(M, N, K, gated):
+    moe = lib()
+    for act, bias, residual, out, pad in (("none", None, True, BF, 0), ("silu", BF, False, BF, 8),
+                                          ("gelu_tanh", F32, True, F32, 0)):
+        c = _make(M, N, K, gated, bias, residual, out, pad=pad)
+        y = _run(moe, c, act, gated, out)
+        _check(y, c, act, gated)
+        for _ in range(3):
+            assert torch.equal(_run(moe, c, act, gated, out), y)
+    z = c["residual"].clone()                         # in place, and into wider rows
+    assert torch.equal(moe.linear(c["x"], c["w"], bias=c["bias"], act=moe.ACT_GELU_TANH,
+                                  gated=gated, residual=z, out=z), y)
+    wide = torch.full((M, N + 24), 7.0, dtype=F32, device=DEV)
+    _run(moe, c, "gelu_tanh", gated, F32, out=wide[:, 8:N + 8])
+    assert torch.equal(wide[:, 8:N + 8], y)
+    assert bool((wide[:, :8] == 7).all()) and bool((wide[:, N + 8:] == 7).all())
+    # a non-finite value stays in its row (x) or its column (w)
+    c["x"][M - 1, 0], c["w"][0, K - 1] = float("inf"), float("nan")
+    bad = ~torch.isfinite(_run(moe, c, "gelu_tanh", gated, F32))
+    assert bool(bad[:, 0].all()) and not bool(bad[:M - 1, 1:].any())
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("M", [5, 40, 5000])
 def test_activations(M, act):
