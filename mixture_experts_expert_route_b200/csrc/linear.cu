@@ -26,12 +26,14 @@
 // rates; cuBLAS = the plain product alone, no epilogue):
 //   few   M=1  K=7168 N=2x2048 gated    12.7  (floor 9.0 by bytes, cuBLAS 20)
 //         M=16 K=14336 N=4096 residual  22.9  (18, 22)
-//   tile  M=77 K=N=2880                 12    (2.7, 7)   latency: ~8 us of launch,
-//         first copies, cluster sum and store around 11 k-blocks a block
-//   split M=512 K=7168 N=2x2048 gated   28    (18, 25)   128-wide tiles 34: they read
+//   tile  M=77 K=N=2880                 9.0   (2.7, 7)   latency: ~6 us of first
+//         copies, cluster sum and store around 11 k-blocks a block
+//         M=K=512 N=4096                6.7   (1.3, 4.4)
+//   split M=512 K=7168 N=2x2048 gated   27    (18, 25)   128-wide tiles 34: they read
 //         1.5x the shared memory that their MMAs take
 //   pair  M=8192 K=7168 N=2x2048 gated  330-390 (288 at the burst rate; cuBLAS
-//         369-372 in the same runs): the power cap; M=1024 K=N=4096 32 (21, 25)
+//         369-372 in the same runs): the power cap; M=1024 K=N=4096 29 (21, 25)
+//         M=2500 K=2048 N=2041          42    (12, 220)  rows that are not aligned
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -106,8 +108,7 @@ __device__ __forceinline__ float load_res(const Args& g, long long row, int col)
                      : __bfloat162float(static_cast<const __nv_bfloat16*>(g.residual)[o]);
 }
 
-__device__ __forceinline__ void store_one(const Args& g, long long row, int col, float v) {
-    if (g.residual) v += load_res(g, row, col);
+__device__ __forceinline__ void store_out(const Args& g, long long row, int col, float v) {
     const long long o = row * g.ldo + col;
     if (g.out_f32) static_cast<float*>(g.out)[o] = v;
     else static_cast<__nv_bfloat16*>(g.out)[o] = __float2bfloat16_rn(v);
@@ -118,33 +119,52 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&b);
 }
 
-// 32-byte accesses: one whole sector per lane
-__device__ __forceinline__ void ld32(const void* p, uint32_t (&r)[8]) {
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7])
-                 : "l"(p)
-                 : "memory");
+// 32 bytes of a row: a whole sector per access where rows are aligned to it, else
+// two of 16 (vec: 32 or 16).
+__device__ __forceinline__ void ld32(const void* p, uint32_t (&r)[8], int vec) {
+    if (vec == 32) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                       "=r"(r[6]), "=r"(r[7])
+                     : "l"(p)
+                     : "memory");
+    } else {
+        const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
+        r[0] = a.x;
+        r[1] = a.y;
+        r[2] = a.z;
+        r[3] = a.w;
+        r[4] = b.x;
+        r[5] = b.y;
+        r[6] = b.z;
+        r[7] = b.w;
+    }
 }
-__device__ __forceinline__ void st32(void* p, const uint32_t (&r)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+__device__ __forceinline__ void st32(void* p, const uint32_t (&r)[8], int vec) {
+    if (vec == 32) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p),
+                     "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                     "r"(r[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = make_uint4(r[0], r[1], r[2], r[3]);
+        static_cast<uint4*>(p)[1] = make_uint4(r[4], r[5], r[6], r[7]);
+    }
 }
 
-// 16 consecutive columns of one row, from column col (a multiple of 16), whole
-// 32-byte sectors at a time; `res` holds the residual's (see res16).
+// 16 consecutive columns of one row, from column col (a multiple of 16); the
+// arrays hold the residual's (see res16).
 __device__ __forceinline__ bool wide16(const Args& g, int col) {
-    return g.vec == 32 && col + 16 <= g.N;
+    return g.vec >= 16 && col + 16 <= g.N;
 }
 __device__ __forceinline__ void res16(const Args& g, long long row, int col, uint32_t (&a)[8],
                                       uint32_t (&b)[8]) {
     if (g.out_f32) {
         const float* p = static_cast<const float*>(g.residual) + row * g.ldr + col;
-        ld32(p, a);
-        ld32(p + 8, b);
+        ld32(p, a, g.vec);
+        ld32(p + 8, b, g.vec);
     } else {
-        ld32(static_cast<const __nv_bfloat16*>(g.residual) + row * g.ldr + col, a);
+        ld32(static_cast<const __nv_bfloat16*>(g.residual) + row * g.ldr + col, a, g.vec);
     }
 }
 __device__ __forceinline__ void add_res16(const Args& g, float (&v)[16], const uint32_t (&a)[8],
@@ -170,46 +190,112 @@ __device__ __forceinline__ void store16(const Args& g, long long row, int col, c
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(v[8 * h + i]);
-            st32(static_cast<float*>(g.out) + row * g.ldo + col + 8 * h, r);
+            st32(static_cast<float*>(g.out) + row * g.ldo + col + 8 * h, r, g.vec);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) r[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-        st32(static_cast<__nv_bfloat16*>(g.out) + row * g.ldo + col, r);
+        st32(static_cast<__nv_bfloat16*>(g.out) + row * g.ldo + col, r, g.vec);
     }
 }
 
-// Four consecutive columns (a multiple of 4).
+// Four consecutive columns (a multiple of 4): the residual's, and the store.
+__device__ __forceinline__ float4 res4(const Args& g, long long row, int col) {
+    const long long o = row * g.ldr + col;
+    if (g.vec < 16 || col + 4 > g.N) {
+        float a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = col + i < g.N ? load_res(g, row, col + i) : 0.0f;
+        return make_float4(a[0], a[1], a[2], a[3]);
+    }
+    if (g.out_f32) return *reinterpret_cast<const float4*>(static_cast<const float*>(g.residual) + o);
+    const uint2 r =
+        *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(g.residual) + o);
+    return make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
+}
 __device__ __forceinline__ void store4(const Args& g, long long row, int col, float4 v) {
+    const long long o = row * g.ldo + col;
     if (g.vec < 16 || col + 4 > g.N) {
         const float a[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (col + i < g.N) store_one(g, row, col + i, a[i]);
-        return;
-    }
-    if (g.out_f32) {
-        if (g.residual) {
-            const float4 r = *reinterpret_cast<const float4*>(
-                static_cast<const float*>(g.residual) + row * g.ldr + col);
-            v.x += r.x;
-            v.y += r.y;
-            v.z += r.z;
-            v.w += r.w;
+        for (int i = 0; i < 4; ++i) {
+            if (col + i >= g.N) break;
+            store_out(g, row, col + i, a[i]);
         }
-        *reinterpret_cast<float4*>(static_cast<float*>(g.out) + row * g.ldo + col) = v;
+    } else if (g.out_f32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(g.out) + o) = v;
     } else {
-        if (g.residual) {
-            const uint2 r = *reinterpret_cast<const uint2*>(
-                static_cast<const __nv_bfloat16*>(g.residual) + row * g.ldr + col);
-            v.x += bf16_lo(r.x);
-            v.y += bf16_hi(r.x);
-            v.z += bf16_lo(r.y);
-            v.w += bf16_hi(r.y);
-        }
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.out) + row * g.ldo + col) =
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(g.out) + o) =
             make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
     }
+}
+
+// The same of a warp's 32 rows where they are not aligned or end within: through
+// a buffer of the warp, so that 16 lanes write 16 consecutive columns (with a
+// row per lane every store touched 32 sectors: 78 us instead of 13 at M = 5000,
+// K = 512, N = 1000).  row0 is lane 0's; all lanes take part.
+constexpr int kBufFloats = 32 * 17;
+template <class T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <class T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+// every second row from p (and q, the residual's) on, n of them
+template <class T>
+__device__ __forceinline__ void rows16(T* p, long long ldo, const T* q, long long ldr,
+                                       const float* buf, int n) {
+    float t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        t[i] = buf[2 * 17 * i];
+        if (q && i < n) t[i] += to_f32(q[2 * i * ldr]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < n) p[2 * i * ldo] = from_f32<T>(t[i]);
+}
+__device__ __forceinline__ void some16(const Args& g, float* buf, long long row0, int col,
+                                       const float (&v)[16]) {
+    const int lane = threadIdx.x & 31, r = lane >> 4, c = lane & 15;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) buf[lane * 17 + j] = v[j];
+    __syncwarp();
+    const int rows = static_cast<int>(min(32ll, g.M - row0));
+    const int n = col + c < g.N ? (rows - r + 1) / 2 : 0;
+    const long long o = (row0 + r) * g.ldo + col + c, d = (row0 + r) * g.ldr + col + c;
+    if (g.out_f32)
+        rows16(static_cast<float*>(g.out) + o, g.ldo,
+               g.residual ? static_cast<const float*>(g.residual) + d : nullptr, g.ldr,
+               buf + r * 17 + c, n);
+    else
+        rows16(static_cast<__nv_bfloat16*>(g.out) + o, g.ldo,
+               g.residual ? static_cast<const __nv_bfloat16*>(g.residual) + d : nullptr, g.ldr,
+               buf + r * 17 + c, n);
+}
+
+// What follows the sums (bias included) of 16 consecutive columns, a row per lane,
+// and their store.  All lanes take part.
+__device__ __forceinline__ void finish16(const Args& g, float* buf, long long row0, int col,
+                                         float (&v)[16], const float (&u)[16]) {
+    activate(v, g.act);
+    if (g.gated) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] *= u[j];
+    }
+    if (!wide16(g, col)) {
+        some16(g, buf, row0, col, v);
+        return;
+    }
+    const long long row = row0 + (threadIdx.x & 31);
+    if (row >= g.M) return;
+    if (g.residual) {
+        uint32_t qa[8], qb[8];
+        res16(g, row, col, qa, qb);
+        add_res16(g, v, qa, qb);
+    }
+    store16(g, row, col, v);
 }
 
 // ------------------------------------------------------------- clusters
@@ -223,10 +309,14 @@ __device__ __forceinline__ float ld_cluster(uint32_t a) {
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
     return v;
 }
-__device__ __forceinline__ void st_cluster4(uint32_t a, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y),
-                 "f"(v.z), "f"(v.w)
-                 : "memory");
+// Bulk copy into another block's shared memory, completing on its mbarrier (both
+// shared::cluster addresses; 16-byte aligned, whole 16 bytes).
+__device__ __forceinline__ void bulk_to_cluster(uint32_t dst, const void* src, uint32_t bytes,
+                                                uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+        ::"r"(dst), "r"(smem_u32(src)), "r"(bytes), "r"(bar)
+        : "memory");
 }
 __device__ __forceinline__ float4 ld_cluster4(uint32_t a) {
     float4 v;
@@ -394,7 +484,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         float v[1] = {z + load_bias(g, col)};
         activate(v, g.act);
         if (g.gated) v[0] *= up + load_bias(g, g.N + col);
-        store_one(g, m, col, v[0]);
+        if (g.residual) v[0] += load_res(g, m, col);
+        store_out(g, m, col, v[0]);
     }
     if (csize > 1) cluster_sync();     // peers may still be reading this block's sums
 }
@@ -425,7 +516,76 @@ struct TileCtl {
     uint32_t tmem;
     int abort;
     uint32_t issued;
+    alignas(16) float bias[128];       // of the tile's accumulator columns
 };
+
+// The rows of a tile that this block of a cluster of CS finishes: four columns
+// a thread, a row's threads side by side, each adding the blocks' sums in rank
+// order.  All of an item's loads are in flight together, and those of a few
+// items (one after the other an item took 1 us).
+template <int BN, int CS>
+__device__ __forceinline__ void finish_rows(const Args& g, const float* bias, const float* sacc,
+                                            int m0, int n0, int rank) {
+    constexpr int LD = BN + 4, U = 8 / CS;
+    const int per = g.gated ? BN / 2 : BN, lq = 31 - __clz(per / 4);
+    const int rows = min(kTileM, g.M - m0);
+    const int r0 = rows * rank / CS, items = (rows * (rank + 1) / CS - r0) << lq;
+    uint32_t from[CS];
+#pragma unroll
+    for (int q = 0; q < CS; ++q) from[q] = cluster_addr(smem_u32(sacc), q);
+    for (int f0 = threadIdx.x; f0 < items; f0 += U * kTileThreads) {
+        int r[U], c[U];
+        bool in[U];
+        float4 v[U][CS], w[U][CS], res[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int f = f0 + u * kTileThreads;
+            r[u] = r0 + (f >> lq);
+            c[u] = (f & ((1 << lq) - 1)) * 4;
+            in[u] = f < items && n0 + c[u] < g.N;
+            res[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (!in[u]) continue;
+            const uint32_t o = (r[u] * LD + c[u]) * 4;
+#pragma unroll
+            for (int q = 0; q < CS; ++q) {
+                v[u][q] = ld_cluster4(from[q] + o);
+                if (g.gated) w[u][q] = ld_cluster4(from[q] + o + BN / 2 * 4);
+            }
+            if (g.residual) res[u] = res4(g, m0 + r[u], n0 + c[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!in[u]) continue;
+            float z[4], up[4];
+            const float4 b = *reinterpret_cast<const float4*>(bias + c[u]);
+            float4 t = v[u][0];
+#pragma unroll
+            for (int q = 1; q < CS; ++q)
+                t = make_float4(t.x + v[u][q].x, t.y + v[u][q].y, t.z + v[u][q].z, t.w + v[u][q].w);
+            z[0] = t.x + b.x;
+            z[1] = t.y + b.y;
+            z[2] = t.z + b.z;
+            z[3] = t.w + b.w;
+            activate(z, g.act);
+            if (g.gated) {
+                const float4 d = *reinterpret_cast<const float4*>(bias + BN / 2 + c[u]);
+                t = w[u][0];
+#pragma unroll
+                for (int q = 1; q < CS; ++q)
+                    t = make_float4(t.x + w[u][q].x, t.y + w[u][q].y, t.z + w[u][q].z,
+                                    t.w + w[u][q].w);
+                up[0] = t.x + d.x;
+                up[1] = t.y + d.y;
+                up[2] = t.z + d.z;
+                up[3] = t.w + d.w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[i] *= up[i];
+            }
+            store4(g, m0 + r[u], n0 + c[u],
+                   make_float4(z[0] + res[u].x, z[1] + res[u].y, z[2] + res[u].z, z[3] + res[u].w));
+        }
+    }
+}
 
 template <int BN>
 __global__ void __launch_bounds__(kTileThreads, 2)
@@ -505,6 +665,9 @@ __global__ void __launch_bounds__(kTileThreads, 2)
             umma_commit(&ctl.empty[st]);
         }
         umma_commit(&ctl.done);
+    } else if (warp >= 4 && threadIdx.x - 128 < BN) {
+        const int i = threadIdx.x - 128, c = n0 + (g.gated && i >= BN / 2 ? i - BN / 2 : i);
+        ctl.bias[i] = c < g.N ? load_bias(g, g.gated && i >= BN / 2 ? g.N + c : c) : 0.0f;
     }
     __syncwarp();
     // the accumulator is whole (or the wait ran out): every thread, so that
@@ -520,80 +683,54 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     }
     __syncthreads();
 
+    const int q = warp & 3, half = warp >> 2;
+    const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    if (csize == 1) {
+        // out straight from the accumulator, a row per lane
+        float* buf = reinterpret_cast<float*>(base) + warp * kBufFloats;    // (of the ring)
+        const int span = per / 2;                      // this warp's output columns
+        for (int c = half * span; c < (half + 1) * span && n0 + c < g.N; c += 16) {
+            float v[16], u[16];
+            tmem_ld16(ta + c, v);
+            if (g.gated) tmem_ld16(ta + BN / 2 + c, u);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                v[i] += ctl.bias[c + i];
+                if (g.gated) u[i] += ctl.bias[BN / 2 + c + i];
+            }
+            finish16(g, buf, m0 + 32 * q, n0 + c, v, u);
+        }
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        if (warp == 2) tmem_dealloc(tmem, BN);
+        return;
+    }
     // accumulator -> shared memory, rows of BN + 4 floats (a lane per row: the 4
     // keep 16-byte stores of 8 lanes on different banks)
     constexpr int LD = BN + 4;
     float* sacc = reinterpret_cast<float*>(base);
     {
-        const int q = warp & 3, half = warp >> 2;
         float* row = sacc + (32 * q + lane) * LD + half * (BN / 2);
-        if (kb1 > kb0) {
 #pragma unroll
-            for (int c = 0; c < BN / 2; c += 16) {
-                float v[16];
-                tmem_ld16(tmem + (static_cast<uint32_t>(32 * q) << 16) + half * (BN / 2) + c, v);
+        for (int c = 0; c < BN / 2; c += 16) {
+            float v[16];
+            tmem_ld16(ta + half * (BN / 2) + c, v);
 #pragma unroll
-                for (int i = 0; i < 16; i += 4)
-                    *reinterpret_cast<float4*>(row + c + i) =
-                        make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-            }
-        } else {
-            for (int c = 0; c < BN / 2; c += 4)
-                *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < 16; i += 4)
+                *reinterpret_cast<float4*>(row + c + i) =
+                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
     }
     tc_fence_before();
-    if (csize > 1) cluster_sync();
-    else __syncthreads();
+    cluster_sync();
     tc_fence_after();
     if (warp == 2) tmem_dealloc(tmem, BN);
-
-    // out: four columns a thread, a row's threads side by side; the rows are
-    // dealt over the cluster's blocks, each adds the blocks' sums in rank order
-    const int quads = per / 4, rows = min(kTileM, g.M - m0);
-    const int r0 = rows * static_cast<int>(rank) / csize, r1 = rows * (static_cast<int>(rank) + 1) / csize;
-    const uint32_t s0 = smem_u32(sacc);
-    for (int f = threadIdx.x; f < (r1 - r0) * quads; f += kTileThreads) {
-        const int r = r0 + f / quads, c = f % quads * 4, col = n0 + c;
-        if (col >= g.N) continue;
-        float4 z, up = make_float4(0.f, 0.f, 0.f, 0.f);
-        const uint32_t off = (r * LD + c) * 4;
-        if (csize == 1) {
-            z = *reinterpret_cast<const float4*>(sacc + r * LD + c);
-            if (g.gated) up = *reinterpret_cast<const float4*>(sacc + r * LD + c + BN / 2);
-        } else {
-            z = up;
-            for (int q = 0; q < csize; ++q) {
-                const uint32_t a = cluster_addr(s0 + off, q);
-                const float4 v = ld_cluster4(a);
-                z.x += v.x;
-                z.y += v.y;
-                z.z += v.z;
-                z.w += v.w;
-                if (g.gated) {
-                    const float4 u = ld_cluster4(a + BN / 2 * 4);
-                    up.x += u.x;
-                    up.y += u.y;
-                    up.z += u.z;
-                    up.w += u.w;
-                }
-            }
-        }
-        float zz[4] = {z.x, z.y, z.z, z.w};
-        const float uu[4] = {up.x, up.y, up.z, up.w};
-        if (g.bias) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) zz[i] += load_bias(g, min(col + i, g.N - 1));
-        }
-        activate(zz, g.act);
-        if (g.gated) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                zz[i] *= uu[i] + (g.bias ? load_bias(g, g.N + min(col + i, g.N - 1)) : 0.0f);
-        }
-        store4(g, m0 + r, col, make_float4(zz[0], zz[1], zz[2], zz[3]));
-    }
-    if (csize > 1) cluster_sync();     // peers may still be reading this block's sums
+    // the rows are dealt over the cluster's blocks
+    if (csize == 2) finish_rows<BN, 2>(g, ctl.bias, sacc, m0, n0, rank);
+    else if (csize == 4) finish_rows<BN, 4>(g, ctl.bias, sacc, m0, n0, rank);
+    else finish_rows<BN, 8>(g, ctl.bias, sacc, m0, n0, rank);
+    cluster_sync();                    // peers may still be reading this block's sums
 }
 
 // ================================================================= pair
@@ -607,7 +744,8 @@ constexpr int kPairN = 256;
 constexpr int kPairStageBytes = (128 + kPairN / 2) * kRowBytes;   // per CTA: 128 token rows,
                                                                   // half of the weight rows
 constexpr int kPairStages = 6;
-constexpr int kPairSmemBytes = 1024 + kPairStages * kPairStageBytes;
+// behind the ring the epilogue warps' buffers for rows that are not aligned
+constexpr int kPairSmemBytes = 1024 + kPairStages * kPairStageBytes + 8 * kBufFloats * 4;
 
 struct PairCtl {
     uint64_t full[kPairStages];
@@ -631,6 +769,9 @@ __device__ __forceinline__ void pair_tile(int t, int tm, int tn, int& m, int& n)
     n = r / h;
 }
 
+// WIDE: rows aligned to 16 bytes and N a multiple of 16.  The other form carries
+// the code for what is not, which costs its epilogue a tenth (instruction fetch).
+template <bool WIDE>
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_pair_kernel(const __grid_constant__ Maps maps, const Args g) {
     extern __shared__ uint8_t dsmem_raw[];
@@ -754,6 +895,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     } else if (warp >= kEpiWarp0) {
         const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
         const int et = threadIdx.x - kEpiWarp0 * 32;
+        float* buf = reinterpret_cast<float*>(base + S * STAGE) + (warp - kEpiWarp0) * kBufFloats;
         uint32_t i = 0;
         for (int t = p0; t < tiles; t += P, ++i) {
             const int acc = i & 1;
@@ -774,7 +916,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int cb = half * span, ce = min((half + 1) * span, g.N - n0);
             uint32_t qa[8], qb[8];
             const bool res = g.residual != nullptr && row < g.M;
-            if (cb < ce && res && wide16(g, n0 + cb)) res16(g, row, n0 + cb, qa, qb);
+            if (cb < ce && res && (WIDE || wide16(g, n0 + cb))) res16(g, row, n0 + cb, qa, qb);
             // (after a fault the waits return at once and the loop runs on, so
             // that all epilogue warps meet at the same barriers)
             if (!mbar_wait(&ctl.tfull[acc], (i >> 1) & 1u, &ctl.abort)) raise();
@@ -808,7 +950,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         u[4 * j + 3] = __uint_as_float(r1[4 * j + 3]) + b.w;
                     }
                 }
-                const bool wide = wide16(g, n0 + c);
+                const bool wide = WIDE || wide16(g, n0 + c);
                 if (res && wide) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[j] = 0.0f;
@@ -817,24 +959,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (c + 16 < ce) {
                     tmem_ld16_async(ta + c + 16, r0);
                     if (g.gated) tmem_ld16_async(ta + BN / 2 + c + 16, r1);
-                    if (res && wide16(g, n0 + c + 16)) res16(g, row, n0 + c + 16, qa, qb);
+                    if (res && (WIDE || wide16(g, n0 + c + 16))) res16(g, row, n0 + c + 16, qa, qb);
                 }
                 activate(v, g.act);
                 if (g.gated) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) v[j] *= u[j];
                 }
-                if (row >= g.M) continue;
-                if (wide) {
+                if (!wide) {
+                    if constexpr (!WIDE) some16(g, buf, row - lane, n0 + c, v);
+                } else if (row < g.M) {
                     if (res) {
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] += w[j];
                     }
                     store16(g, row, n0 + c, v);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (n0 + c + j < g.N) store_one(g, row, n0 + c + j, v[j]);
                 }
             }
             tc_fence_before();
@@ -866,13 +1005,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // ================================================================= split
 // The pair kernel's 256 x 256 tile, one per cluster of two pairs that split K:
 // for long products with too few such tiles for all pairs.  The CTAs of the same
-// 128 rows then finish half of the columns each: either pushes its sums of the
-// other's half into that one's ring, which has run dry.  The exchange costs 5 us
-// (16.5 us in all at M = 512, K = 2048, N = 4096, where the products take 5).
+// 128 rows then finish half of the columns each: either copies its sums of the
+// other's half into that one's ring, which has run dry (as bulk copies; lane by
+// lane, with 16-byte remote stores, it took 3 us).
 constexpr int kSplitW = kPairN / 2;            // accumulator columns of a share
 constexpr int kSplitLD = kSplitW + 4;          // the 4 keep 16-byte stores of 8 lanes on
                                                // different banks
-static_assert(128 * kSplitLD * 4 <= kPairStages * kPairStageBytes, "a share fits into the ring");
+constexpr int kShareBytes = 128 * kSplitLD * 4;
+static_assert(2 * kShareBytes <= kPairStages * kPairStageBytes, "two shares fit into the ring");
 __device__ __forceinline__ void umma_commit_pair_of(uint64_t* bar, int pair) {
     const uint16_t mask = static_cast<uint16_t>(0x3 << (2 * pair));
     asm volatile(
@@ -882,33 +1022,11 @@ __device__ __forceinline__ void umma_commit_pair_of(uint64_t* bar, int pair) {
         : "memory");
 }
 
-// 16 finished columns of a row, without the pair kernel's overlap.
-__device__ __forceinline__ void finish16(const Args& g, long long row, int col, float (&v)[16],
-                                         const float (&u)[16]) {
-    activate(v, g.act);
-    if (g.gated) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] *= u[j];
-    }
-    if (row >= g.M) return;
-    if (wide16(g, col)) {
-        if (g.residual) {
-            uint32_t qa[8], qb[8];
-            res16(g, row, col, qa, qb);
-            add_res16(g, v, qa, qb);
-        }
-        store16(g, row, col, v);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (col + j < g.N) store_one(g, row, col + j, v[j]);
-    }
-}
-
 __global__ void __launch_bounds__(kPairThreads, 1)
     linear_split_kernel(const __grid_constant__ Maps maps, const Args g) {
     extern __shared__ uint8_t dsmem_raw[];
     __shared__ PairCtl ctl;
+    __shared__ uint64_t arrived;              // the other pair's share
     uint8_t* base = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(dsmem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     constexpr int BN = kPairN, STAGE = kPairStageBytes, S = kPairStages;
@@ -922,7 +1040,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         mbar_init(&ctl.tfull[0], 1);
         mbar_init(&ctl.drain, 1);
+        mbar_init(&arrived, 1);
         fence_mbar_init();
+        mbar_arrive_expect_tx(&arrived, kShareBytes);
         ctl.abort = 0;
         ctl.prod_pos = ctl.mma_pos = ctl.mma_issued = 0;
         tma_prefetch_desc(&maps.x);
@@ -1033,29 +1153,42 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         __syncthreads();
     }
-    cluster_sync();          // every ring is idle
+    // this CTA's ring is idle
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
     // accumulator column of column l of share j: a gated share's first half are
     // gate columns, its second half their up columns
     auto column = [&](int j, int l) {
         return g.gated ? (l < W / 2 ? j * (W / 2) + l : BN / 2 + j * (W / 2) + l - W / 2) : j * W + l;
     };
     const int srow = 32 * q + lane;
-    float* const share = reinterpret_cast<float*>(base) + srow * LD;     // [128 rows][LD]
+    const float* const share = reinterpret_cast<float*>(base) + srow * LD;   // what arrives
+    float* const sent = reinterpret_cast<float*>(base + kShareBytes) + srow * LD;
     if (warp >= kEpiWarp0) {
-        const uint32_t dst = cluster_addr(smem_u32(share + half * (W / 2)), rank ^ 2);
 #pragma unroll
         for (int c = 0; c < W / 2; c += 16) {
+            const int l = half * (W / 2) + c;
             float v[16];
-            tmem_ld16(ta + column(pair ^ 1, half * (W / 2) + c), v);
+            tmem_ld16(ta + column(pair ^ 1, l), v);
 #pragma unroll
             for (int i = 0; i < 16; i += 4)
-                st_cluster4(dst + (c + i) * 4, make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+                *reinterpret_cast<float4*>(sent + l + i) =
+                    make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
+        fence_proxy_async_smem();
     }
-    cluster_sync();          // both shares have arrived
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");      // all rings are
+    if (warp >= kEpiWarp0) {
+        // 32 rows are whole once both their warps are here
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+        if (half == 0 && lane == 0)
+            bulk_to_cluster(cluster_addr(smem_u32(share), rank ^ 2), sent, kShareBytes / 4,
+                            cluster_addr(smem_u32(&arrived), rank ^ 2));
+        if (!mbar_wait(&arrived, 0, nullptr)) raise();
+    }
     if (warp >= kEpiWarp0) {
         const int outs = g.gated ? W / 2 : W;              // output columns of a share
-        const long long row = static_cast<long long>(m) * 256 + side * 128 + srow;
+        const long long row0 = static_cast<long long>(m) * 256 + side * 128 + 32 * q;
+        float* buf = reinterpret_cast<float*>(base + S * STAGE) + (warp - kEpiWarp0) * kBufFloats;
         auto total = [&](int l, float (&v)[16]) {
             const int at = column(pair, l);
             tmem_ld16(ta + at, v);
@@ -1076,7 +1209,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             float v[16], u[16];
             total(l, v);
             if (g.gated) total(l + W / 2, u);
-            finish16(g, row, col, v, u);
+            finish16(g, buf, row0, col, v, u);
         }
     }
     tc_fence_before();
@@ -1180,10 +1313,15 @@ cudaError_t launch_tile(const Args& g, int sms, cudaStream_t s) {
     const long long tiles = (static_cast<long long>(g.M) + kTileM - 1) / kTileM *
                             ((static_cast<long long>(g.N) + per - 1) / per);
     const int KB = (g.K + kBK - 1) / kBK;
-    // blocks of a cluster split K while all find room on the SMs, two each, and
-    // each keeps at least 4 k-blocks
+    // blocks of a cluster split K while all find room on the SMs and each keeps
+    // at least 4 k-blocks; 6 where it shares its SM, and 12 where it would not
+    // without the first split (us, more / fewer blocks: M = K = 512, N = 4096 10 /
+    // 6.7; M = 512, K = 1024, N = 4096 11 / 9.2; M = 256, K = 2048, N = 768 7.9 /
+    // 7.1; but M = 64, K = N = 2880, 180 blocks of 11 k-blocks, 8.6 / 10.6)
     int csize = 1;
-    while (csize < 8 && tiles * csize * 2 <= 2 * sms && KB >= csize * 8) csize *= 2;
+    while (csize < 8 && tiles * csize * 2 <= 2 * sms &&
+           KB >= (tiles * csize * 2 <= sms ? csize * 8 : csize == 1 ? 24 : csize * 12))
+        csize *= 2;
     Maps maps;
     memset(&maps, 0, sizeof(maps));
     if (!make_map(&maps.x, g.x, g.K, g.M, g.ldx, kTileM) ||
@@ -1193,10 +1331,11 @@ cudaError_t launch_tile(const Args& g, int sms, cudaStream_t s) {
                   s, maps, g, csize);
 }
 
+template <bool WIDE>
 cudaError_t launch_pair(const Args& g, int sms, cudaStream_t s) {
     static std::once_flag once[kMaxDevices];
     static cudaError_t err[kMaxDevices];
-    cudaError_t e = opt_in(linear_pair_kernel, kPairSmemBytes, once, err);
+    cudaError_t e = opt_in(linear_pair_kernel<WIDE>, kPairSmemBytes, once, err);
     if (e != cudaSuccess) return e;
     const int per = g.gated ? kPairN / 2 : kPairN;
     const long long tiles = (static_cast<long long>(g.M) + 255) / 256 *
@@ -1208,7 +1347,7 @@ cudaError_t launch_pair(const Args& g, int sms, cudaStream_t s) {
         !make_map(&maps.w, g.w, g.K, g.gated ? 2LL * g.N : g.N, g.ldw, kPairN / 2))
         return cudaErrorInvalidValue;
     const long long pairs = tiles < sms / 2 ? tiles : sms / 2;
-    return launch(linear_pair_kernel, pairs * 2, kPairThreads, kPairSmemBytes, 2, s, maps,
+    return launch(linear_pair_kernel<WIDE>, pairs * 2, kPairThreads, kPairSmemBytes, 2, s, maps,
                   g);
 }
 
@@ -1288,13 +1427,15 @@ cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s) {
     const int per = p.gated ? 128 : 256;
     const long long t256 = (static_cast<long long>(p.M) + 255) / 256 *
                            ((static_cast<long long>(p.N) + per - 1) / per);
-    if (p.M > 128 && t256 * 4 >= sms) return launch_pair(g, sms, s);
+    if (p.M > 128 && t256 * 4 >= sms)
+        return g.vec && p.N % 16 == 0 ? launch_pair<true>(g, sms, s) : launch_pair<false>(g, sms, s);
     // Fewer such tiles: two pairs to each, where all are resident and K is long
     // enough to pay for their exchange (us, split / 128-wide): M = 512, K = 7168,
-    // N = 2 x 2048 (32) 28 / 34; K = N = 4096 23 / 27; M = 256, K = N = 7168 (28)
-    // 29 / 36; M = 512, K = 2048, N = 4096 16.5 / 16.8; with 16 tiles, M = 256,
-    // K = N = 4096 19 / 17.
-    if (p.M > 128 && t256 > 16 && p.K >= 4096 && t256 <= split_clusters())
+    // N = 2 x 2048 (32) 27 / 34; K = N = 4096 20 / 27; K = 2048 14 / 16, K = 1024 11
+    // / 9.2; with the last 256 rows half empty M = 300, K = N = 2880 (24) 15 / 13.6,
+    // K = 4096 18 / 18; with 16 tiles, M = 256, K = N = 4096 19 / 17.
+    const bool waste = (p.M - 1) % 256 < 128;
+    if (p.M > 128 && t256 > 16 && p.K >= (waste ? 4096 : 2048) && t256 < split_clusters())
         return launch_split(g, t256, s);
     const long long t128 = (static_cast<long long>(p.M) + 127) / 128 *
                            ((static_cast<long long>(p.N) + per / 2 - 1) / (per / 2));

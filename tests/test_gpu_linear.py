@@ -80,7 +80,8 @@ def _run(moe, c, act, gated, out_dtype, **kw):
 # every kernel's edges: 16 | 17 tokens, 128- and 256-row tiles, ragged N and K, one k-block
 SIZES = [(1, 8, 4096), (1, 1, 8), (3, 5, 72), (8, 256, 512), (9, 100, 200), (16, 257, 1024),
          (16, 4100, 64), (17, 64, 64), (17, 1, 8), (33, 100, 200), (100, 333, 520),
-         (128, 64, 2048), (129, 130, 136), (300, 8, 4096), (513, 1000, 72)]
+         (128, 64, 2048), (129, 130, 136), (300, 8, 4096), (513, 1000, 72),
+         (520, 1001, 200), (260, 1003, 1024), (140, 301, 2048)]
 
 
 @pytest.mark.parametrize("gated", [False, True])
@@ -95,7 +96,7 @@ def test_sizes(M, N, K, gated):
 
 # enough 256-row tiles for the CTA pairs (74 of them on 148 SMs), ragged in every direction
 PAIR_SIZES = [(5000, 1000, 192), (2500, 2040, 520), (20000, 250, 72), (4864, 1024, 64),
-              (1024, 5000, 136)]
+              (1024, 5000, 136), (2500, 2041, 136), (4700, 1100, 64)]
 
 
 @pytest.mark.parametrize("gated", [False, True])
