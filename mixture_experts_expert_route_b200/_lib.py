@@ -445,6 +445,22 @@ def _rows(t, name, rows, cols, dtype, idx):
     return rs if rows > 1 else (cols + 7) // 8 * 8
 
 
+def _bind(*args):
+    """The compiled call of moe_linear (csrc/binding.cpp), from the first call on; without it
+    the calls go through ctypes, and cost the host twice as much."""
+    global _fast
+    try:
+        from . import _binding
+        _binding.init(ctypes.cast(lib().moe_linear, ctypes.c_void_p).value)
+        _fast = _binding.linear
+    except ModuleNotFoundError:
+        _fast = lambda *args: NotImplemented  # noqa: E731
+    return _fast(*args)
+
+
+_fast = _bind
+
+
 def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=None, out=None,
            out_dtype=None, status=None, stream=None):
     """act(x w^T + bias) + residual, or with ``gated`` act(z[:, :N]) * z[:, N:] + residual.
@@ -452,6 +468,11 @@ def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=N
     x bf16 [M, K] and w bf16 [N, K] (gated: [2N, K], gate rows then up rows), rows any multiple
     of 8 elements apart; bias bf16 or f32 [rows of w]; residual and out of ``out_dtype`` (bf16,
     the default, or f32).  ``out`` may be the residual."""
+    if stream is None and status is None:
+        y = _fast(x, w, bias, act, gated, residual, out, out_dtype)
+        if y is not NotImplemented:
+            return y
+    # another device or stream, a status word, or an argument to refuse
     idx = x.get_device()
     if idx < 0:
         raise ValueError("expected a CUDA tensor")

@@ -5,7 +5,7 @@
 --debug-checks builds libmoe_b200_debug.so instead: the same library compiled
 with MOE_DEBUG_CHECKS, whose kernels validate the permutation they are handed
 and report a bad entry in the status word (MOE_ERR_DEVICE).  The binding
-loads it when the environment sets MOE_B200_DEBUG_CHECKS=1.
+loads it when the environment sets MOE_B200_DEBUG_CHECKS=1.  Both build _binding.so too.
 """
 from __future__ import annotations
 
@@ -13,6 +13,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -24,6 +26,7 @@ SOURCES = ["route_permute.cu", "elementwise.cu", "grouped_gemm.cu", "moe_api.cu"
 HOST_SOURCES = ["host_ffn.cpp"]
 HEADERS = ["common.cuh", "kernels.h", "topk.cuh"]
 LIB = os.path.join(HERE, "libmoe_b200.so")
+BINDING = os.path.join(HERE, "_binding.so")    # a Python extension: moe.linear's call
 LIB_DEBUG = os.path.join(HERE, "libmoe_b200_debug.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -48,8 +51,37 @@ def _stale(lib: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_binding(force: bool = False) -> None:
+    """csrc/binding.cpp against the installed torch (host code only).  The package works
+    without it, with slower calls, so a machine without Python's headers only gets a warning."""
+    src = os.path.join(CSRC, "binding.cpp")
+    deps = (src, os.path.join(ROOT, "include", "moe.h"))
+    if not force and os.path.exists(BINDING) and \
+            all(os.path.getmtime(BINDING) >= os.path.getmtime(d) for d in deps):
+        return
+    import torch
+    pkg = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    includes = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"],
+                os.path.join(pkg, "include"),
+                os.path.join(pkg, "include", "torch", "csrc", "api", "include"),
+                os.path.join(cuda, "include")]
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    try:
+        subprocess.check_call(["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+                               "-fvisibility=hidden",
+                               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                               *(a for d in includes for a in ("-isystem", d)), src, "-o", tmp,
+                               "-L" + os.path.join(pkg, "lib"), "-lc10", "-lc10_cuda",
+                               "-ltorch_cpu", "-ltorch_python"])
+        os.replace(tmp, BINDING)
+    except subprocess.CalledProcessError as e:
+        warnings.warn(f"{BINDING} was not built ({e}): calls go through ctypes")
+
+
 def build(force: bool = False, ptxas_verbose: bool = False, debug: bool = False) -> str:
     lib = lib_path(debug)
+    build_binding(force and not debug)
     if not force and not _stale(lib):
         return lib
     objdir = os.path.join(ROOT, "_build", "debug" if debug else "release")
