@@ -1427,7 +1427,11 @@ cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s) {
     const int per = p.gated ? 128 : 256;
     const long long t256 = (static_cast<long long>(p.M) + 255) / 256 *
                            ((static_cast<long long>(p.N) + per - 1) / per);
-    if (p.M > 128 && t256 * 4 >= sms)
+    // With few k-blocks and rows that are not aligned the epilogue counts, which
+    // twice the warps of the 128-wide tiles hide better (us, pair / 128-wide: M =
+    // 554, K = 128, N = 6602 38 / 15; M = 5000, K = 512, N = 1001 40 / 29; M = 4096,
+    // K = 1024, N = 2047 36 / 33; M = 3000, K = 2000, N = 2 x 3001 62 / 91).
+    if (p.M > 128 && t256 * 4 >= sms && (g.vec || p.K > 1024))
         return g.vec && p.N % 16 == 0 ? launch_pair<true>(g, sms, s) : launch_pair<false>(g, sms, s);
     // Fewer such tiles: two pairs to each, where all are resident and K is long
     // enough to pay for their exchange (us, split / 128-wide): M = 512, K = 7168,
