@@ -39,14 +39,14 @@
 //
 // Measured on one B200 (us; floor = the active experts' bytes at the copy's 6.53
 // TB/s; then moe_forward, whose chain of kernels costs ~28 us before the stream):
-//   bf16 E=128 H=2048 I=768 top-8     T = 1: 29-31 (11.6; 42)    T = 8: 86 (74; 99)
-//   bf16 E=8 H=4096 I=14336 top-2     T = 1: 117 (108; 123)      T = 8: 378 (371; 354)
-//   bf16 E=64 H=7168 I=2048 top-8     T = 1: 118 (108; 124)      T = 8: 566 (566; 528)
-//   e4m3 E=32 H=I=2880 top-4          T = 1: 35 (15; 49)         T = 8: 104 (79; 111)
-// Where T = 1's 30 us go (the first of them): 4 us routing and tables in every
-// CTA, 1.3 to the first tile, 8 of gate/up stream, 2.5 to the first barrier's
-// end under the down tiles' prefetch, 5 of h and down products, 1.3 for the
-// second barrier, 2.5 of final sums, 2.5 between launches.
+//   bf16 E=128 H=2048 I=768 top-8     T = 1: 27-29 (11.6; 42)    T = 8: 84 (72; 98)
+//   bf16 E=8 H=4096 I=14336 top-2     T = 1: 116 (108; 124)      T = 8: 414 (398; 386)
+//   bf16 E=64 H=7168 I=2048 top-8     T = 1: 117 (108; 124)      T = 8: 612 (554; 539)
+//   e4m3 E=32 H=I=2880 top-4          T = 1: 32-34 (15; 53)      T = 8: 104 (81; 113)
+// Where T = 1's 27.5 us go (the first of them): 3.2 us routing and tables in
+// every CTA, 1.7 to the first tile, 7.4 of gate/up stream (9.6 in the last CTA),
+// 1.7 for the first barrier under the down tiles' prefetch, 4.6 of h and down
+// products, 1.2 for the second barrier, 2.3 of final sums, 2.5 between launches.
 //
 // All sums are in a fixed order: results do not depend on timing.
 #include <cstdint>
