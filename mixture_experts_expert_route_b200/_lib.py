@@ -382,12 +382,41 @@ def decode_workspace(dtype: int, T: int, k: int, E: int, H: int, I: int, device,
     return ws
 
 
+class _Calls:
+    """The compiled calls of moe_linear and moe_decode_forward (csrc/binding.cpp), bound to the
+    library by the first of them; without the extension every call goes through ctypes, and
+    costs the host twice as much."""
+
+    def __init__(self):
+        self.linear = lambda *args: self._bind().linear(*args)
+        self.decode = lambda *args: self._bind().decode(*args)
+
+    def _bind(self):
+        try:
+            from . import _binding as b
+            b.init(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in
+                     ("moe_linear", "moe_decode_forward", "moe_packed_weights_size")))
+            self.linear, self.decode = b.linear, b.decode
+        except ModuleNotFoundError:
+            self.linear = self.decode = lambda *args: NotImplemented
+        return self
+
+
+_calls = _Calls()
+
+
 def decode_forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int,
                    residual=None, out=None, ids=None, w=None, status=None, ws=None,
                    stream=None):
     """The whole layer for T <= 16 tokens (T * k <= 128) in one kernel:
     out = residual + sum_j w_j * FFN_{id_j}(x).  ``ws`` comes from decode_workspace
     and is reused from call to call (None: a new one for this call)."""
+    if stream is None and ws is not None:
+        y = _calls.decode(dtype, x, logits, packed, scales, E, I, k, residual, out, ids, w, status,
+                          ws)
+        if y is not NotImplemented:
+            return y
+    # another device or stream, no workspace, or an argument to refuse
     idx = x.get_device()
     if idx < 0:
         raise ValueError("expected a CUDA tensor")
@@ -445,22 +474,6 @@ def _rows(t, name, rows, cols, dtype, idx):
     return rs if rows > 1 else (cols + 7) // 8 * 8
 
 
-def _bind(*args):
-    """The compiled call of moe_linear (csrc/binding.cpp), from the first call on; without it
-    the calls go through ctypes, and cost the host twice as much."""
-    global _fast
-    try:
-        from . import _binding
-        _binding.init(ctypes.cast(lib().moe_linear, ctypes.c_void_p).value)
-        _fast = _binding.linear
-    except ModuleNotFoundError:
-        _fast = lambda *args: NotImplemented  # noqa: E731
-    return _fast(*args)
-
-
-_fast = _bind
-
-
 def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=None, out=None,
            out_dtype=None, status=None, stream=None):
     """act(x w^T + bias) + residual, or with ``gated`` act(z[:, :N]) * z[:, N:] + residual.
@@ -469,7 +482,7 @@ def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=N
     of 8 elements apart; bias bf16 or f32 [rows of w]; residual and out of ``out_dtype`` (bf16,
     the default, or f32).  ``out`` may be the residual."""
     if stream is None and status is None:
-        y = _fast(x, w, bias, act, gated, residual, out, out_dtype)
+        y = _calls.linear(x, w, bias, act, gated, residual, out, out_dtype)
         if y is not NotImplemented:
             return y
     # another device or stream, a status word, or an argument to refuse

@@ -201,6 +201,28 @@ def test_no_partial_sum_is_read_before_it_is_written(T, E, k, H, I, dtype):
             assert torch.equal(moe.decode_forward(*args, ws=poisoned), out)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+def test_compiled_call_and_python_form_agree(dtype, monkeypatch):
+    """Both forms of the call give the same bits and optional outputs."""
+    moe = lib()
+    from mixture_experts_expert_route_b200 import _binding, _lib
+    T, E, k, H, I = 5, 16, 3, 256, 192
+    layer = moe.MoELayer(*_weights(E, H, I), k, dtype=dtype)
+    x, logits, res = _inputs(T, H, E)
+    def call(**kw):
+        ids = torch.full((T, k), -1, dtype=torch.int32, device=DEV)
+        w = torch.zeros((T, k), device=DEV)
+        return layer.decode(x, logits, ids=ids, w=w, **kw), ids, w
+    first = [call(), call(residual=res)]
+    given = torch.empty_like(x)
+    assert layer.decode(x, logits, residual=res, out=given) is given
+    assert torch.equal(given, first[1][0]) and _lib._calls.decode is _binding.decode
+    monkeypatch.setattr(_lib._calls, "decode", lambda *a: NotImplemented)
+    for got, want in zip([call(), call(residual=res)], first):
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert layer.check() == 0
+
+
 def test_a_timeout_makes_the_workspaces_anew():
     """After MOE_ERR_TIMEOUT (here written by the host) decode calls do not use the old one."""
     moe = lib()

@@ -211,7 +211,6 @@ def test_compiled_call_and_python_form_agree(monkeypatch):
     """Both forms of the call give the same bits and types, and return a given output itself."""
     moe = lib()
     from mixture_experts_expert_route_b200 import _binding, _lib
-    assert _lib._fast in (_lib._bind, _binding.linear)
     cases = [(_make(M, N, 264, gated, bias, res, out, pad=pad), gated, out)
              for M, N, gated, bias, res, out, pad in (
                  (1, 40, False, None, False, BF, 0), (5, 33, True, BF, True, F32, 8),
@@ -220,11 +219,11 @@ def test_compiled_call_and_python_form_agree(monkeypatch):
     given = torch.empty((5, 80), dtype=F32, device=DEV)[:, 8:41]
     assert _run(moe, cases[1][0], "silu", True, None, out=given) is given
     assert torch.equal(given, first[1])
-    assert _lib._fast is _binding.linear
+    assert _lib._calls.linear is _binding.linear
     w = torch.nn.Parameter(cases[0][0]["w"].clone())        # a subclass that wants a gradient
     y = moe.linear(cases[0][0]["x"], w, act=moe.ACT_SILU)
     assert torch.equal(y, first[0]) and not y.requires_grad
-    monkeypatch.setattr(_lib, "_fast", lambda *a: NotImplemented)
+    monkeypatch.setattr(_lib._calls, "linear", lambda *a: NotImplemented)
     for (c, gated, out), y in zip(cases, first):
         z = _run(moe, c, "silu", gated, out)
         assert z.dtype == y.dtype and z.stride() == y.stride() and torch.equal(z, y)
