@@ -302,6 +302,21 @@ def combine(y_perm, inv_perm, T: int, k: int, H: int, out=None, stream=None):
     return out
 
 
+def _take(t, name, shape, dtype, idx):
+    """Address of an optional contiguous argument tensor of a layer entry point, checked."""
+    if t is None:
+        return None
+    if t.get_device() != idx:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{idx}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
 def forward_workspace_size(dtype, T, k, E, H, I, block_m=0) -> int:
     return lib().moe_forward_workspace_size(dtype, T, k, E, H, I, block_m)
 
@@ -313,9 +328,15 @@ def forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int, out=N
     each stage: entry, route+permute, FP8 x quantisation, gate/up, h quant, down,
     combine.  ``combine``: COMBINE_AUTO, COMBINE_DETERMINISTIC or COMBINE_FUSED.
     ``lora`` (a Lora) with ``adapter`` (CUDA int32 [T], -1 = none) applies
-    multi-LoRA adapters (bf16 layers)."""
+    multi-LoRA adapters (bf16 layers).  x, logits, out, ids and w are contiguous."""
+    idx = x.get_device()
+    if idx < 0:
+        raise ValueError("expected a CUDA tensor")
+    if x.dim() != 2:
+        raise ValueError("x: expected [T, H]")
     T, H = x.shape
-    out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device) if out is None else out
+    bf16, f32 = torch.bfloat16, torch.float32
+    out = torch.empty((T, H), dtype=bf16, device=x.device) if out is None else out
     n = forward_workspace_size(dtype, T, k, E, H, I, block_m)
     if ws is None:
         ws = torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
@@ -328,8 +349,10 @@ def forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int, out=N
                 e.record()
         ev_arr = (ctypes.c_void_p * 7)(*[e.cuda_event for e in events])
     largs = lora.args(adapter) if lora is not None else None
-    a = ForwardArgs(dtype, T, k, E, H, I, block_m, _ptr(x), _ptr(logits), _ptr(packed),
-                    _ptr(scales), _ptr(out), _ptr(ids), _ptr(w), _ptr(status), max_ctas,
+    a = ForwardArgs(dtype, T, k, E, H, I, block_m, _take(x, "x", (T, H), bf16, idx),
+                    _take(logits, "logits", (T, E), f32, idx), _ptr(packed), _ptr(scales),
+                    _take(out, "out", (T, H), bf16, idx), _take(ids, "ids", (T, k), torch.int32, idx),
+                    _take(w, "w", (T, k), f32, idx), _ptr(status), max_ctas,
                     ctypes.cast(ev_arr, ctypes.c_void_p) if ev_arr is not None else None,
                     7 if ev_arr is not None else 0, combine,
                     ctypes.pointer(largs) if largs is not None else None)
@@ -352,21 +375,6 @@ def _on_device(dev: torch.device, stream=None):
     if dev.index == torch.cuda.current_device():
         return contextlib.nullcontext()
     return torch.cuda.device(dev)
-
-
-def _take(t, name, shape, dtype, idx):
-    """Address of an optional contiguous argument tensor of the decode entry point, checked."""
-    if t is None:
-        return None
-    if t.get_device() != idx:
-        raise ValueError(f"{name}: on {t.device}, expected cuda:{idx}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name}: {t.dtype}, expected {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
 
 
 def decode_workspace(dtype: int, T: int, k: int, E: int, H: int, I: int, device,
@@ -634,7 +642,7 @@ class MoEBlock:
 
     w_router bf16 [E, H] with an optional bias [E]; shared_gu bf16 [2S, H] (G's rows, then
     U's) and shared_down bf16 [H, S], or neither.  A few tokens run through the layer's decode
-    form (see MoELayer.decodes), more through its call."""
+    form (see MoELayer.decodes), more through its call; both take contiguous rows of x only."""
 
     def __init__(self, layer: MoELayer, w_router, b_router=None, shared_gu=None,
                  shared_down=None):
