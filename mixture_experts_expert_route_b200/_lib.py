@@ -302,6 +302,18 @@ def combine(y_perm, inv_perm, T: int, k: int, H: int, out=None, stream=None):
     return out
 
 
+def _on_device(dev: torch.device, stream=None):
+    """Makes the tensors' device the current one, and the given stream (if any) torch's
+    current stream, so that buffers made inside belong to it."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError("the stream belongs to another device than the tensors")
+        return torch.cuda.stream(stream)
+    if dev.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(dev)
+
+
 def _take(t, name, shape, dtype, idx):
     """Address of an optional contiguous argument tensor of a layer entry point, checked."""
     if t is None:
@@ -328,12 +340,20 @@ def forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int, out=N
     each stage: entry, route+permute, FP8 x quantisation, gate/up, h quant, down,
     combine.  ``combine``: COMBINE_AUTO, COMBINE_DETERMINISTIC or COMBINE_FUSED.
     ``lora`` (a Lora) with ``adapter`` (CUDA int32 [T], -1 = none) applies
-    multi-LoRA adapters (bf16 layers).  x, logits, out, ids and w are contiguous."""
+    multi-LoRA adapters (bf16 layers).  x, logits, out, ids and w are contiguous.
+    Runs on x's device, on ``stream`` or the device's current one."""
     idx = x.get_device()
     if idx < 0:
         raise ValueError("expected a CUDA tensor")
     if x.dim() != 2:
         raise ValueError("x: expected [T, H]")
+    if stream is not None or idx != torch._C._cuda_getDevice():
+        with _on_device(x.device, stream):
+            return forward(dtype, x, logits, packed, scales, E, I, k, out, ids, w, status, ws,
+                           block_m, max_ctas, events, combine, lora, adapter)
+    for t, name in ((packed, "packed"), (scales, "scales"), (status, "status"), (ws, "ws")):
+        if t is not None and t.get_device() != idx:
+            raise ValueError(f"{name}: on {t.device}, expected cuda:{idx}")
     T, H = x.shape
     bf16, f32 = torch.bfloat16, torch.float32
     out = torch.empty((T, H), dtype=bf16, device=x.device) if out is None else out
@@ -363,18 +383,6 @@ def forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int, out=N
 
 DECODE_MAX_T, DECODE_MAX_ASSIGN = 16, 128     # tokens, T * k
 _DECODE_WS = {}    # (device index, stream) -> the workspace of MoELayer.decode calls there
-
-
-def _on_device(dev: torch.device, stream=None):
-    """Makes the tensors' device the current one, and the given stream (if any) torch's
-    current stream, so that buffers made inside belong to it."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError("the stream belongs to another device than the tensors")
-        return torch.cuda.stream(stream)
-    if dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(dev)
 
 
 def decode_workspace(dtype: int, T: int, k: int, E: int, H: int, I: int, device,
@@ -578,11 +586,14 @@ class MoELayer:
         return self._ws[T]
 
     def __call__(self, x, logits, out=None, events=None, stream=None):
+        if stream is not None or self.device.index != torch._C._cuda_getDevice():
+            with _on_device(self.device, stream):
+                return self(x, logits, out, events)
         T = x.shape[0]
         return forward(self.dtype, x, logits, self.packed, self.scales, self.E, self.I,
                        self.k, out=out, status=self.status, ws=self.workspace(T),
                        block_m=self.block_m, max_ctas=self.max_ctas, events=events,
-                       combine=self.combine, stream=stream)
+                       combine=self.combine)
 
     def decode_workspace(self, T: int, stream=None) -> torch.Tensor:
         """The workspace of decode calls on a stream: one per device and stream, shared by all
@@ -625,8 +636,10 @@ class MoELayer:
                               self.k, residual, out, ids, w, self.status,
                               self.decode_workspace(T) if T > 0 else None)
 
-    def check(self) -> int:
-        code = check_status(self.status)
+    def check(self, stream=None) -> int:
+        """The status word after the work on the stream (None: the device's current one)."""
+        with _on_device(self.device, stream):
+            code = check_status(self.status)
         if code == 5:       # a wait ran out: later decode calls get workspaces made anew
             for key in [key for key in _DECODE_WS if key[0] == self.device.index]:
                 del _DECODE_WS[key]
@@ -652,7 +665,7 @@ class MoEBlock:
         self.shared_gu, self.shared_down = shared_gu, shared_down
 
     def __call__(self, x, residual=None, stream=None):
-        if stream is not None:
+        if stream is not None or x.get_device() != torch._C._cuda_getDevice():
             with _on_device(x.device, stream):
                 return self(x, residual)
         logits = linear(x, self.w_router, bias=self.b_router, out_dtype=torch.float32)

@@ -1,0 +1,121 @@
+"""The layer's and the block's Python side without a GPU: which device, stream, workspace and
+status word their calls use.  Tensors and streams are stand-ins; nothing is launched."""
+import contextlib
+
+import pytest
+import torch
+
+
+class OnDevice:
+    """A CUDA tensor as far as the calls' device handling looks at it."""
+    is_cuda = True
+
+    def __init__(self, shape, index, dtype=torch.bfloat16):
+        self.shape, self.index, self.dtype = shape, index, dtype
+        self.device = torch.device("cuda", index)
+
+    def get_device(self):
+        return self.index
+
+    def dim(self):
+        return len(self.shape)
+
+    def data_ptr(self):
+        return 0x1000
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return 1 << 40
+
+
+@pytest.fixture
+def L(monkeypatch):
+    from mixture_experts_expert_route_b200 import _lib, build
+    build.build()
+    _lib.lib()
+    current = [0]
+
+    @contextlib.contextmanager
+    def on_device(dev, stream=None):
+        before = current[0]
+        current[0] = dev.index
+        yield
+        current[0] = before
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0])
+    monkeypatch.setattr(_lib, "_on_device", on_device)
+    _lib.test_current = current
+    yield _lib
+    del _lib.test_current
+
+
+def _layer(L, E=8, k=2, H=256, I=128, index=1):
+    layer = object.__new__(L.MoELayer)
+    layer.E, layer.H, layer.I, layer.k, layer.dtype = E, H, I, k, 0
+    layer.block_m = layer.max_ctas = layer.combine = 0
+    layer.packed, layer.scales = OnDevice((1,), index, torch.uint8), None
+    layer.status, layer.device = OnDevice((1,), index, torch.int32), torch.device("cuda", index)
+    layer._ws, layer._decode_need = {}, {}
+    return layer
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_every_step_of_a_block_runs_on_the_tensors_device(L, monkeypatch, T):
+    """The current device is 0, the tensors are on 1: so are products, experts and the sum."""
+    layer = _layer(L)
+    seen = []
+    result = OnDevice((T, 256), 1)
+    result.add_ = lambda r: seen.append(("add", L.test_current[0])) or result
+
+    def record(name):
+        def call(*a, **kw):
+            seen.append((name, L.test_current[0]))
+            return result
+        return call
+
+    monkeypatch.setattr(L, "linear", record("linear"))
+    monkeypatch.setattr(L, "forward", record("forward"))
+    monkeypatch.setattr(L, "decode_forward", record("decode"))
+    monkeypatch.setattr(L.MoELayer, "workspace", record("workspace"))
+    monkeypatch.setattr(L.MoELayer, "decode_workspace", record("workspace"))
+    monkeypatch.setattr(L.MoELayer, "decodes", lambda self, T: T <= 16)
+    block = L.MoEBlock(layer, OnDevice((8, 256), 1), None, OnDevice((64, 256), 1),
+                       OnDevice((256, 32), 1))
+    block(OnDevice((T, 256), 1), OnDevice((T, 256), 1))
+    assert {n for n, _ in seen} >= {"linear", "workspace", "decode" if T <= 16 else "forward"}
+    assert all(dev == 1 for _, dev in seen), seen
+    assert L.test_current[0] == 0
+
+
+def test_forward_runs_on_the_tensors_device(L, monkeypatch):
+    seen = []
+
+    class Lib:
+        def __getattr__(self, name):
+            def call(*a):
+                seen.append((name, L.test_current[0]))
+                return 0 if name == "moe_forward" else 64
+            return call
+
+    monkeypatch.setattr(L, "lib", lambda: Lib())
+    monkeypatch.setattr(L, "_stream", lambda stream=None: 0)
+    x, logits = OnDevice((20, 256), 1), OnDevice((20, 8), 1, torch.float32)
+    packed, ws, out = (OnDevice((1,), 1, torch.uint8), OnDevice((1,), 1, torch.uint8),
+                       OnDevice((20, 256), 1))
+    assert L.forward(0, x, logits, packed, None, 8, 128, 2, out=out, ws=ws) is out
+    assert ("moe_forward", 1) in seen and all(dev == 1 for _, dev in seen)
+    # weights, scales, status and workspace of another device are refused
+    for bad in (dict(packed=OnDevice((1,), 0)), dict(scales=OnDevice((8, 3), 0, torch.float32)),
+                dict(status=OnDevice((1,), 0, torch.int32)), dict(ws=OnDevice((1,), 0)),
+                dict(logits=OnDevice((20, 8), 0, torch.float32)), dict(out=OnDevice((20, 256), 0))):
+        with pytest.raises(ValueError, match="expected cuda:1"):
+            L.forward(**{**dict(dtype=0, x=x, logits=logits, packed=packed, scales=None, E=8,
+                                I=128, k=2, out=out, ws=ws), **bad})
+
+
+def test_check_waits_on_the_layers_device(L, monkeypatch):
+    seen = []
+    monkeypatch.setattr(L, "check_status", lambda t: seen.append(L.test_current[0]) or 0)
+    assert _layer(L).check() == 0 and seen == [1]
