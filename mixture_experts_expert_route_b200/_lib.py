@@ -579,11 +579,20 @@ class MoELayer:
         self._decode_need = {}
 
     def workspace(self, T: int) -> torch.Tensor:
-        if T not in self._ws:
+        """The workspace of a call with T tokens on the device's current stream: one per T and
+        stream (calls on one stream follow one another, on different streams they may overlap).
+        A call captured into a graph gets one of its own: the graph may be replayed on any
+        stream, beside other calls."""
+        capturing = torch.cuda.is_current_stream_capturing()
+        key = (T, torch._C._cuda_getCurrentRawStream(self.device.index))
+        ws = None if capturing else self._ws.get(key)
+        if ws is None:
             n = forward_workspace_size(self.dtype, T, self.k, self.E, self.H, self.I,
                                        self.block_m)
-            self._ws[T] = torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
-        return self._ws[T]
+            ws = torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
+            if not capturing:
+                self._ws[key] = ws
+        return ws
 
     def __call__(self, x, logits, out=None, events=None, stream=None):
         if stream is not None or self.device.index != torch._C._cuda_getDevice():

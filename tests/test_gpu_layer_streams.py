@@ -1,0 +1,73 @@
+"""MoELayer's call and MoEBlock beyond a few tokens: at the same time on several streams, and
+captured into graphs that are replayed beside one another and beside eager calls."""
+import pytest
+import torch
+
+from tests.gpu_helpers import lib
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF = torch.bfloat16
+
+
+def _block(moe, E=16, k=2, H=512, I=384, S=128, dtype=0, seed=0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g, device=DEV)  # noqa: E731
+    layer = moe.MoELayer((r(E, H, I) / H ** 0.5).to(BF), (r(E, H, I) / H ** 0.5).to(BF),
+                         (r(E, I, H) / I ** 0.5).to(BF), k, dtype=dtype)
+    return moe.MoEBlock(layer, (r(E, H) / H ** 0.5).to(BF), None,
+                        (r(2 * S, H) / H ** 0.5).to(BF), (r(H, S) / S ** 0.5).to(BF))
+
+
+def _x(T, seed, H=512):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.randn((T, H), generator=g, device=DEV).to(BF)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("T", [40, 600])
+def test_block_on_two_streams_at_once(T, dtype):
+    moe = lib()
+    block = _block(moe, dtype=dtype)
+    xs = [_x(T, s) for s in range(4)]
+    want = [block(x, residual=x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for rep in range(20):
+        for n, x in enumerate(xs):
+            got.append((n, block(x, residual=x, stream=streams[n % 2])))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[n]) for n, y in got)
+    assert block.layer.check() == 0
+
+
+@pytest.mark.parametrize("T", [40, 600])
+def test_graphs_beside_one_another_and_beside_eager_calls(T):
+    moe = lib()
+    block = _block(moe)
+    statics = [_x(T, s) for s in range(2)]
+    block(statics[0], residual=statics[0])
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in statics:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(block(x, residual=x))
+        graphs.append(gr)
+    eager_x = _x(T, 9)
+    eager_want = block(eager_x, residual=eager_x)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.Stream()]
+    for rep in range(10):
+        for n, x in enumerate(statics):
+            x.copy_(_x(T, 100 + 2 * rep + n))
+        want = [block(x, residual=x) for x in statics]
+        torch.cuda.synchronize()
+        for n in range(2):
+            with torch.cuda.stream(streams[n]):
+                graphs[n].replay()
+        eager = [block(eager_x, residual=eager_x, stream=streams[2]) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(outs[n], want[n]) for n in range(2))
+        assert all(torch.equal(e, eager_want) for e in eager)
+    assert block.layer.check() == 0

@@ -119,3 +119,23 @@ def test_check_waits_on_the_layers_device(L, monkeypatch):
     seen = []
     monkeypatch.setattr(L, "check_status", lambda t: seen.append(L.test_current[0]) or 0)
     assert _layer(L).check() == 0 and seen == [1]
+
+
+def test_workspaces_of_streams_and_captures(L, monkeypatch):
+    """Calls that may run at the same time do not share a workspace: another stream has its own,
+    and a captured call has one that nothing else is given."""
+    layer, state = _layer(L), dict(stream=7, capturing=False)
+    monkeypatch.setattr(L, "forward_workspace_size", lambda *a: 100)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: bytearray(n))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda idx: state["stream"])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state["capturing"])
+    first = layer.workspace(40)
+    assert layer.workspace(40) is first and layer.workspace(41) is not first
+    state["stream"] = 8
+    second = layer.workspace(40)
+    assert second is not first and layer.workspace(40) is second
+    state["capturing"] = True
+    captured = [layer.workspace(40), layer.workspace(40)]
+    assert captured[0] is not captured[1] and all(c is not second for c in captured)
+    state.update(stream=7, capturing=False)
+    assert layer.workspace(40) is first
