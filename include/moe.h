@@ -28,10 +28,11 @@
  *   - T = 0 is a valid no-op.
  *   - Limits: 1 <= k <= E <= 256; H and I multiples of 64; block_m a multiple
  *     of 16 (the token granularity of the tensor-core tiles).
- *   - Process-wide state is limited to two things: the per-device opt-in of
+ *   - Process-wide state is limited to three things: the per-device opt-in of
  *     the larger kernels to more than 48 KB of shared memory (set on the first
- *     launch on each device, read-only afterwards), and the fixed scratch
- *     array of moe_align_permute_noalloc (see its entry).  The CPU/GPU split
+ *     launch on each device, read-only afterwards), the fixed scratch array of
+ *     moe_align_permute_noalloc (see its entry), and moe_linear's status word
+ *     of each device (see moe_linear_status).  The CPU/GPU split
  *     of moe_split.h adds its host thread pool (see there).  Apart from
  *     moe_align_permute_noalloc, calls on different streams with separate
  *     buffers may run concurrently.
@@ -371,7 +372,8 @@ MOE_API moe_status moe_decode_forward(const moe_decode_args* args, void* ws, siz
  *   residual  device [M,N] of out_type, rows ldr apart, or NULL; may be out
  *             itself with the same stride
  *   out       device [M,N] of out_type, rows ldo apart; must not overlap x or w
- *   status    optional device status word
+ *   status    device status word, or NULL: the device's own (moe_linear_status).
+ *             A wait that runs out (MOE_ERR_TIMEOUT) leaves out incomplete
  * Activations: NONE; RELU; SILU z/(1+e^-z); GELU z(1+erf(z/sqrt 2))/2;
  * GELU_TANH, its tanh form z(1+tanh(sqrt(2/pi)(z+0.044715z^3)))/2.  A NaN stays
  * a NaN through each.
@@ -410,6 +412,13 @@ typedef struct {
 } moe_linear_args;
 
 MOE_API moe_status moe_linear(const moe_linear_args* args, moe_stream_t stream);
+
+/*
+ * Synchronises the stream, then returns what moe_linear calls without a status
+ * word have recorded on the current device since the last call of this
+ * function: MOE_OK or MOE_ERR_TIMEOUT.
+ */
+MOE_API moe_status moe_linear_status(moe_stream_t stream);
 
 /*
  * Reads a device status word: synchronises the stream, then returns

@@ -111,6 +111,7 @@ _SIGS = {
     "moe_decode_workspace_init": ([P, SZ, P], I32),
     "moe_decode_forward": ([ctypes.POINTER(DecodeArgs), P, SZ, P], I32),
     "moe_linear": ([P, P], I32),
+    "moe_linear_status": ([P], I32),
     "moe_check_status": ([P, P], I32),
     "moe_selftest_wait_timeout": ([P, I32, P], I32),
     # CPU/GPU split (include/moe_split.h)
@@ -496,12 +497,13 @@ def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=N
 
     x bf16 [M, K] and w bf16 [N, K] (gated: [2N, K], gate rows then up rows), rows any multiple
     of 8 elements apart; bias bf16 or f32 [rows of w]; residual and out of ``out_dtype`` (bf16,
-    the default, or f32).  ``out`` may be the residual."""
-    if stream is None and status is None:
-        y = _calls.linear(x, w, bias, act, gated, residual, out, out_dtype)
+    the default, or f32).  ``out`` may be the residual.  ``status`` (int32, on x's device) gets
+    the code of a wait that runs out; without one linear_status tells."""
+    if stream is None:
+        y = _calls.linear(x, w, bias, act, gated, residual, out, out_dtype, status)
         if y is not NotImplemented:
             return y
-    # another device or stream, a status word, or an argument to refuse
+    # another device or stream, or an argument to refuse
     idx = x.get_device()
     if idx < 0:
         raise ValueError("expected a CUDA tensor")
@@ -536,8 +538,8 @@ def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=N
         ldr = _rows(residual, "residual", M, N, out_dtype, idx)
         res_p = residual.data_ptr()
     if status is not None:
-        if status.get_device() != idx:
-            raise ValueError(f"status: on {status.device}, expected cuda:{idx}")
+        if status.get_device() != idx or status.dtype is not torch.int32 or status.numel() < 1:
+            raise ValueError(f"status: expected int32 on cuda:{idx}")
         status_p = status.data_ptr()
     if out is None:
         out, ldo = x.new_empty((M, N)) if out_type == 0 else x.new_empty((M, N), dtype=out_dtype), N
@@ -549,6 +551,13 @@ def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=N
     if code:
         raise MoEError(code, "moe_linear")
     return out
+
+
+def linear_status(stream=None) -> int:
+    """Synchronises the stream (None: the current one) and returns the code that linear calls
+    without a status word recorded on the current device since this was last called: 0, or 5
+    where a wait ran out."""
+    return lib().moe_linear_status(_stream(stream))
 
 
 def check_status(status: torch.Tensor, stream=None) -> int:
@@ -664,7 +673,8 @@ class MoEBlock:
 
     w_router bf16 [E, H] with an optional bias [E]; shared_gu bf16 [2S, H] (G's rows, then
     U's) and shared_down bf16 [H, S], or neither.  A few tokens run through the layer's decode
-    form (see MoELayer.decodes), more through its call; both take contiguous rows of x only."""
+    form (see MoELayer.decodes), more through its call; both take contiguous rows of x only.
+    A fault in any part is in the layer's status word (layer.check())."""
 
     def __init__(self, layer: MoELayer, w_router, b_router=None, shared_gu=None,
                  shared_down=None):
@@ -677,13 +687,15 @@ class MoEBlock:
         if stream is not None or x.get_device() != torch._C._cuda_getDevice():
             with _on_device(x.device, stream):
                 return self(x, residual)
-        logits = linear(x, self.w_router, bias=self.b_router, out_dtype=torch.float32)
+        st = self.layer.status       # of the products too: layer.check() tells of the whole block
+        logits = linear(x, self.w_router, bias=self.b_router, out_dtype=torch.float32, status=st)
         few = self.layer.decodes(x.shape[0])
         out = residual if few else self.layer(x, logits)
         if self.shared_gu is not None:
-            h = linear(x, self.shared_gu, act=ACT_SILU, gated=True)
+            h = linear(x, self.shared_gu, act=ACT_SILU, gated=True, status=st)
             # (in place where the routed experts' sum is this call's own)
-            out = linear(h, self.shared_down, residual=out, out=None if few else out)
+            out = linear(h, self.shared_down, residual=out, out=None if few else out,
+                         status=st)
         if few:
             return self.layer.decode(x, logits, residual=out)
         return out if residual is None else out.add_(residual)

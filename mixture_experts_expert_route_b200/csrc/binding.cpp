@@ -3,9 +3,9 @@
 // 4 us, its arguments' checks, the output's allocation and the call through
 // ctypes take the host 7.6 (here 3.9).
 //
-// linear(x, w, bias, act, gated, residual, out, out_dtype) and decode(dtype, x,
-// logits, packed, scales, E, I, k, residual, out, ids, w, status, ws) check what
-// the Python forms check, and return the output, or NotImplemented where anything
+// linear(x, w, bias, act, gated, residual, out, out_dtype, status) and
+// decode(dtype, x, logits, packed, scales, E, I, k, residual, out, ids, w, status,
+// ws) check what the Python forms check, and return the output, or NotImplemented where anything
 // is not as the entry point wants it: the Python form then says what.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -106,6 +106,13 @@ PyObject* run_linear(PyObject* const* args) {
         a.ldr = row_stride(r, M, N, type, dev);
         if (a.ldr < 0) return nullptr;
         a.residual = r.const_data_ptr();
+    }
+    if (args[8] != Py_None) {
+        if (!THPVariable_Check(args[8])) return nullptr;
+        const at::Tensor& s = THPVariable_Unpack(args[8]);
+        if (!s.is_cuda() || s.get_device() != dev || s.scalar_type() != at::kInt || s.numel() < 1)
+            return nullptr;
+        a.status = static_cast<int32_t*>(s.mutable_data_ptr());
     }
     at::Tensor out;
     if (args[6] != Py_None) {
@@ -239,7 +246,7 @@ template <class F> PyCFunction method(F f) {
 }
 
 PyMethodDef kMethods[] = {
-    {"linear", method(call<8, run_linear>), METH_FASTCALL, nullptr},
+    {"linear", method(call<9, run_linear>), METH_FASTCALL, nullptr},
     {"decode", method(call<14, run_decode>), METH_FASTCALL, nullptr},
     {"init", method(init), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

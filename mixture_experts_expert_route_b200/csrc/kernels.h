@@ -227,6 +227,8 @@ struct LinearProblem {
     int32_t* status;
 };
 cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s);
+// the current device's word of calls without one (status null); clears it
+cudaError_t read_linear_status(int32_t* code, cudaStream_t s);
 
 // ---- the bf16 grouped FFN (a3..a6) over E_sub consecutive segments of a
 // permutation (moe_api.cu): counts/offsets point at the first of them and

@@ -49,6 +49,10 @@ constexpr int kRowBytes = 128;           // one swizzle atom: 64 bf16 of K
 constexpr int kBK = 64;
 constexpr uint64_t kDrainLimitNs = 10000000ull;
 
+// Where a wait that ran out is recorded when the call gives no status word: one
+// per device, read by moe_linear_status.
+__device__ int32_t own_status;
+
 struct Args {
     int M, N, K;
     int act, gated;
@@ -63,6 +67,10 @@ struct Args {
     int vec;                             // bytes that out's and residual's rows are aligned to: 32, 16 or 0
     int32_t* status;
 };
+
+__device__ __forceinline__ void report_timeout(const Args& g) {
+    report(g.status ? g.status : &own_status, MOE_ERR_TIMEOUT);
+}
 
 __device__ __forceinline__ float load_bias(const Args& g, int row) {
     if (!g.bias) return 0.0f;
@@ -633,7 +641,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         for (int kb = kb0; kb < kb1; ++kb, ++issued) {
             const uint32_t st = issued % S, use = issued / S;
             if (use > 0 && !mbar_wait(&ctl.empty[st], (use - 1) & 1u, &ctl.abort)) {
-                report(g.status, MOE_ERR_TIMEOUT);
+                report_timeout(g);
                 *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
                 break;
             }
@@ -652,7 +660,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         for (int kb = kb0; kb < kb1; ++kb) {
             const uint32_t i = kb - kb0, st = i % S;
             if (!mbar_wait(&ctl.full[st], (i / S) & 1u, &ctl.abort)) {
-                report(g.status, MOE_ERR_TIMEOUT);
+                report_timeout(g);
                 *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
                 break;
             }
@@ -672,7 +680,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     __syncwarp();
     // the accumulator is whole (or the wait ran out): every thread, so that
     // none leaves while products read the ring
-    if (!mbar_wait(&ctl.done, 0, nullptr, 2 * kWaitLimitNs)) report(g.status, MOE_ERR_TIMEOUT);
+    if (!mbar_wait(&ctl.done, 0, nullptr, 2 * kWaitLimitNs)) report_timeout(g);
     tc_fence_after();
     __syncthreads();
     if (*reinterpret_cast<volatile int*>(&ctl.abort) && threadIdx.x == 0) {
@@ -814,7 +822,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int P = gridDim.x >> 1, p0 = blockIdx.x >> 1;
     const int KB = (g.K + kBK - 1) / kBK;
     auto raise = [&]() {
-        report(g.status, MOE_ERR_TIMEOUT);
+        report_timeout(g);
         *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
     };
 
@@ -1066,7 +1074,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int KB = (g.K + kBK - 1) / kBK;
     const int kb0 = pair ? KB / 2 : 0, kb1 = pair ? KB : KB / 2;
     auto raise = [&]() {
-        report(g.status, MOE_ERR_TIMEOUT);
+        report_timeout(g);
         *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
     };
     const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
@@ -1445,6 +1453,15 @@ cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s) {
                            ((static_cast<long long>(p.N) + per / 2 - 1) / (per / 2));
     if (t128 * 2 >= sms) return launch_tile<128>(g, sms, s);
     return launch_tile<64>(g, sms, s);
+}
+
+cudaError_t read_linear_status(int32_t* code, cudaStream_t s) {
+    void* word = nullptr;
+    cudaError_t e = cudaGetSymbolAddress(&word, own_status);
+    if (e == cudaSuccess) e = cudaMemcpyAsync(code, word, sizeof(*code), cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && *code != 0) e = cudaMemsetAsync(word, 0, sizeof(*code), s);
+    return e;
 }
 
 }  // namespace moe

@@ -702,6 +702,12 @@ moe_status moe_linear(const moe_linear_args* a, moe_stream_t stream) {
     return from_cuda(launch_linear(p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+moe_status moe_linear_status(moe_stream_t stream) {
+    int32_t v = 0;
+    const cudaError_t e = read_linear_status(&v, reinterpret_cast<cudaStream_t>(stream));
+    return e != cudaSuccess ? MOE_ERR_CUDA : static_cast<moe_status>(v);
+}
+
 moe_status moe_check_status(const int32_t* dev_status, moe_stream_t stream) {
     if (!dev_status) return MOE_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -139,3 +139,31 @@ def test_workspaces_of_streams_and_captures(L, monkeypatch):
     assert captured[0] is not captured[1] and all(c is not second for c in captured)
     state.update(stream=7, capturing=False)
     assert layer.workspace(40) is first
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_a_blocks_products_report_to_the_layer(L, monkeypatch, T):
+    """A wait that runs out in any of the block's products is seen by layer.check()."""
+    layer, seen = _layer(L), []
+    result = OnDevice((T, 256), 1)
+
+    def linear(*a, status=None, **kw):
+        seen.append(status)
+        return result
+
+    monkeypatch.setattr(L, "linear", linear)
+    monkeypatch.setattr(L.MoELayer, "__call__", lambda *a, **kw: result)
+    monkeypatch.setattr(L.MoELayer, "decode", lambda *a, **kw: result)
+    monkeypatch.setattr(L.MoELayer, "decodes", lambda self, T: T <= 16)
+    L.MoEBlock(layer, OnDevice((8, 256), 1), None, OnDevice((64, 256), 1),
+               OnDevice((256, 32), 1))(OnDevice((T, 256), 1))
+    assert len(seen) == 3 and all(s is layer.status for s in seen)
+
+
+def test_linear_passes_its_status_word_on(L, monkeypatch):
+    """The compiled call gets it (a call with a status word is not a slower one)."""
+    seen = []
+    monkeypatch.setattr(L._calls, "linear", lambda *a: seen.append(a) or "out")
+    status = OnDevice((1,), 0, torch.int32)
+    assert L.linear(OnDevice((4, 64), 0), OnDevice((8, 64), 0), status=status) == "out"
+    assert seen[0][-1] is status
