@@ -603,11 +603,19 @@ class MoELayer:
                 self._ws[key] = ws
         return ws
 
+    def _tokens(self, x) -> int:
+        """The rows of x, whose width must be the layer's: the packed tiles of another H would be
+        read as this one's."""
+        T, H = x.shape
+        if H != self.H:
+            raise ValueError(f"x: {H} columns, the layer has H = {self.H}")
+        return T
+
     def __call__(self, x, logits, out=None, events=None, stream=None):
         if stream is not None or self.device.index != torch._C._cuda_getDevice():
             with _on_device(self.device, stream):
                 return self(x, logits, out, events)
-        T = x.shape[0]
+        T = self._tokens(x)
         return forward(self.dtype, x, logits, self.packed, self.scales, self.E, self.I,
                        self.k, out=out, status=self.status, ws=self.workspace(T),
                        block_m=self.block_m, max_ctas=self.max_ctas, events=events,
@@ -649,7 +657,7 @@ class MoELayer:
         if stream is not None or self.device.index != torch._C._cuda_getDevice():
             with _on_device(self.device, stream):
                 return self.decode(x, logits, residual, out, ids, w)
-        T = x.shape[0]
+        T = self._tokens(x)
         return decode_forward(self.dtype, x, logits, self.packed, self.scales, self.E, self.I,
                               self.k, residual, out, ids, w, self.status,
                               self.decode_workspace(T) if T > 0 else None)

@@ -63,3 +63,22 @@ def test_arguments_of_the_layers_call():
             moe.forward(**{**args, **bad})
     out = torch.empty_like(x)
     assert moe.forward(**args, out=out, ids=ids, w=w) is out and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("T", [4, 20])
+def test_x_of_another_width(T, dtype):
+    """x narrower or wider than the layer's H (H = 192 and 256 have e4m3 tiles of one size)."""
+    moe = lib()
+    layer = _layer(moe, H=256, dtype=dtype)
+    for H in (64, 128, 192, 320, 512):
+        x, logits = _inputs(T, H, 8)
+        with pytest.raises(ValueError, match="H = 256"):
+            layer(x, logits)
+        with pytest.raises(ValueError, match="H = 256"):
+            layer.decode(x, logits)
+    for x in (x[0], x[:, :, None]):
+        with pytest.raises(ValueError):
+            layer(x, logits)
+        with pytest.raises(ValueError):
+            layer.decode(x, logits)

@@ -167,3 +167,17 @@ def test_linear_passes_its_status_word_on(L, monkeypatch):
     status = OnDevice((1,), 0, torch.int32)
     assert L.linear(OnDevice((4, 64), 0), OnDevice((8, 64), 0), status=status) == "out"
     assert seen[0][-1] is status
+
+
+@pytest.mark.parametrize("form", ["__call__", "decode"])
+def test_x_of_another_width_is_refused(L, monkeypatch, form):
+    """Before anything is launched, for every T and type (e4m3 tiles of H = 192 and 256 have the
+    same size, so the size of the packed weights does not tell them apart)."""
+    for name in ("forward", "decode_forward", "decode_workspace"):
+        monkeypatch.setattr(L, name, lambda *a, **kw: pytest.fail("launched"))
+    layer = _layer(L, H=256, index=0)
+    for dtype in (0, 1):
+        layer.dtype = dtype
+        for shape in ((4, 192), (20, 128), (4, 320), (256,), (4, 256, 1)):
+            with pytest.raises(ValueError):
+                getattr(layer, form)(OnDevice(shape, 0), OnDevice((shape[0], 8), 0))
