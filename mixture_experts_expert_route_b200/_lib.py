@@ -11,6 +11,7 @@ import contextlib
 import ctypes
 import os
 import struct
+import warnings
 
 import torch
 
@@ -409,12 +410,23 @@ class _Calls:
         self.decode = lambda *args: self._bind().decode(*args)
 
     def _bind(self):
+        addresses = [ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in
+                     ("moe_linear", "moe_decode_forward", "moe_packed_weights_size")]
+        why = None
         try:
             from . import _binding as b
-            b.init(*(ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value for name in
-                     ("moe_linear", "moe_decode_forward", "moe_packed_weights_size")))
+            if b.torch_version != torch.__version__.split("+")[0]:
+                why = f"built for torch {b.torch_version}"
+        except ModuleNotFoundError:         # (not built: build.py has said why)
+            b = None
+        except ImportError as e:            # of another torch or Python, say
+            b, why = None, e
+        if why is not None:
+            warnings.warn(f"_binding.so is not used, calls go through ctypes: {why}")
+        if b is not None and why is None:
+            b.init(*addresses)
             self.linear, self.decode = b.linear, b.decode
-        except ModuleNotFoundError:
+        else:
             self.linear = self.decode = lambda *args: NotImplemented
         return self
 
