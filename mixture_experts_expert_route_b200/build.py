@@ -27,6 +27,7 @@ HOST_SOURCES = ["host_ffn.cpp"]
 HEADERS = ["common.cuh", "kernels.h", "topk.cuh"]
 LIB = os.path.join(HERE, "libmoe_b200.so")
 BINDING = os.path.join(HERE, "_binding.so")    # a Python extension: moe.linear's call
+BINDING_STAMP = os.path.join(ROOT, "_build", "binding.txt")    # what it was built for
 LIB_DEBUG = os.path.join(HERE, "libmoe_b200_debug.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -51,12 +52,23 @@ def _stale(lib: str) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_stamp() -> str:
+    """What the extension is built for besides its sources: it uses torch's and Python's own
+    object layouts."""
+    import torch
+    return f"{sys.implementation.cache_tag} torch {torch.__version__} " \
+           f"abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+
+
 def build_binding(force: bool = False) -> None:
     """csrc/binding.cpp against the installed torch (host code only).  The package works
-    without it, with slower calls, so a machine without Python's headers only gets a warning."""
+    without it, with slower calls, so a machine without g++ or Python's headers only gets a
+    warning."""
     src = os.path.join(CSRC, "binding.cpp")
     deps = (src, os.path.join(ROOT, "include", "moe.h"))
-    if not force and os.path.exists(BINDING) and \
+    stamp = _binding_stamp()
+    if not force and os.path.exists(BINDING) and os.path.exists(BINDING_STAMP) and \
+            open(BINDING_STAMP).read() == stamp and \
             all(os.path.getmtime(BINDING) >= os.path.getmtime(d) for d in deps):
         return
     import torch
@@ -75,8 +87,15 @@ def build_binding(force: bool = False) -> None:
                                "-L" + os.path.join(pkg, "lib"), "-lc10", "-lc10_cuda",
                                "-ltorch_cpu", "-ltorch_python"])
         os.replace(tmp, BINDING)
-    except subprocess.CalledProcessError as e:
+        os.makedirs(os.path.dirname(BINDING_STAMP), exist_ok=True)
+        with open(BINDING_STAMP, "w") as f:
+            f.write(stamp)
+    except (subprocess.CalledProcessError, OSError) as e:
         warnings.warn(f"{BINDING} was not built ({e}): calls go through ctypes")
+        # an extension of other sources, torch or Python must not be taken for this one
+        for path in (tmp, BINDING):
+            if os.path.exists(path):
+                os.remove(path)
 
 
 def build(force: bool = False, ptxas_verbose: bool = False, debug: bool = False) -> str:

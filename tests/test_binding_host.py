@@ -1,6 +1,8 @@
 """The compiled calls (csrc/binding.cpp) without a GPU: an extension that does not fit this
 torch or Python, and its build."""
 import importlib
+import os
+import subprocess
 import sys
 import types
 
@@ -88,3 +90,51 @@ def test_a_missing_library_stays_an_error(L, monkeypatch, tmp_path):
     monkeypatch.setattr(L, "_lib", None)
     with pytest.raises(ImportError, match="absent.so"):
         L._Calls().linear(*range(9))
+
+
+@pytest.fixture
+def elsewhere(monkeypatch, tmp_path):
+    """build.py with the extension's place in an empty folder, and the commands it runs."""
+    from mixture_experts_expert_route_b200 import build
+    commands = []
+
+    def run(cmd):
+        commands.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("built")
+
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(build, "BINDING_STAMP", str(tmp_path / "b" / "binding.txt"), raising=False)
+    monkeypatch.setattr(build.subprocess, "check_call", run)
+    return build, commands
+
+
+def test_another_torch_rebuilds_the_extension(elsewhere, monkeypatch):
+    build, commands = elsewhere
+    build.build_binding()
+    build.build_binding()
+    assert len(commands) == 1
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    build.build_binding()
+    build.build_binding()
+    assert len(commands) == 2
+    monkeypatch.setattr(sys.implementation, "cache_tag", "cpython-399")
+    build.build_binding()
+    assert len(commands) == 3
+
+
+@pytest.mark.parametrize("error", [FileNotFoundError("g++"),
+                                   subprocess.CalledProcessError(1, ["g++"])])
+def test_a_machine_that_cannot_build_the_extension(elsewhere, monkeypatch, error):
+    """No compiler, or no headers: a warning, and no extension of other sources is left over."""
+    build, commands = elsewhere
+    build.build_binding()
+
+    def run(cmd):
+        raise error
+
+    monkeypatch.setattr(build.subprocess, "check_call", run)
+    monkeypatch.setattr(torch, "__version__", "9.9.9")
+    with pytest.warns(UserWarning, match="calls go through ctypes"):
+        build.build_binding()
+    assert not os.path.exists(build.BINDING)
