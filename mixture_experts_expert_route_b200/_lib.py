@@ -707,6 +707,7 @@ class MoEBlock:
         if stream is not None or x.get_device() != torch._C._cuda_getDevice():
             with _on_device(x.device, stream):
                 return self(x, residual)
+        _take(residual, "residual", x.shape, torch.bfloat16, x.get_device())
         st = self.layer.status       # of the products too: layer.check() tells of the whole block
         logits = linear(x, self.w_router, bias=self.b_router, out_dtype=torch.float32, status=st)
         few = self.layer.decodes(x.shape[0])

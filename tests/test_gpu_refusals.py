@@ -82,3 +82,18 @@ def test_x_of_another_width(T, dtype):
             layer(x, logits)
         with pytest.raises(ValueError):
             layer.decode(x, logits)
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_residuals_that_a_block_refuses(T):
+    """The same ones for every T: nothing is broadcast or converted."""
+    moe = lib()
+    layer = _layer(moe)
+    block = moe.MoEBlock(layer, (torch.randn((8, 256), device=DEV) / 16).to(BF))
+    x, _ = _inputs(T, 256, 8)
+    for residual in (x[0].contiguous(), x[:1].contiguous(), x.float(), x[:T - 1], x.cpu(),
+                     torch.zeros((T, 512), dtype=BF, device=DEV)[:, :256], x[:1].expand(T, 256)):
+        with pytest.raises(ValueError, match="residual"):
+            block(x, residual)
+    before = x.clone()
+    assert torch.equal(block(x, x), block(x, residual=before)) and torch.equal(x, before)

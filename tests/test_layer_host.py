@@ -181,3 +181,14 @@ def test_x_of_another_width_is_refused(L, monkeypatch, form):
         for shape in ((4, 192), (20, 128), (4, 320), (256,), (4, 256, 1)):
             with pytest.raises(ValueError):
                 getattr(layer, form)(OnDevice(shape, 0), OnDevice((shape[0], 8), 0))
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_a_blocks_residual_is_checked_before_anything_runs(L, monkeypatch, T):
+    monkeypatch.setattr(L, "linear", lambda *a, **kw: pytest.fail("launched"))
+    block = L.MoEBlock(_layer(L, index=0), OnDevice((8, 256), 0))
+    x = OnDevice((T, 256), 0)
+    for bad in (OnDevice((256,), 0), OnDevice((1, 256), 0), OnDevice((T, 256), 0, torch.float32),
+                OnDevice((T, 256), 1)):
+        with pytest.raises(ValueError, match="residual"):
+            block(x, bad)
