@@ -331,6 +331,24 @@ def _take(t, name, shape, dtype, idx):
     return t.data_ptr()
 
 
+def _bytes(t, name, idx):
+    """Address of a buffer of bytes (packed weights, a workspace), whose numel is its size."""
+    if t.get_device() != idx:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{idx}")
+    if t.dtype is not torch.uint8 or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous uint8")
+    return t.data_ptr()
+
+
+def _word(t, idx):
+    """Address of an optional status word."""
+    if t is None:
+        return None
+    if t.get_device() != idx or t.dtype is not torch.int32 or t.numel() < 1:
+        raise ValueError(f"status: expected int32 on cuda:{idx}")
+    return t.data_ptr()
+
+
 def forward_workspace_size(dtype, T, k, E, H, I, block_m=0) -> int:
     return lib().moe_forward_workspace_size(dtype, T, k, E, H, I, block_m)
 
@@ -353,9 +371,8 @@ def forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int, out=N
         with _on_device(x.device, stream):
             return forward(dtype, x, logits, packed, scales, E, I, k, out, ids, w, status, ws,
                            block_m, max_ctas, events, combine, lora, adapter)
-    for t, name in ((packed, "packed"), (scales, "scales"), (status, "status"), (ws, "ws")):
-        if t is not None and t.get_device() != idx:
-            raise ValueError(f"{name}: on {t.device}, expected cuda:{idx}")
+    if scales is not None and scales.get_device() != idx:
+        raise ValueError(f"scales: on {scales.device}, expected cuda:{idx}")
     T, H = x.shape
     bf16, f32 = torch.bfloat16, torch.float32
     out = torch.empty((T, H), dtype=bf16, device=x.device) if out is None else out
@@ -372,13 +389,14 @@ def forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int, out=N
         ev_arr = (ctypes.c_void_p * 7)(*[e.cuda_event for e in events])
     largs = lora.args(adapter) if lora is not None else None
     a = ForwardArgs(dtype, T, k, E, H, I, block_m, _take(x, "x", (T, H), bf16, idx),
-                    _take(logits, "logits", (T, E), f32, idx), _ptr(packed), _ptr(scales),
+                    _take(logits, "logits", (T, E), f32, idx), _bytes(packed, "packed", idx),
+                    _ptr(scales),
                     _take(out, "out", (T, H), bf16, idx), _take(ids, "ids", (T, k), torch.int32, idx),
-                    _take(w, "w", (T, k), f32, idx), _ptr(status), max_ctas,
+                    _take(w, "w", (T, k), f32, idx), _word(status, idx), max_ctas,
                     ctypes.cast(ev_arr, ctypes.c_void_p) if ev_arr is not None else None,
                     7 if ev_arr is not None else 0, combine,
                     ctypes.pointer(largs) if largs is not None else None)
-    _check(lib().moe_forward(ctypes.byref(a), _ptr(ws), ws.numel(), _stream(stream)),
+    _check(lib().moe_forward(ctypes.byref(a), _bytes(ws, "ws", idx), ws.numel(), _stream(stream)),
            "moe_forward")
     return out
 
@@ -457,9 +475,7 @@ def decode_forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int
                                   w, status, ws)
     T, H = x.shape
     bf16, f32 = torch.bfloat16, torch.float32
-    for t, name in ((packed, "packed"), (status, "status"), (ws, "ws")):
-        if t is not None and t.get_device() != idx:
-            raise ValueError(f"{name}: on {t.device}, expected cuda:{idx}")
+    packed_p = _bytes(packed, "packed", idx)
     if packed.numel() < lib().moe_packed_weights_size(dtype, E, H, I):
         raise ValueError("packed: smaller than these sizes need")
     if out is None:
@@ -467,12 +483,13 @@ def decode_forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int
     if ws is None and T > 0:
         ws = decode_workspace(dtype, T, k, E, H, I, x.device)
     a = DecodeArgs(dtype, T, k, E, H, I, _take(x, "x", (T, H), bf16, idx),
-                   _take(logits, "logits", (T, E), f32, idx), packed.data_ptr(),
+                   _take(logits, "logits", (T, E), f32, idx), packed_p,
                    _take(scales, "scales", (E, 3), f32, idx),
                    _take(residual, "residual", (T, H), bf16, idx),
                    _take(out, "out", (T, H), bf16, idx), _take(ids, "ids", (T, k), torch.int32, idx),
-                   _take(w, "w", (T, k), f32, idx), None if status is None else status.data_ptr())
-    code = lib().moe_decode_forward(ctypes.byref(a), None if ws is None else ws.data_ptr(),
+                   _take(w, "w", (T, k), f32, idx), _word(status, idx))
+    code = lib().moe_decode_forward(ctypes.byref(a),
+                                    None if ws is None else _bytes(ws, "ws", idx),
                                     0 if ws is None else ws.numel(),
                                     torch._C._cuda_getCurrentRawStream(idx))
     if code:
@@ -538,7 +555,7 @@ def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=N
         raise ValueError(f"out_dtype: {out_dtype}, expected bfloat16 or float32")
     ldx = _rows(x, "x", M, K, bf16, idx)
     ldw = _rows(w, "w", rows, K, bf16, idx)
-    bias_type = bias_p = ldr = res_p = status_p = 0
+    bias_type = bias_p = ldr = res_p = 0
     if bias is not None:
         bias_type = _FLOAT_TYPE.get(bias.dtype)
         if bias_type is None:
@@ -549,10 +566,7 @@ def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=N
     if residual is not None:
         ldr = _rows(residual, "residual", M, N, out_dtype, idx)
         res_p = residual.data_ptr()
-    if status is not None:
-        if status.get_device() != idx or status.dtype is not torch.int32 or status.numel() < 1:
-            raise ValueError(f"status: expected int32 on cuda:{idx}")
-        status_p = status.data_ptr()
+    status_p = _word(status, idx) or 0
     if out is None:
         out, ldo = x.new_empty((M, N)) if out_type == 0 else x.new_empty((M, N), dtype=out_dtype), N
     else:

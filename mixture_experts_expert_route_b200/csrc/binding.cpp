@@ -47,6 +47,23 @@ bool float_type(at::ScalarType t, int* code) {
     return t == at::kFloat || t == at::kBFloat16;
 }
 
+// An optional status word on the device.
+bool status_word(PyObject* o, int dev, int32_t** p) {
+    *p = nullptr;
+    if (o == Py_None) return true;
+    if (!THPVariable_Check(o)) return false;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda() || t.get_device() != dev || t.scalar_type() != at::kInt || t.numel() < 1)
+        return false;
+    *p = static_cast<int32_t*>(t.mutable_data_ptr());
+    return true;
+}
+
+// A buffer of bytes on the device, whose numel is its size.
+bool bytes_on(const at::Tensor& t, int dev) {
+    return t.is_cuda() && t.get_device() == dev && t.scalar_type() == at::kByte && t.is_contiguous();
+}
+
 // The output that the caller gave, else the new one.
 PyObject* result(PyObject* given, at::Tensor&& out) {
     if (given == Py_None) return THPVariable_Wrap(std::move(out));
@@ -108,13 +125,7 @@ PyObject* run_linear(PyObject* const* args) {
         if (a.ldr < 0) return nullptr;
         a.residual = r.const_data_ptr();
     }
-    if (args[8] != Py_None) {
-        if (!THPVariable_Check(args[8])) return nullptr;
-        const at::Tensor& s = THPVariable_Unpack(args[8]);
-        if (!s.is_cuda() || s.get_device() != dev || s.scalar_type() != at::kInt || s.numel() < 1)
-            return nullptr;
-        a.status = static_cast<int32_t*>(s.mutable_data_ptr());
-    }
+    if (!status_word(args[8], dev, &a.status)) return nullptr;
     at::Tensor out;
     if (args[6] != Py_None) {
         out = THPVariable_Unpack(args[6]);
@@ -155,8 +166,7 @@ PyObject* run_decode(PyObject* const* args) {
     const at::Tensor& ws = THPVariable_Unpack(args[13]);
     if (!x.is_cuda() || x.dim() != 2) return nullptr;
     const int dev = x.get_device();
-    if (dev != c10::cuda::current_device() || !packed.is_cuda() || packed.get_device() != dev ||
-        !ws.is_cuda() || ws.get_device() != dev)
+    if (dev != c10::cuda::current_device() || !bytes_on(packed, dev) || !bytes_on(ws, dev))
         return nullptr;
     const int64_t T = x.size(0), H = x.size(1);
     const long dtype = PyLong_AsLong(args[0]), E = PyLong_AsLong(args[5]),
@@ -188,12 +198,7 @@ PyObject* run_decode(PyObject* const* args) {
     a.scales = static_cast<const float*>(scales);
     a.ids = static_cast<int32_t*>(const_cast<void*>(ids));
     a.w = static_cast<float*>(const_cast<void*>(w));
-    if (args[12] != Py_None) {
-        if (!THPVariable_Check(args[12])) return nullptr;
-        const at::Tensor& t = THPVariable_Unpack(args[12]);
-        if (!t.is_cuda() || t.get_device() != dev) return nullptr;
-        a.status = static_cast<int32_t*>(t.mutable_data_ptr());
-    }
+    if (!status_word(args[12], dev, &a.status)) return nullptr;
     at::Tensor out;
     if (args[9] != Py_None) {
         const void* p;

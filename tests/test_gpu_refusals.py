@@ -97,3 +97,35 @@ def test_residuals_that_a_block_refuses(T):
             block(x, residual)
     before = x.clone()
     assert torch.equal(block(x, x), block(x, residual=before)) and torch.equal(x, before)
+
+
+@pytest.mark.parametrize("T", [3, 20])
+def test_buffers_of_another_type_or_layout(T):
+    """Packed weights, workspace and status word: a broadcast buffer has fewer bytes than its
+    numel says, a status word of another type fewer than the kernel writes."""
+    moe = lib()
+    layer = _layer(moe)
+    x, logits = _inputs(T, 256, 8)
+    if T <= 16:
+        ws = moe.decode_workspace(0, T, 2, 8, 256, 128, DEV)
+
+        def call(packed=layer.packed, ws=ws, status=layer.status):
+            return moe.decode_forward(0, x, logits, packed, None, 8, 128, 2, ws=ws, status=status)
+    else:
+        ws = layer.workspace(T)
+
+        def call(packed=layer.packed, ws=ws, status=layer.status):
+            return moe.forward(0, x, logits, packed, None, 8, 128, 2, ws=ws, status=status)
+    want = call()
+    one = torch.zeros(1, dtype=torch.uint8, device=DEV)
+    for name, t in (("packed", layer.packed), ("ws", ws)):
+        for bad in (one.expand(t.numel()), torch.zeros(2 * t.numel(), dtype=torch.uint8,
+                                                       device=DEV)[::2],
+                    torch.zeros(t.numel(), dtype=torch.float16, device=DEV), t.cpu()):
+            with pytest.raises(ValueError, match=name):
+                call(**{name: bad})
+    for bad in (one, torch.zeros(1, dtype=torch.int64, device=DEV), layer.status.cpu(),
+                torch.zeros(0, dtype=torch.int32, device=DEV)):
+        with pytest.raises(ValueError, match="status"):
+            call(status=bad)
+    assert torch.equal(call(), want) and layer.check() == 0

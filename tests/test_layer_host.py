@@ -107,10 +107,10 @@ def test_forward_runs_on_the_tensors_device(L, monkeypatch):
     assert L.forward(0, x, logits, packed, None, 8, 128, 2, out=out, ws=ws) is out
     assert ("moe_forward", 1) in seen and all(dev == 1 for _, dev in seen)
     # weights, scales, status and workspace of another device are refused
-    for bad in (dict(packed=OnDevice((1,), 0)), dict(scales=OnDevice((8, 3), 0, torch.float32)),
-                dict(status=OnDevice((1,), 0, torch.int32)), dict(ws=OnDevice((1,), 0)),
+    for bad in (dict(packed=OnDevice((1,), 0, torch.uint8)), dict(scales=OnDevice((8, 3), 0, torch.float32)),
+                dict(status=OnDevice((1,), 0, torch.int32)), dict(ws=OnDevice((1,), 0, torch.uint8)),
                 dict(logits=OnDevice((20, 8), 0, torch.float32)), dict(out=OnDevice((20, 256), 0))):
-        with pytest.raises(ValueError, match="expected cuda:1"):
+        with pytest.raises(ValueError, match="cuda:1"):
             L.forward(**{**dict(dtype=0, x=x, logits=logits, packed=packed, scales=None, E=8,
                                 I=128, k=2, out=out, ws=ws), **bad})
 
@@ -192,3 +192,21 @@ def test_a_blocks_residual_is_checked_before_anything_runs(L, monkeypatch, T):
                 OnDevice((T, 256), 1)):
         with pytest.raises(ValueError, match="residual"):
             block(x, bad)
+
+
+def test_buffers_are_checked_as_bytes(L):
+    """(on host tensors, whose device index is -1)"""
+    flat = torch.zeros(64, dtype=torch.uint8)
+    assert L._bytes(flat, "ws", -1) == flat.data_ptr()
+    for bad in (flat[:1].expand(64), flat[::2], flat.view(torch.float16)):
+        with pytest.raises(ValueError, match="ws: expected contiguous uint8"):
+            L._bytes(bad, "ws", -1)
+    with pytest.raises(ValueError, match="ws: on cpu"):
+        L._bytes(flat, "ws", 0)
+    word = torch.zeros(1, dtype=torch.int32)
+    assert L._word(word, -1) == word.data_ptr() and L._word(None, -1) is None
+    for bad in (flat, word.long(), word[:0]):
+        with pytest.raises(ValueError, match="status"):
+            L._word(bad, -1)
+    with pytest.raises(ValueError, match="status"):
+        L._word(word, 0)
