@@ -71,3 +71,19 @@ def test_graphs_beside_one_another_and_beside_eager_calls(T):
         assert all(torch.equal(outs[n], want[n]) for n in range(2))
         assert all(torch.equal(e, eager_want) for e in eager)
     assert block.layer.check() == 0
+
+
+def test_a_decode_workspace_made_on_a_stream():
+    """With the device named without its index too."""
+    moe = lib()
+    block = _block(moe)
+    layer, x = block.layer, _x(4, 0)
+    logits = moe.linear(x, block.w_router, out_dtype=torch.float32)
+    want = layer.decode(x, logits)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for device in ("cuda", "cuda:0", torch.device("cuda", 0)):
+        ws = moe.decode_workspace(0, 4, 2, 16, 512, 384, device, stream=side)
+        got = moe.decode_forward(0, x, logits, layer.packed, None, 16, 384, 2, ws=ws, stream=side)
+        side.synchronize()
+        assert torch.equal(got, want)

@@ -210,3 +210,19 @@ def test_buffers_are_checked_as_bytes(L):
             L._word(bad, -1)
     with pytest.raises(ValueError, match="status"):
         L._word(word, 0)
+
+
+def test_a_device_without_an_index_is_the_current_one(monkeypatch):
+    """device="cuda" and a stream of the current device; a stream of another one is refused."""
+    from types import SimpleNamespace
+
+    from mixture_experts_expert_route_b200 import _lib
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: ("stream", s))
+    monkeypatch.setattr(torch.cuda, "device", lambda d: ("device", d))
+    here, there = (SimpleNamespace(device=torch.device("cuda", i)) for i in (1, 0))
+    assert _lib._on_device(torch.device("cuda"), here) == ("stream", here)
+    assert isinstance(_lib._on_device(torch.device("cuda")), contextlib.nullcontext)
+    assert _lib._on_device(torch.device("cuda", 0)) == ("device", torch.device("cuda", 0))
+    with pytest.raises(ValueError, match="another device"):
+        _lib._on_device(torch.device("cuda"), there)
