@@ -435,6 +435,17 @@ MOE_API moe_status moe_check_status(const int32_t* dev_status, moe_stream_t stre
  */
 MOE_API moe_status moe_selftest_wait_timeout(int32_t* dev_status, int timeout_us, moe_stream_t stream);
 
+/*
+ * The same for the waits of moe_decode_forward and of moe_linear from 17 rows of
+ * x on; debug builds only (MOE_ERR_UNSUPPORTED otherwise).  From now on every
+ * wait in them is limited to limit_us (1 .. 1000000), and the blocks of one
+ * cluster rank (moe_decode_forward: the block of that index) copy only their
+ * first `copies` tiles: the waits for the others run out, MOE_ERR_TIMEOUT is
+ * recorded and the call ends, its output incomplete.  copies < 0 ends this.
+ * Process-wide; not for use beside other calls.
+ */
+MOE_API moe_status moe_selftest_withhold(int copies, int rank, int limit_us);
+
 #ifdef __cplusplus
 }
 #endif

@@ -115,6 +115,7 @@ _SIGS = {
     "moe_linear_status": ([P], I32),
     "moe_check_status": ([P, P], I32),
     "moe_selftest_wait_timeout": ([P, I32, P], I32),
+    "moe_selftest_withhold": ([I32, I32, I32], I32),
     # CPU/GPU split (include/moe_split.h)
     "moe_split_place": ([P, I32, I32, P], I32),
     "moe_split_plan": ([P, P, I32, ctypes.POINTER(SplitCosts), I32, P], I32),
@@ -595,6 +596,12 @@ def check_status(status: torch.Tensor, stream=None) -> int:
 def selftest_wait_timeout(status: torch.Tensor, timeout_us: int, stream=None) -> None:
     _check(lib().moe_selftest_wait_timeout(_ptr(status), timeout_us, _stream(stream)),
            "moe_selftest_wait_timeout")
+
+
+def selftest_withhold(copies: int, rank: int = 0, limit_us: int = 2000) -> None:
+    """Debug builds: decode and linear launches leave out copies, so that their waits run out
+    (see moe.h); copies < 0 ends it."""
+    _check(lib().moe_selftest_withhold(copies, rank, limit_us), "moe_selftest_withhold")
 
 
 class MoELayer:

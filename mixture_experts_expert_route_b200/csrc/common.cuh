@@ -27,6 +27,25 @@ constexpr int kMaxExperts = 256;
 constexpr int kMaxCtas = 256;          // upper bound on the persistent grid
 constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s: no healthy wait comes close
 
+// What moe_selftest_withhold has set (debug builds; nothing elsewhere): the
+// blocks of one rank copy only their first tiles, and waits are short.  The base
+// of a pipelined kernel's arguments.
+#ifdef MOE_DEBUG_CHECKS
+struct SelfTest {
+    int copies = -1, rank = 0;
+    uint64_t limit_ns = kWaitLimitNs;
+    __device__ __forceinline__ bool withheld(int rank_, int issued) const {
+        return copies >= 0 && rank_ == rank && issued >= copies;
+    }
+    __device__ __forceinline__ uint64_t wait_limit() const { return limit_ns; }
+};
+#else
+struct SelfTest {
+    __device__ __forceinline__ bool withheld(int, int) const { return false; }
+    __device__ __forceinline__ uint64_t wait_limit() const { return kWaitLimitNs; }
+};
+#endif
+
 // Status word: the first fault wins.
 __device__ __forceinline__ void report(int32_t* status, int code) {
     if (status) atomicCAS(status, 0, code);

@@ -124,7 +124,7 @@ __host__ __device__ __forceinline__ int operator/(int x, const Divisor& v) {
 }
 Divisor divisor(int d) { return Divisor{d, 1.0f / static_cast<float>(d)}; }
 
-struct Args {
+struct Args : SelfTest {
     int T, k, E, H, I;
     int mt_gu, kb_gu, mt_dn, kb_dn;
     Divisor by_mt_gu, by_kb_gu, by_mt_dn, by_S1, by_S2, by_G, by_hquads;
@@ -267,21 +267,22 @@ __device__ __forceinline__ void fault(Shared& s, int32_t* status) {
 
 // The bounded wait of this kernel's rings: the timer is read only now and then
 // (a read takes longer than a tile's products).
-__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool ring_wait(const Args& g, uint64_t* bar, uint32_t parity,
+                                          volatile int* abort) {
     uint64_t t0 = 0;
     for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
         if ((i & 31u) != 31u) continue;
         if (*abort) return false;
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
-        else if (now - t0 > kWaitLimitNs) return false;
+        else if (now - t0 > g.wait_limit()) return false;
     }
     return true;
 }
 
 // Arrival of this CTA at a grid barrier and the bounded wait until the counter
 // reaches `target`.  Called by one thread, between two consumer_sync.
-__device__ __forceinline__ bool grid_barrier(uint64_t* counter, uint64_t target) {
+__device__ __forceinline__ bool grid_barrier(const Args& g, uint64_t* counter, uint64_t target) {
     asm volatile("fence.acq_rel.gpu;\n\tred.release.gpu.global.add.u64 [%0], 1;" ::"l"(counter)
                  : "memory");
     const uint64_t t0 = globaltimer_ns();
@@ -289,7 +290,7 @@ __device__ __forceinline__ bool grid_barrier(uint64_t* counter, uint64_t target)
         uint64_t v;
         asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(counter) : "memory");
         if (v >= target) return true;
-        if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+        if (globaltimer_ns() - t0 > g.wait_limit()) return false;
     }
 }
 
@@ -634,12 +635,17 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
         Ring ring(slots);
         int it = 0;
         bool ok = true;
-        for (int X = a1; lane == 0 && X < b1 && ok;) {
+        bool withheld = false;
+        for (int X = a1; lane == 0 && X < b1 && ok && !withheld;) {
             const int i = X / g.by_S1, end = (i + 1) * S1 < b1 ? (i + 1) * S1 : b1;
             const uint8_t* w =
                 g.w_gu + (static_cast<size_t>(s.expert[i]) * S1 + (X - i * S1)) * kTileBytes;
             for (; X < end; ++X, w += kTileBytes) {
-                if (it >= slots && !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
+                if (g.withheld(cta, it)) {
+                    withheld = true;
+                    break;
+                }
+                if (it >= slots && !ring_wait(g, &s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
                     ok = false;
                     break;
                 }
@@ -652,17 +658,22 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
         }
         Plan plan(a2, b2, g, CK);
         Chunk ch;
-        while (lane == 0 && ok && !plan.done()) {
+        while (lane == 0 && ok && !withheld && !plan.done()) {
             plan.batch();
-            while (ok && plan.take(ch)) {
+            while (ok && !withheld && plan.take(ch)) {
                 const uint8_t* w = g.w_dn + static_cast<size_t>(s.expert[ch.i]) * S2 * kTileBytes;
                 int m0 = ch.m, kb0 = ch.kb;                    // of visit v0
-                for (int v0 = 0; v0 < ch.visits && ok; v0 += kGroups) {
-                    for (int L = ch.a + v0, d = 0; L < ch.b && ok; L += g.mt_dn, ++d) {
+                for (int v0 = 0; v0 < ch.visits && ok && !withheld; v0 += kGroups) {
+                    for (int L = ch.a + v0, d = 0; L < ch.b && ok && !withheld;
+                         L += g.mt_dn, ++d) {
                         int m = m0, kb = kb0 + d;
                         for (int q = 0; q < kGroups; ++q) {
+                            if (g.withheld(cta, it)) {
+                                withheld = true;
+                                break;
+                            }
                             if (it >= slots &&
-                                !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
+                                !ring_wait(g, &s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
                                 ok = false;
                                 break;
                             }
@@ -687,17 +698,11 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
                 }
             }
         }
-        if (!ok) {
-            fault(s, g.status);
-            // this CTA's copies in flight (the last `slots`, or fewer) land
-            // before its shared memory goes
-            Ring back(slots);
-            for (int j = 0; j < it; ++j) {
-                if (j >= it - slots)
-                    mbar_wait(&s.full[back.slot], back.phase, nullptr, 10000000ull);
-                back.skip(1);
-            }
-        }
+        if (!ok) fault(s, g.status);
+        // this CTA's copies in flight (of the last `slots` tiles, or fewer) land
+        // before its shared memory goes, also where a product warp gave up
+        for (int j = it > slots ? it - slots : 0; j < it; ++j)
+            mbar_wait(&s.full[j % slots], (j / slots) & 1u, nullptr, 10000000ull);
     } else if (warp == kXWarp) {
         // ---- the x slices of the gate/up tiles, in 16-byte pieces, one per lane
         // and turn (as bulk copies of a few hundred bytes each they kept the copy
@@ -706,13 +711,17 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
         int it = 0;
         constexpr int PIECES = BK / 8;                 // of a token's slice
         const int q = lane % PIECES;
-        for (int X = a1; X < b1;) {
+        bool ok = true;
+        for (int X = a1; X < b1 && ok;) {
             const int i = X / g.by_S1, end = (i + 1) * S1 < b1 ? (i + 1) * S1 : b1;
             const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
             int kb = X - X / g.by_kb_gu * g.kb_gu;
             for (; X < end; ++X) {
-                if (it >= slots && !ring_wait(&s.empty[ring.slot], ring.phase ^ 1u, &s.abort))
+                if (it >= slots && !ring_wait(g, &s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
                     fault(s, g.status);
+                    ok = false;
+                    break;
+                }
                 const uint32_t dst = smem_u32(smem + ring.slot * slot_sz + kTileBytes) + q * 16;
                 // (the last e4m3 k-block may hold 64 of its 128 columns: the rest
                 // is filled with zeros)
@@ -730,8 +739,13 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
         }
         cp_async_wait_all();
     } else {
-        // ---- consumers.  After a fault every wait returns at once, and the
-        // loops run on to their ends, so all warps meet at the same barriers.
+        // ---- consumers.  After a fault every wait returns soon, and the loops run
+        // on to their ends, so all warps meet at the same barriers.  But a warp whose
+        // wait ran out frees no slot any more: only a slot whose tile was there is
+        // free, so the copying warps never arrive on a phase with arrivals of
+        // another lap (with more than it has left the barrier is undefined), and
+        // stop in turn.
+        bool frees = lane == 0;
         const int gq = lane >> 2, t = lane & 3;
         const int grp = warp / kGroupWarps, wrow = warp % kGroupWarps * 32;  // first weight row
         Ring ring(slots, grp);
@@ -791,7 +805,10 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
             float acc[4][4] = {};
             for (; X < end; ++X) {
                 if (((X - a1) & (kGroups - 1)) != grp) continue;
-                if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort)) fault(s, g.status);
+                if (!ring_wait(g, &s.full[ring.slot], ring.phase, &s.abort)) {
+                    fault(s, g.status);
+                    frees = false;
+                }
                 uint8_t* tile = smem + ring.slot * slot_sz;
                 Wts w;
                 load_w(w, tile + wrow * kTileRowBytes, gq, t);
@@ -813,7 +830,7 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
                 if (MANY && (!FP8 || cnt > 8))
                     xb = load_act<FP8>(xs + rb * x_row_bytes<FP8>(), t);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
+                if (frees) mbar_arrive(&s.empty[ring.slot]);
                 ring.skip(kGroups);
                 if constexpr (!FP8) {
                     tile_mma(acc, w, xa, xb);
@@ -845,7 +862,7 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
             consumer_sync();
         }
         consumer_sync();
-        if (threadIdx.x == kBarThread && !grid_barrier(&g.hdr->arrive[0][0], target[0]))
+        if (threadIdx.x == kBarThread && !grid_barrier(g, &g.hdr->arrive[0][0], target[0]))
             fault(s, g.status);
         consumer_sync();
 
@@ -937,13 +954,15 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
                     const uint8_t* hr = hbuf + (ch.slot + kb0) * rows * h_row_bytes<FP8>();
                     for (int L = ch.a + v0; L < ch.b;
                          L += g.mt_dn, hr += rows * h_row_bytes<FP8>()) {
-                        if (!ring_wait(&s.full[ring.slot], ring.phase, &s.abort))
+                        if (!ring_wait(g, &s.full[ring.slot], ring.phase, &s.abort)) {
                             fault(s, g.status);
+                            frees = false;
+                        }
                         const bool real = visit && L + vq < ch.b;
                         Wts w;
                         if (real) load_w(w, smem + ring.slot * slot_sz + wrow * kTileRowBytes, gq, t);
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&s.empty[ring.slot]);
+                        if (frees) mbar_arrive(&s.empty[ring.slot]);
                         ring.skip(kGroups);
                         if (!real) continue;
                         const uint8_t* ha = hr + ra * h_row_bytes<FP8>();
@@ -1016,7 +1035,7 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
                        : make_uint2(0u, 0u);
         };
         uint2 res = residual_of(item_of(cta * per_cta));
-        if (threadIdx.x == kBarThread && !grid_barrier(&g.hdr->arrive[1][0], target[1]))
+        if (threadIdx.x == kBarThread && !grid_barrier(g, &g.hdr->arrive[1][0], target[1]))
             fault(s, g.status);
         consumer_sync();
 
@@ -1270,6 +1289,7 @@ cudaError_t launch_decode(const DecodeProblem& p, cudaStream_t s) {
     const int grid = device_sm_count();
     const Sizes z = sizes(fp8, p.T, p.k, p.E, p.H, p.I, grid);
     Args g{};
+    static_cast<SelfTest&>(g) = self_test();
     g.T = p.T;
     g.k = p.k;
     g.E = p.E;

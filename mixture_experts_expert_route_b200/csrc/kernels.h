@@ -191,6 +191,7 @@ size_t gemm_partials_bytes(int nmax);
 cudaError_t launch_grouped_gemm(const GemmProblem& p, cudaStream_t s);
 
 int device_sm_count();
+const struct SelfTest& self_test();      // (see common.cuh)
 
 // ---- the whole layer for a few tokens (decode.cu)
 constexpr int kDecodeMaxT = 16;

@@ -1,7 +1,8 @@
 // moe_api.cu -- the extern "C" boundary declared in include/moe.h: argument
 // validation (nothing is launched on a bad argument), workspace carving, and
 // the order of launches on the caller's stream.  Never allocates, never
-// synchronises (except moe_check_status, whose job is to read the device).
+// synchronises (except moe_check_status and moe_linear_status, whose job is to
+// read the device).
 #include <nvtx3/nvToolsExt.h>
 
 #include <cstdint>
@@ -13,6 +14,8 @@
 using namespace moe;
 
 namespace {
+
+SelfTest g_self_test;        // see moe_selftest_withhold
 
 constexpr size_t kAlign = 256;
 // control block: status, amax_x, amax_h, stream-K counters of the gate/up and
@@ -357,6 +360,8 @@ Combine pick_combine(int mode) {
 }  // namespace
 
 namespace moe {
+
+const SelfTest& self_test() { return g_self_test; }
 
 size_t segment_ffn_ws_bytes(int T, int capacity, int H, int I) {
     Carver c{nullptr};
@@ -718,6 +723,18 @@ moe_status moe_check_status(const int32_t* dev_status, moe_stream_t stream) {
     if (v == 0) return MOE_OK;
     if (v == MOE_ERR_TIMEOUT || v == MOE_ERR_DEVICE) return static_cast<moe_status>(v);
     return MOE_ERR_DEVICE;
+}
+
+moe_status moe_selftest_withhold(int copies, int rank, int limit_us) {
+#ifdef MOE_DEBUG_CHECKS
+    if (copies >= 0 && (rank < 0 || limit_us < 1 || limit_us > 1000000)) return MOE_ERR_INVALID_ARG;
+    g_self_test = SelfTest{};
+    if (copies >= 0) g_self_test = SelfTest{copies, rank, limit_us * 1000ull};
+    return MOE_OK;
+#else
+    (void)copies, (void)rank, (void)limit_us;
+    return MOE_ERR_UNSUPPORTED;
+#endif
 }
 
 moe_status moe_selftest_wait_timeout(int32_t* dev_status, int timeout_us, moe_stream_t stream) {
