@@ -53,7 +53,7 @@ constexpr uint64_t kDrainLimitNs = 10000000ull;
 // per device, read by moe_linear_status.
 __device__ int32_t own_status;
 
-struct Args {
+struct Args : SelfTest {
     int M, N, K;
     int act, gated;
     const __nv_bfloat16* x;
@@ -664,8 +664,10 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     if (warp == 0 && lane == 0) {
         uint32_t issued = 0;
         for (int kb = kb0; kb < kb1; ++kb, ++issued) {
+            if (g.withheld(rank, issued)) break;
             const uint32_t st = issued % S, use = issued / S;
-            if (use > 0 && !mbar_wait(&ctl.empty[st], (use - 1) & 1u, &ctl.abort)) {
+            if (use > 0 &&
+                !mbar_wait(&ctl.empty[st], (use - 1) & 1u, &ctl.abort, g.wait_limit())) {
                 report_timeout(g);
                 *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
                 break;
@@ -684,7 +686,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         const uint32_t idesc = make_idesc<false>(kTileM, BN);
         for (int kb = kb0; kb < kb1; ++kb) {
             const uint32_t i = kb - kb0, st = i % S;
-            if (!mbar_wait(&ctl.full[st], (i / S) & 1u, &ctl.abort)) {
+            if (!mbar_wait(&ctl.full[st], (i / S) & 1u, &ctl.abort, g.wait_limit())) {
                 report_timeout(g);
                 *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
                 break;
@@ -705,7 +707,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     __syncwarp();
     // the accumulator is whole (or the wait ran out): every thread, so that
     // none leaves while products read the ring
-    if (!mbar_wait(&ctl.done, 0, nullptr, 2 * kWaitLimitNs)) report_timeout(g);
+    if (!mbar_wait(&ctl.done, 0, nullptr, 2 * g.wait_limit())) report_timeout(g);
     tc_fence_after();
     __syncthreads();
     if (*reinterpret_cast<volatile int*>(&ctl.abort) && threadIdx.x == 0) {
@@ -788,9 +790,50 @@ struct PairCtl {
     uint64_t drain;
     uint32_t tmem;
     int abort;
-    uint32_t prod_pos, mma_pos, mma_issued;
+    uint32_t prod_pos, mma_pos;        // stages filled (by this CTA), and read
     alignas(16) float bias[2][kPairN];
 };
+
+// A wait that ran out ends the cluster's work together: every CTA's waits return,
+// and after the last cluster barrier all of them know.
+template <int CTAS>
+__device__ __forceinline__ void abort_cluster(const Args& g, PairCtl& ctl) {
+    report_timeout(g);
+#pragma unroll
+    for (int r = 0; r < CTAS; ++r)
+        asm volatile("st.shared::cluster.u32 [%0], 1;" ::"r"(cluster_addr(smem_u32(&ctl.abort), r))
+                     : "memory");
+}
+
+// Then the products that a pair has issued end, and its copies land (bounded),
+// before its memory goes.  Of the stages that the products have not read some may
+// have been filled by one CTA only: the even one, on whose barriers both CTAs'
+// copies complete, adds what the phase lacks of the other's.
+__device__ __forceinline__ void drain_pair(PairCtl& ctl, int warp, int lane, int side, int rank) {
+    if (side != 0 || lane != 0) return;
+    if (warp == 1) {
+        umma_commit_pair_local(&ctl.drain);
+        mbar_wait(&ctl.drain, 0, nullptr, kDrainLimitNs);
+    } else if (warp == 0) {
+        const uint32_t own = ctl.prod_pos;
+        uint32_t peer;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                     : "=r"(peer)
+                     : "r"(cluster_addr(smem_u32(&ctl.prod_pos), rank + 1))
+                     : "memory");
+        for (uint32_t it = ctl.mma_pos; it < max(own, peer); ++it) {
+            uint64_t* bar = &ctl.full[it % kPairStages];
+            if (it >= own)
+                mbar_arrive_expect_tx(bar, kPairStageBytes);
+            else if (it >= peer)
+                asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(
+                                 smem_u32(bar)),
+                             "r"(kPairStageBytes)
+                             : "memory");
+            mbar_wait(bar, (it / kPairStages) & 1u, nullptr, kDrainLimitNs);
+        }
+    }
+}
 
 // Tile t of the rasterised order: groups of 8 row tiles, in a group column tile
 // by column tile, so that the tiles in flight share operands in L2.
@@ -826,7 +869,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         mbar_init(&ctl.drain, 1);
         fence_mbar_init();
         ctl.abort = 0;
-        ctl.prod_pos = ctl.mma_pos = ctl.mma_issued = 0;
+        ctl.prod_pos = ctl.mma_pos = 0;
         tma_prefetch_desc(&maps.x);
         tma_prefetch_desc(&maps.w);
     }
@@ -846,10 +889,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int tm = (g.M + 255) / 256, tn = (g.N + per - 1) / per, tiles = tm * tn;
     const int P = gridDim.x >> 1, p0 = blockIdx.x >> 1;
     const int KB = (g.K + kBK - 1) / kBK;
-    auto raise = [&]() {
-        report_timeout(g);
-        *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
-    };
+    auto raise = [&]() { abort_cluster<2>(g, ctl); };
 
     if (warp == 0) {
         if (lane == 0) {
@@ -866,7 +906,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const int xrow = m * 256 + rank * 128;
                 const int wrow = g.gated ? rank * g.N + n * per : n * BN + rank * (BN / 2);
                 for (int kb = 0; kb < KB; ++kb, ++it) {
-                    if (!mbar_wait(&ctl.empty[st], par, &ctl.abort)) {
+                    if (g.withheld(rank, it)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!mbar_wait(&ctl.empty[st], par, &ctl.abort, g.wait_limit())) {
                         raise();
                         ok = false;
                         break;
@@ -893,17 +937,17 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int st = 0;
             uint32_t ph = 0, it = 0, i = 0;
             bool ok = true;
-            ctl.mma_issued = 1;
             for (int t = p0; t < tiles && ok; t += P, ++i) {
                 const int acc = i & 1;
-                if (!mbar_wait(&ctl.tempty[acc], ((i >> 1) & 1u) ^ 1u, &ctl.abort)) {
+                if (!mbar_wait(&ctl.tempty[acc], ((i >> 1) & 1u) ^ 1u, &ctl.abort,
+                               g.wait_limit())) {
                     raise();
                     break;
                 }
                 tc_fence_after();
                 const uint32_t d = tmem + acc * BN;
                 for (int kb = 0; kb < KB; ++kb, ++it) {
-                    if (!mbar_wait(&ctl.full[st], ph, &ctl.abort)) {
+                    if (!mbar_wait(&ctl.full[st], ph, &ctl.abort, g.wait_limit())) {
                         raise();
                         ok = false;
                         break;
@@ -952,7 +996,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             if (cb < ce && res && (WIDE || wide16(g, n0 + cb))) res16(g, row, n0 + cb, qa, qb);
             // (after a fault the waits return at once and the loop runs on, so
             // that all epilogue warps meet at the same barriers)
-            if (!mbar_wait(&ctl.tfull[acc], (i >> 1) & 1u, &ctl.abort)) raise();
+            if (!mbar_wait(&ctl.tfull[acc], (i >> 1) & 1u, &ctl.abort, g.wait_limit())) raise();
             tc_fence_after();
             // 16 columns at a time; the next ones' accumulators and residual are
             // on their way while these are worked on
@@ -1016,19 +1060,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
 
     __syncthreads();
-    if (*reinterpret_cast<volatile int*>(&ctl.abort)) {
-        // own products and copies in flight end (bounded) before the memory goes
-        if (warp == 1 && lane == 0 && ctl.mma_issued) {
-            umma_commit_pair_local(&ctl.drain);
-            mbar_wait(&ctl.drain, 0, nullptr, kDrainLimitNs);
-        }
-        if (warp == 0 && lane == 0 && rank == 0) {
-            for (uint32_t it = ctl.mma_pos; it < ctl.prod_pos; ++it)
-                mbar_wait(&ctl.full[it % S], (it / S) & 1u, nullptr, kDrainLimitNs);
-        }
-        __syncthreads();
-    }
     cluster_sync();
+    if (*reinterpret_cast<volatile int*>(&ctl.abort)) {        // in both CTAs or none
+        drain_pair(ctl, warp, lane, rank, rank);
+        __syncwarp();
+        __syncthreads();
+        cluster_sync();
+    }
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, 2 * BN);
@@ -1077,7 +1115,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         fence_mbar_init();
         mbar_arrive_expect_tx(&arrived, kShareBytes);
         ctl.abort = 0;
-        ctl.prod_pos = ctl.mma_pos = ctl.mma_issued = 0;
+        ctl.prod_pos = ctl.mma_pos = 0;
         tma_prefetch_desc(&maps.x);
         tma_prefetch_desc(&maps.w);
     }
@@ -1098,10 +1136,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int m = t % tm, n0 = t / tm * per;
     const int KB = (g.K + kBK - 1) / kBK;
     const int kb0 = pair ? KB / 2 : 0, kb1 = pair ? KB : KB / 2;
-    auto raise = [&]() {
-        report_timeout(g);
-        *reinterpret_cast<volatile int*>(&ctl.abort) = 1;
-    };
+    auto raise = [&]() { abort_cluster<4>(g, ctl); };
     const int q = warp & 3, half = (warp - kEpiWarp0) >> 2;
     const uint32_t ta = tmem + (static_cast<uint32_t>(32 * q) << 16);
 
@@ -1114,7 +1149,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int st = 0;
             uint32_t par = 1;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                if (!mbar_wait(&ctl.empty[st], par, &ctl.abort)) {
+                if (g.withheld(rank, it)) break;
+                if (!mbar_wait(&ctl.empty[st], par, &ctl.abort, g.wait_limit())) {
                     raise();
                     break;
                 }
@@ -1139,9 +1175,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int st = 0;
             uint32_t ph = 0, it = 0;
             bool ok = true;
-            ctl.mma_issued = 1;
             for (int kb = kb0; kb < kb1; ++kb, ++it) {
-                if (!mbar_wait(&ctl.full[st], ph, &ctl.abort)) {
+                if (!mbar_wait(&ctl.full[st], ph, &ctl.abort, g.wait_limit())) {
                     raise();
                     ok = false;
                     break;
@@ -1169,24 +1204,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             const int c = n0 + (g.gated && et >= BN / 2 ? et - BN / 2 : et);
             ctl.bias[0][et] = c < g.N ? load_bias(g, g.gated && et >= BN / 2 ? g.N + c : c) : 0.0f;
         }
-        if (!mbar_wait(&ctl.tfull[0], 0, &ctl.abort)) raise();
+        if (!mbar_wait(&ctl.tfull[0], 0, &ctl.abort, g.wait_limit())) raise();
         tc_fence_after();
     }
     __syncthreads();
-    if (*reinterpret_cast<volatile int*>(&ctl.abort)) {
-        // own products and copies in flight end (bounded) before the ring is
-        // written over
-        if (warp == 1 && lane == 0 && ctl.mma_issued) {
-            umma_commit_pair_local(&ctl.drain);
-            mbar_wait(&ctl.drain, 0, nullptr, kDrainLimitNs);
-        }
-        if (warp == 0 && lane == 0 && side == 0) {
-            for (uint32_t it = ctl.mma_pos; it < ctl.prod_pos; ++it)
-                mbar_wait(&ctl.full[it % S], (it / S) & 1u, nullptr, kDrainLimitNs);
-        }
-        __syncthreads();
-    }
-    // this CTA's ring is idle
+    // this CTA's ring is idle (or, after a fault, what is in it is of no account)
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
     // accumulator column of column l of share j: a gated share's first half are
     // gate columns, its second half their up columns
@@ -1216,7 +1238,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (half == 0 && lane == 0)
             bulk_to_cluster(cluster_addr(smem_u32(share), rank ^ 2), sent, kShareBytes / 4,
                             cluster_addr(smem_u32(&arrived), rank ^ 2));
-        if (!mbar_wait(&arrived, 0, nullptr)) raise();
+        if (!mbar_wait(&arrived, 0, nullptr, g.wait_limit())) raise();
     }
     if (warp >= kEpiWarp0) {
         const int outs = g.gated ? W / 2 : W;              // output columns of a share
@@ -1247,6 +1269,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     }
     tc_fence_before();
     cluster_sync();          // both CTAs of a pair have read their accumulators
+    if (*reinterpret_cast<volatile int*>(&ctl.abort)) {        // in all CTAs or none
+        drain_pair(ctl, warp, lane, side, rank);
+        __syncwarp();
+        __syncthreads();
+        cluster_sync();
+    }
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, BN);
@@ -1428,6 +1456,7 @@ cudaError_t launch_split(const Args& g, long long tiles, cudaStream_t s) {
 
 cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s) {
     Args g{};
+    static_cast<SelfTest&>(g) = self_test();
     g.M = p.M;
     g.N = p.N;
     g.K = p.K;

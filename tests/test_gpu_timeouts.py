@@ -1,4 +1,4 @@
-"""Waits that run out in the few-token layer: the copies that they wait for are withheld
+"""Waits that run out in the few-token layer and in the dense products: the copies that they wait for are withheld
 (moe_selftest_withhold, in a child process with the debug build) and the limit is 2 ms.  The call
 ends, MOE_ERR_TIMEOUT is in the status word, and the next call is right.  Nothing faults or hangs:
 every wait is bounded, and no copy or product is under way when a block leaves."""
@@ -53,6 +53,51 @@ for dtype in (0, 1):
 print("timeouts ok")
 '''
 
+LINEAR = PRELUDE + r'''
+SHAPES = [  # M, K, N, gated, ranks of a cluster
+    (512, 512, 4096, False, 1),       # 128-wide tiles, one block each
+    (77, 2880, 2880, False, 4),       # 64-wide tiles, four blocks
+    (4864, 1024, 1024, False, 2),     # CTA pairs, several tiles each
+    (2500, 1088, 2041, False, 2),     # ... with rows that are not aligned
+    (5000, 512, 1000, True, 2),
+    (512, 4160, 2048, True, 4),       # two pairs to a tile
+]
+for M, K, N, gated, ranks in SHAPES:
+    x, w = r(M, K).to(BF), (r(2 * N if gated else N, K) / K ** 0.5).to(BF)
+    def call(**kw):
+        return moe.linear(x, w, act=moe.ACT_SILU, gated=gated, **kw)
+    want = call()
+    assert moe.linear_status() == 0
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for copies in (0, 1, 5, 6, 9, 20, 33):
+        for rank in range(ranks):
+            moe.selftest_withhold(copies, rank)
+            own = copies % 2 == 0         # a status word, or the device's
+            out = call(status=status if own else None)
+            code = moe.check_status(status) if own else moe.linear_status()
+            moe.selftest_withhold(-1)
+            assert code == 5 or (code == 0 and copies > 4 and torch.equal(out, want)), \
+                (M, K, N, copies, rank, code)
+            assert code == 5 or copies > 0
+            status.zero_()
+            assert torch.equal(call(status=status), want) and moe.check_status(status) == 0
+            assert moe.linear_status() == 0
+# a block tells of its products
+E, k, H, I = 8, 2, 256, 128
+layer = moe.MoELayer((r(E, H, I) / 16).to(BF), (r(E, H, I) / 16).to(BF), (r(E, I, H) / 11).to(BF), k)
+block = moe.MoEBlock(layer, (r(E, H) / 16).to(BF))
+x = r(40, H).to(BF)
+want = block(x)
+assert layer.check() == 0
+moe.selftest_withhold(0)
+block(x)
+assert layer.check() == 5
+moe.selftest_withhold(-1)
+layer.status.zero_()
+assert torch.equal(block(x), want) and layer.check() == 0
+print("timeouts ok")
+'''
+
 
 def _child(code):
     env = dict(os.environ, MOE_B200_DEBUG_CHECKS="1")
@@ -64,6 +109,10 @@ def _child(code):
 
 def test_decode_waits_run_out():
     _child(DECODE)
+
+
+def test_linear_waits_run_out():
+    _child(LINEAR)
 
 
 def test_the_release_build_withholds_nothing():
