@@ -711,16 +711,15 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
         int it = 0;
         constexpr int PIECES = BK / 8;                 // of a token's slice
         const int q = lane % PIECES;
-        bool ok = true;
-        for (int X = a1; X < b1 && ok;) {
+        for (int X = a1; X < b1;) {
             const int i = X / g.by_S1, end = (i + 1) * S1 < b1 ? (i + 1) * S1 : b1;
             const int c0 = s.base[i], cnt = s.base[i + 1] - c0;
             int kb = X - X / g.by_kb_gu * g.kb_gu;
             for (; X < end; ++X) {
                 if (it >= slots && !ring_wait(g, &s.empty[ring.slot], ring.phase ^ 1u, &s.abort)) {
                     fault(s, g.status);
-                    ok = false;
-                    break;
+                    cp_async_wait_all();
+                    return;         // (a flag to leave the loops took 1% of the stream)
                 }
                 const uint32_t dst = smem_u32(smem + ring.slot * slot_sz + kTileBytes) + q * 16;
                 // (the last e4m3 k-block may hold 64 of its 128 columns: the rest
