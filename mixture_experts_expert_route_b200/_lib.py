@@ -12,6 +12,7 @@ import ctypes
 import os
 import struct
 import warnings
+import weakref
 
 import torch
 
@@ -405,7 +406,9 @@ def forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int, out=N
 
 
 DECODE_MAX_T, DECODE_MAX_ASSIGN = 16, 128     # tokens, T * k
-_DECODE_WS = {}    # (device index, stream) -> the workspace of MoELayer.decode calls there
+# (device index, stream) -> the workspace of MoELayer.decode calls there, kept by the layers
+# that use it
+_DECODE_WS = weakref.WeakValueDictionary()
 
 
 def decode_workspace(dtype: int, T: int, k: int, E: int, H: int, I: int, device,
@@ -620,7 +623,7 @@ class MoELayer:
         self.device = Wg.device
         self.status = torch.zeros(1, dtype=torch.int32, device=self.device)
         self._ws = {}
-        self._decode_need = {}
+        self._decode_need, self._decode_ws = {}, {}
 
     def workspace(self, T: int) -> torch.Tensor:
         """The workspace of a call with T tokens on the device's current stream: one per T and
@@ -659,7 +662,7 @@ class MoELayer:
     def decode_workspace(self, T: int, stream=None) -> torch.Tensor:
         """The workspace of decode calls on a stream: one per device and stream, shared by all
         layers (calls on one stream follow one another, on different streams they may
-        overlap).  A call captured into a graph gets one of its own, whose initialisation is
+        overlap) and released with the last of them.  A call captured into a graph gets one of its own, whose initialisation is
         captured with it: the graph may be replayed on any stream, and outlive the cache."""
         if torch.cuda.is_current_stream_capturing():
             return decode_workspace(self.dtype, T, self.k, self.E, self.H, self.I,
@@ -675,6 +678,7 @@ class MoELayer:
             ws = decode_workspace(self.dtype, T, self.k, self.E, self.H, self.I, self.device,
                                   stream)
             _DECODE_WS[key] = ws
+        self._decode_ws[key] = ws
         return ws
 
     def decodes(self, T: int) -> bool:
@@ -702,8 +706,8 @@ class MoELayer:
         with _on_device(self.device, stream):
             code = check_status(self.status)
         if code == 5:       # a wait ran out: later decode calls get workspaces made anew
-            for key in [key for key in _DECODE_WS if key[0] == self.device.index]:
-                del _DECODE_WS[key]
+            for key in [key for key in list(_DECODE_WS) if key[0] == self.device.index]:
+                _DECODE_WS.pop(key, None)
         return code
 
 

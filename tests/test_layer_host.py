@@ -57,7 +57,7 @@ def _layer(L, E=8, k=2, H=256, I=128, index=1):
     layer.block_m = layer.max_ctas = layer.combine = 0
     layer.packed, layer.scales = OnDevice((1,), index, torch.uint8), None
     layer.status, layer.device = OnDevice((1,), index, torch.int32), torch.device("cuda", index)
-    layer._ws, layer._decode_need = {}, {}
+    layer._ws, layer._decode_need, layer._decode_ws = {}, {}, {}
     return layer
 
 
@@ -226,3 +226,31 @@ def test_a_device_without_an_index_is_the_current_one(monkeypatch):
     assert _lib._on_device(torch.device("cuda", 0)) == ("device", torch.device("cuda", 0))
     with pytest.raises(ValueError, match="another device"):
         _lib._on_device(torch.device("cuda"), there)
+
+
+def test_decode_workspaces_are_shared_and_released(L, monkeypatch):
+    """One per stream for all layers, grown for the largest call; gone with the last layer."""
+    class Workspace:
+        def __init__(self, n):
+            self.n = n
+
+        def numel(self):
+            return self.n
+
+    class Lib:
+        moe_decode_workspace_size = staticmethod(lambda dtype, T, k, E, H, I: 1000 * T)
+
+    monkeypatch.setattr(L, "lib", lambda: Lib)
+    monkeypatch.setattr(L, "decode_workspace",
+                        lambda dtype, T, k, E, H, I, dev, stream=None: Workspace(1000 * T))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda idx: 7)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    a, b, key = _layer(L, index=93), _layer(L, index=93), (93, 7)
+    small = a.decode_workspace(2)
+    assert b.decode_workspace(1) is small and L._DECODE_WS[key] is small
+    large = b.decode_workspace(5)
+    assert large is not small and a.decode_workspace(2) is large
+    del small, large, a
+    assert key in L._DECODE_WS
+    del b
+    assert key not in L._DECODE_WS
