@@ -379,9 +379,13 @@ def forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int, out=N
         raise ValueError(f"scales: on {scales.device}, expected cuda:{idx}")
     T, H = x.shape
     bf16, f32 = torch.bfloat16, torch.float32
-    out = torch.empty((T, H), dtype=bf16, device=x.device) if out is None else out
-    n = forward_workspace_size(dtype, T, k, E, H, I, block_m)
+    if out is None:
+        out = x.new_empty((T, H), dtype=bf16)
+        out_p = out.data_ptr()
+    else:
+        out_p = _take(out, "out", (T, H), bf16, idx)
     if ws is None:
+        n = forward_workspace_size(dtype, T, k, E, H, I, block_m)
         ws = torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
     ev_arr = None
     if events is not None:
@@ -395,7 +399,7 @@ def forward(dtype: int, x, logits, packed, scales, E: int, I: int, k: int, out=N
     a = ForwardArgs(dtype, T, k, E, H, I, block_m, _take(x, "x", (T, H), bf16, idx),
                     _take(logits, "logits", (T, E), f32, idx), _bytes(packed, "packed", idx),
                     _ptr(scales),
-                    _take(out, "out", (T, H), bf16, idx), _take(ids, "ids", (T, k), torch.int32, idx),
+                    out_p, _take(ids, "ids", (T, k), torch.int32, idx),
                     _take(w, "w", (T, k), f32, idx), _word(status, idx), max_ctas,
                     ctypes.cast(ev_arr, ctypes.c_void_p) if ev_arr is not None else None,
                     7 if ev_arr is not None else 0, combine,
