@@ -1376,9 +1376,9 @@ cudaError_t launch_tile(const Args& g, int sms, cudaStream_t s) {
     const int KB = (g.K + kBK - 1) / kBK;
     // blocks of a cluster split K while all find room on the SMs and each keeps
     // at least 4 k-blocks; 6 where it shares its SM, and 12 where it would not
-    // without the first split (us, more / fewer blocks: M = K = 512, N = 4096 10 /
-    // 6.7; M = 512, K = 1024, N = 4096 11 / 9.2; M = 256, K = 2048, N = 768 7.9 /
-    // 7.1; but M = 64, K = N = 2880, 180 blocks of 11 k-blocks, 8.6 / 10.6)
+    // without the first split (us, more / fewer blocks: M = K = 512, N = 4096 10.0 /
+    // 7.5; M = 512, K = 1024, N = 4096 11.7 / 10.2; M = 256, K = 2048, N = 768 8.0 /
+    // 7.4; but M = 64, K = N = 2880, 180 blocks of 11 k-blocks, 9.4 / 11.5)
     int csize = 1;
     while (csize < 8 && tiles * csize * 2 <= 2 * sms &&
            KB >= (tiles * csize * 2 <= sms ? csize * 8 : csize == 1 ? 24 : csize * 12))
@@ -1481,31 +1481,36 @@ cudaError_t launch_linear(const LinearProblem& p, cudaStream_t s) {
     const int sms = device_sm_count();
     if (p.M <= 16) return launch_few(g, sms, s);
     // Measured on B200 (us, pair / 128-wide / 64-wide tiles): M = 1024, K = N =
-    // 4096 (64 pair tiles) 32 / 44 / 61; M = 512, K = 7168, N = 2 x 2048 (32) 43 /
-    // 34 / 42; M = 128, K = 4096, N = 2 x 14336 54 / 50 / 62; M = 300, K = N = 2880
-    // (69 128-wide tiles) 23 / 15 / 14; M = 4096, K = 2048, N = 128 (32) 15 / 13 /
-    // 10.  So: pairs once half of them have a tile and its 256 rows are not half
-    // empty; else 128-wide tiles once there is one for every second SM.
+    // 4096 (64 pair tiles) 28 / 34 / 45; M = 512, K = 7168, N = 2 x 2048 (32) 40 /
+    // 34 / 40; M = 128, K = 4096, N = 2 x 14336 58 / 49 / 60; M = 300, K = N = 2880
+    // (69 128-wide tiles) 19 / 14.0 / 13.3; M = 4096, K = 2048, N = 128 (32) 14.6 /
+    // 8.6 / 8.9.  So: pairs once half of them have a tile and its 256 rows are not
+    // half empty; else 128-wide tiles once there is one for every second SM.
     const int per = p.gated ? 128 : 256;
     const long long t256 = (static_cast<long long>(p.M) + 255) / 256 *
                            ((static_cast<long long>(p.N) + per - 1) / per);
-    // With few k-blocks and rows that are not aligned the epilogue counts, which
-    // twice the warps of the 128-wide tiles hide better (us, pair / 128-wide: M =
-    // 554, K = 128, N = 6602 38 / 15; M = 5000, K = 512, N = 1001 40 / 29; M = 4096,
-    // K = 1024, N = 2047 36 / 33; M = 3000, K = 2000, N = 2 x 3001 62 / 91).
-    if (p.M > 128 && t256 * 4 >= sms && (g.vec || p.K > 1024))
+    // Rows that are not aligned make the epilogue count, which twice the warps of
+    // the 128-wide tiles hide better unless K is long (us, pair / 128-wide: M = 554,
+    // K = 128, N = 6602 29 / 12; M = 5000, K = 512, N = 1001 32 / 22, K = 2048 41 /
+    // 38; M = 2500, N = 2041, K = 2048 41 / 39, K = 4096 58 / 59; M = 3000, K = 2000,
+    // N = 2 x 3001 62 / 91: half as many outputs of the same products).
+    if (p.M > 128 && t256 * 4 >= sms && (g.vec || p.K > (p.gated ? 1024 : 2048)))
         return g.vec && p.N % 16 == 0 ? launch_pair<true>(g, sms, s) : launch_pair<false>(g, sms, s);
-    // Fewer such tiles: two pairs to each, where all are resident and K is long
-    // enough to pay for their exchange (us, split / 128-wide): M = 512, K = 7168,
-    // N = 2 x 2048 (32) 27 / 34; K = N = 4096 20 / 27; K = 2048 14 / 16, K = 1024 11
-    // / 9.2; with the last 256 rows half empty M = 300, K = N = 2880 (24) 15 / 13.6,
-    // K = 4096 18 / 18; with 16 tiles, M = 256, K = N = 4096 19 / 17.
+    // Fewer such tiles: two pairs to each, where all are resident, K is long enough
+    // to pay for their exchange, and there are too many 128-wide tiles for two
+    // blocks of each to have SMs of their own (us, split / 128-wide: M = 512, K =
+    // 7168, N = 2 x 2048 28 / 34; M = 512, N = 4096, K = 4096 20 / 23, K = 2048 15.3 /
+    // 16.7; with the last 256 rows half empty M = 300, K = N = 4096 19 / 22; but with
+    // 69 128-wide tiles, M = 300, N = 2880, K = 4096 18 / 16, K = 14336 42 / 35, where
+    // 64-wide ones take 16 and 43; with 16 pair tiles, M = 256, K = N = 4096 16.7 /
+    // 16.6).
     const bool waste = (p.M - 1) % 256 < 128;
-    if (p.M > 128 && t256 > 16 && p.K >= (waste ? 4096 : 2048) && t256 < split_clusters())
-        return launch_split(g, t256, s);
     const long long t128 = (static_cast<long long>(p.M) + 127) / 128 *
                            ((static_cast<long long>(p.N) + per / 2 - 1) / (per / 2));
-    if (t128 * 2 >= sms) return launch_tile<128>(g, sms, s);
+    if (p.M > 128 && t256 > 16 && t128 * 2 > sms && p.K >= (waste ? 4096 : 2048) &&
+        t256 < split_clusters())
+        return launch_split(g, t256, s);
+    if (t128 * 2 >= sms || (t256 > 16 && p.K >= 4096)) return launch_tile<128>(g, sms, s);
     return launch_tile<64>(g, sms, s);
 }
 

@@ -58,7 +58,7 @@ SHAPES = [  # M, K, N, gated, ranks of a cluster
     (512, 512, 4096, False, 1),       # 128-wide tiles, one block each
     (77, 2880, 2880, False, 4),       # 64-wide tiles, four blocks
     (4864, 1024, 1024, False, 2),     # CTA pairs, several tiles each
-    (2500, 1088, 2041, False, 2),     # ... with rows that are not aligned
+    (2500, 2112, 2041, False, 2),     # ... with rows that are not aligned
     (5000, 512, 1000, True, 2),
     (512, 4160, 2048, True, 4),       # two pairs to a tile
 ]
