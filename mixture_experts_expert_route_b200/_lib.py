@@ -687,11 +687,11 @@ class MoELayer:
 
     def decodes(self, T: int) -> bool:
         """Whether decode is the faster form for T tokens: within its limits, and at most 1 GiB
-        of experts that the tokens may activate.  Measured on B200, decode / call: E = 128
-        H = 2048 I = 768 top-8, T = 1 29 / 42 us, T = 8 87 / 99, T = 16 130 / 141; e4m3 E = 32
-        H = I = 2880 top-4, T = 1 33 / 48, T = 8 103 / 111, T = 16 145 / 141; E = 64 H = 7168
-        I = 2048 top-8, T = 1 118 / 124, T = 2 212 / 208, T = 4 364 / 345; E = 8 H = 4096
-        I = 14336 top-2, T = 1 117 / 123, T = 4 287 / 279."""
+        of experts that the tokens may activate.  Measured on B200, us, decode / call on the same
+        inputs: E = 128 H = 2048 I = 768 top-8, T = 1 27 / 40, T = 8 86 / 98, T = 16 130 / 142;
+        e4m3 E = 32 H = I = 2880 top-4, T = 1 31 / 46, T = 8 102 / 111, T = 16 141 / 141; E = 64
+        H = 7168 I = 2048 top-8, T = 1 119 / 125, T = 2 204 / 205, T = 4 367 / 348; E = 8 H = 4096
+        I = 14336 top-2, T = 1 116 / 124, T = 4 286 / 275."""
         n = self.packed.numel() // self.E * min(T * self.k, self.E)
         return T <= DECODE_MAX_T and T * self.k <= DECODE_MAX_ASSIGN and n <= 1 << 30
 
@@ -725,7 +725,9 @@ class MoEBlock:
     w_router bf16 [E, H] with an optional bias [E]; shared_gu bf16 [2S, H] (G's rows, then
     U's) and shared_down bf16 [H, S], or neither.  A few tokens run through the layer's decode
     form (see MoELayer.decodes), more through its call; both take contiguous rows of x only.
-    A fault in any part is in the layer's status word (layer.check())."""
+    A fault in any part is in the layer's status word (layer.check()).  The two forms differ in
+    precision (decode keeps h in 16 bits, the call in bf16's 8), most for e4m3 experts, whose
+    activations only the call quantises; shared(x) and the routed sum are bf16 on their way."""
 
     def __init__(self, layer: MoELayer, w_router, b_router=None, shared_gu=None,
                  shared_down=None):

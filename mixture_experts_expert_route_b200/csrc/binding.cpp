@@ -1,7 +1,7 @@
 // binding.cpp -- the calls of moe_linear and moe_decode_forward from Python
 // without the interpreter's part of them: a product of a few tokens takes the GPU
 // 4 us, its arguments' checks, the output's allocation and the call through
-// ctypes take the host 7.6 (here 3.9).
+// ctypes take the host 7.5 (here 3.9).
 //
 // linear(x, w, bias, act, gated, residual, out, out_dtype, status) and
 // decode(dtype, x, logits, packed, scales, E, I, k, residual, out, ids, w, status,

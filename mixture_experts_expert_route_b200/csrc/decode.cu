@@ -38,12 +38,17 @@
 // down tile of a small layer took 1000 cycles.
 //
 // Measured on one B200 (us; floor = the active experts' bytes at the copy's 6.53
-// TB/s; then moe_forward, whose chain of kernels costs ~28 us before the stream):
-//   bf16 E=128 H=2048 I=768 top-8     T = 1: 27-29 (11.6; 42)    T = 8: 84 (72; 98)
-//   bf16 E=8 H=4096 I=14336 top-2     T = 1: 116 (108; 124)      T = 8: 414 (398; 386)
-//   bf16 E=64 H=7168 I=2048 top-8     T = 1: 117 (108; 124)      T = 8: 612 (554; 539)
-//   e4m3 E=32 H=I=2880 top-4          T = 1: 32-34 (15; 53)      T = 8: 104 (81; 113)
-// Where T = 1's 27.5 us go (the first of them): 3.2 us routing and tables in
+// TB/s; then moe_forward on the same inputs, whose chain of kernels costs 6
+// to 15 us more than this one's start and end, but whose tcgen05 stream is the
+// faster one):
+//   bf16 E=128 H=2048 I=768 top-8     T = 1: 27 (12; 40)      T = 8: 86 (74; 98)     T = 16: 130 (120; 142)
+//   bf16 E=8 H=4096 I=14336 top-2     T = 1: 116 (108; 124)   T = 8: 375-405 (377; 360-377)
+//   bf16 E=64 H=7168 I=2048 top-8     T = 1: 119 (108; 125)   T = 2: 204 (198; 205)  T = 8: 582-625 (578; 546-559)
+//   e4m3 E=32 H=I=2880 top-4          T = 1: 31 (15; 46)      T = 8: 102 (81; 111)   T = 13: 131 (102; 133)
+//                                     T = 16: 141 (109; 141)
+// 18 warps leave 96 registers a thread: 20 to 152 bytes of spills by form, most
+// where an expert may have more than 8 tokens.
+// Where T = 1's 27 us go (the first of them): 3.2 us routing and tables in
 // every CTA, 1.7 to the first tile, 7.4 of gate/up stream (9.6 in the last CTA),
 // 1.7 for the first barrier under the down tiles' prefetch, 4.6 of h and down
 // products, 1.2 for the second barrier, 2.3 of final sums, 2.5 between launches.
@@ -553,7 +558,9 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
     return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// Stores one (e4m3) or two sums, or adds to what the same lane stored before.
+// Stores one (e4m3) or two sums, or adds to what this CTA stored for an earlier
+// chunk of the expert: another group's warp may have, before the consumer_sync
+// that ends each batch.
 template <bool FP8>
 __device__ __forceinline__ void put(float* d, float v0, float v1, bool first) {
     if constexpr (FP8) {

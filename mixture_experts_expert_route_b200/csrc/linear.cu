@@ -23,17 +23,20 @@
 // No kernel needs a workspace, and no sum depends on timing.
 //
 // Measured on one B200 in a graph (us; floor at the measured copy and bf16 GEMM
-// rates; cuBLAS = the plain product alone, no epilogue):
-//   few   M=1  K=7168 N=2x2048 gated    12.7  (floor 9.0 by bytes, cuBLAS 20)
-//         M=16 K=14336 N=4096 residual  22.9  (18, 22)
-//   tile  M=77 K=N=2880                 9.0   (2.7, 7)   latency: ~6 us of first
+// rates; cuBLAS = the plain product alone, no epilogue, in the same run):
+//   few   M=1  K=7168 N=2x2048 gated    12.8  (floor 9.0 by bytes, cuBLAS 20.6)
+//         M=13 K=2048 N=7168 residual   9.9   (4.6, 8.0)  224 blocks on 148 SMs
+//         M=16 K=14336 N=4096 residual  23    (18, 24)
+//   tile  M=77 K=N=2880                 10.1  (2.7, 7.5)  latency: ~6 us of first
 //         copies, cluster sum and store around 11 k-blocks a block
-//         M=K=512 N=4096                6.7   (1.3, 4.4)
-//   split M=512 K=7168 N=2x2048 gated   27    (18, 25)   128-wide tiles 34: they read
+//         M=4096 K=2048 N=128           8.9   (3.0, 5.3)
+//         M=K=512 N=4096                7.5   (1.3, 5.0)
+//         M=2500 K=2048 N=2041          39    (12.5, 218) rows that are not aligned
+//   split M=512 K=7168 N=2x2048 gated   27-28 (18, 24)   128-wide tiles 34: they read
 //         1.5x the shared memory that their MMAs take
-//   pair  M=8192 K=7168 N=2x2048 gated  330-390 (288 at the burst rate; cuBLAS
-//         369-372 in the same runs): the power cap; M=1024 K=N=4096 29 (21, 25)
-//         M=2500 K=2048 N=2041          42    (12, 220)  rows that are not aligned
+//   pair  M=8192 K=7168 N=2x2048 gated  314-370 (288 at the burst rate; cuBLAS
+//         321-378 in the same runs): the power cap; M=1024 K=N=4096 28 (21, 25.6);
+//         M=1500 K=N=2048 16.5 (7.5, 11.5): 48 tiles on 74 pairs
 #include <cstdint>
 #include <cstring>
 #include <mutex>
