@@ -309,8 +309,10 @@ def combine(y_perm, inv_perm, T: int, k: int, H: int, out=None, stream=None):
 def _on_device(dev: torch.device, stream=None):
     """Makes the tensors' device the current one, and the given stream (if any) torch's
     current stream, so that buffers made inside belong to it."""
+    if dev.type != "cuda":
+        raise ValueError("expected a CUDA tensor")
     if dev.index is None:
-        dev = torch.device(dev.type, torch.cuda.current_device())
+        dev = torch.device("cuda", torch.cuda.current_device())
     if stream is not None:
         if stream.device != dev:
             raise ValueError("the stream belongs to another device than the tensors")

@@ -254,3 +254,13 @@ def test_decode_workspaces_are_shared_and_released(L, monkeypatch):
     assert key in L._DECODE_WS
     del b
     assert key not in L._DECODE_WS
+
+
+def test_a_block_refuses_host_tensors(monkeypatch):
+    """(and does not look for their device for ever)"""
+    from mixture_experts_expert_route_b200 import _lib
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    block = _lib.MoEBlock(None, None)
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        block(torch.zeros((4, 64), dtype=torch.bfloat16))
