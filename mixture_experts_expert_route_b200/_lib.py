@@ -594,8 +594,9 @@ def linear(x, w, bias=None, act: int = ACT_NONE, gated: bool = False, residual=N
 def linear_status(stream=None) -> int:
     """Synchronises the stream (None: the current one) and returns the code that linear calls
     without a status word recorded on the current device since this was last called: 0, or 5
-    where a wait ran out."""
-    return lib().moe_linear_status(_stream(stream))
+    where a wait ran out.  With a stream of another device, that device's."""
+    with torch.cuda.stream(stream):      # (None: nothing changes)
+        return lib().moe_linear_status(_stream(stream))
 
 
 def check_status(status: torch.Tensor, stream=None) -> int:
@@ -667,9 +668,10 @@ class MoELayer:
 
     def decode_workspace(self, T: int, stream=None) -> torch.Tensor:
         """The workspace of decode calls on a stream: one per device and stream, shared by all
-        layers (calls on one stream follow one another, on different streams they may
-        overlap) and released with the last of them.  A call captured into a graph gets one of its own, whose initialisation is
-        captured with it: the graph may be replayed on any stream, and outlive the cache."""
+        layers (calls on one stream follow one another, on different streams they may overlap)
+        and released with the last of them.  A call captured into a graph gets one of its own,
+        whose initialisation is captured with it: the graph may be replayed on any stream, and
+        outlive the cache."""
         if torch.cuda.is_current_stream_capturing():
             return decode_workspace(self.dtype, T, self.k, self.E, self.H, self.I,
                                     self.device, stream)

@@ -87,3 +87,23 @@ def test_a_decode_workspace_made_on_a_stream():
         got = moe.decode_forward(0, x, logits, layer.packed, None, 16, 384, 2, ws=ws, stream=side)
         side.synchronize()
         assert torch.equal(got, want)
+
+
+def test_few_tokens_beside_a_busy_stream():
+    """The few-token form, whose blocks wait on one another, on one stream while another is full
+    of products and layer calls that start early (and each other's): no wait runs out."""
+    moe = lib()
+    few, many = _block(moe, seed=1), _block(moe, seed=2)
+    xs, xl = [_x(T, T) for T in (1, 5, 16)], _x(900, 3)
+    want = [few(x, residual=x) for x in xs]
+    want_l = many(xl, residual=xl)
+    torch.cuda.synchronize()
+    s1, s2, s3 = (torch.cuda.Stream() for _ in range(3))
+    got, got_l = [], []
+    for rep in range(30):
+        got_l += [many(xl, residual=xl, stream=s2) for _ in range(3)]
+        got += [(n, few(x, residual=x, stream=s)) for n, x in enumerate(xs) for s in (s1, s3)]
+    torch.cuda.synchronize()
+    assert few.layer.check() == 0 and many.layer.check() == 0
+    assert all(torch.equal(y, want[n]) for n, y in got)
+    assert all(torch.equal(y, want_l) for y in got_l)

@@ -264,3 +264,24 @@ def test_a_block_refuses_host_tensors(monkeypatch):
     block = _lib.MoEBlock(None, None)
     with pytest.raises(ValueError, match="CUDA tensor"):
         block(torch.zeros((4, 64), dtype=torch.bfloat16))
+
+
+def test_linear_status_reads_the_word_of_the_streams_device(L, monkeypatch):
+    from types import SimpleNamespace
+    seen = []
+
+    @contextlib.contextmanager
+    def stream_context(s):
+        before = L.test_current[0]
+        if s is not None:
+            L.test_current[0] = s.device.index
+        yield
+        L.test_current[0] = before
+
+    monkeypatch.setattr(torch.cuda, "stream", stream_context)
+    monkeypatch.setattr(L, "_stream", lambda s: 0 if s is None else s.cuda_stream)
+    monkeypatch.setattr(L, "lib", lambda: SimpleNamespace(
+        moe_linear_status=lambda s: seen.append((s, L.test_current[0])) or 0))
+    assert L.linear_status() == 0
+    assert L.linear_status(SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=7)) == 0
+    assert seen == [(0, 0), (7, 1)]
