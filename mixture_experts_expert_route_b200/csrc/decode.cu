@@ -251,6 +251,9 @@ __device__ __forceinline__ float f16_scale(uint32_t bits) {
 __device__ __forceinline__ float scale_inv(float s) {
     return __uint_as_float((254u << 23) - __float_as_uint(s));
 }
+// The down sums of e4m3 layers lack the matrix' scale (its largest weight / 448)
+// until the end: this power of two in its place keeps them finite where out is.
+constexpr float kSumScale = 1.0f / 16384.0f;
 __device__ __forceinline__ uint32_t finite_mag(float v) {
     const uint32_t m = __float_as_uint(v) & 0x7fffffffu;
     return m < 0x7f800000u ? m : 0u;
@@ -771,7 +774,8 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
                                       __popc(s.mask[e] & ((1u << tk) - 1u)),
                                   s.base[i + 1] - c0);
             s.term_tile[f] = i * S2;
-            s.term_w[f] = FP8 ? s.w[f] * __ldg(g.scales + e * 3 + 2) : s.w[f];
+            s.term_w[f] =
+                FP8 ? s.w[f] * __ldg(g.scales + e * 3 + 2) * (1.0f / kSumScale) : s.w[f];
             if (cta == 0) {
                 if (g.ids) g.ids[f] = e;
                 if (g.w) g.w[f] = s.w[f];
@@ -948,7 +952,8 @@ __device__ __forceinline__ void run_steps(const Args& g, Shared& s, const Run& r
                 if constexpr (FP8) {
 #pragma unroll
                     for (int q = 0; q < (MANY ? 4 : 2); ++q)
-                        inv[q] = scale_inv(f16_scale(s.hmax[n][8 * (q >> 1) + 2 * t + (q & 1)]));
+                        inv[q] = kSumScale *
+                                 scale_inv(f16_scale(s.hmax[n][8 * (q >> 1) + 2 * t + (q & 1)]));
                 }
                 // this group's first visit's k-block (counted from the chunk's
                 // first) and row tile
